@@ -21,6 +21,8 @@ LIB_PATH = os.path.join(_HERE, "libgdn61.so")
 
 GDN_DTYPE_F32 = 0
 GDN_DTYPE_BF16 = 1
+GDN_Q8_INT8 = 0
+GDN_Q8_E4M3 = 1
 
 _c_void_p = ctypes.c_void_p
 _c_int = ctypes.c_int
@@ -68,6 +70,19 @@ _SIGNATURES = {
                                  _c_void_p, _c_void_p, _c_void_p, _c_void_p, _c_size_t, _c_void_p]),
     "gdn_state_to_pool": (_c_int, [_c_void_p, _c_void_p, _c_void_p,
                                    _c_int, _c_int, _c_int, _c_int, _c_int, _c_void_p]),
+    "gdn_conv_fwd": (_c_int, [_c_void_p, _c_ll, _c_ll, _c_void_p, _c_void_p, _c_int] + [_c_void_p] * 3 + [_c_int] * 5
+                     + [_c_float] + [_c_void_p] * 3 + [_c_int, _c_void_p] + [_c_int] * 6 + [_c_void_p]),
+    "gdn_conv_step": (_c_int, [_c_void_p, _c_ll, _c_ll, _c_void_p, _c_void_p, _c_int] + [_c_void_p] * 3
+                      + [_c_int] * 3 + [_c_void_p] * 2 + [_c_int] * 6 + [_c_void_p]),
+    "ssm_chunk_fwd_workspace_bytes": (_c_size_t, [_c_int] * 9),
+    "ssm_chunk_fwd": (_c_int, [_c_void_p, _c_ll, _c_ll] * 5 + [_c_void_p] * 3 + [_c_int] + [_c_void_p] * 3
+                      + [_c_int] * 9 + [_c_void_p, _c_void_p, _c_size_t, _c_void_p]),
+    "ssm_step": (_c_int, [_c_void_p, _c_ll, _c_ll] * 5 + [_c_void_p] * 3 + [_c_int, _c_void_p, _c_int, _c_void_p]
+                 + [_c_int] * 8 + [_c_void_p, _c_void_p]),
+    "gdn_state_store_q8": (_c_int, [_c_void_p, _c_int, _c_int, _c_void_p, _c_void_p, _c_int, _c_void_p, _c_int,
+                                    _c_void_p] + [_c_int] * 4 + [_c_void_p]),
+    "gdn_state_load_q8": (_c_int, [_c_void_p, _c_int, _c_void_p, _c_int, _c_void_p, _c_void_p, _c_int, _c_int,
+                                   _c_void_p] + [_c_int] * 4 + [_c_void_p]),
 }
 
 _lib = None
@@ -131,7 +146,8 @@ def _need(t: Optional[torch.Tensor], name: str, dtype: Optional[torch.dtype], sh
         raise ValueError(f"{name} must be contiguous")
 
 
-STAGES = ("varlen_tables", "intra", "scan", "decode", "handoff", "bwd_dh", "fwd_h")
+STAGES = ("varlen_tables", "intra", "scan", "decode", "handoff", "bwd_dh", "fwd_h", "conv", "ssm_scan", "ssm_step",
+          "state_q8")
 
 
 def profile_enable(on: bool = True) -> None:
@@ -510,3 +526,251 @@ def chunk_fwd_h(k: torch.Tensor, v: torch.Tensor, g: Optional[torch.Tensor] = No
                                  _dtype_code(sdt), int(bool(state_v_first)), _ptr(ht), _ptr(cu_seqlens), N,
                                  B, T, Hk, HV, K, V, chunk_size, _io_code(torch.bfloat16), _stream(dev)))
     return h, ht
+
+
+# ------------------------------------------------ operators around the scans
+def _call(dev: torch.device, fn, *args) -> None:
+    """One library call on the tensors' device and its current stream."""
+    if torch.cuda.current_device() != dev.index:
+        with torch.cuda.device(dev):
+            _check(fn(*args, torch.cuda.current_stream(dev).cuda_stream))
+        return
+    status = fn(*args, torch._C._cuda_getCurrentRawStream(dev.index))
+    if status:
+        _check(status)
+
+
+def _rows(t: torch.Tensor, name: str, dtype: torch.dtype, shape: tuple, dev: torch.device):
+    """(pointer, batch stride, token stride) of an operand [B, T, ...] whose
+    rows may lie apart (a slice of a wider tensor); what follows B and T must be
+    packed."""
+    if t.device != dev:
+        raise ValueError(f"{name} must be on {dev}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    st = t.stride()
+    if (shape[-1] > 1 and st[-1] != 1) or (len(shape) == 4 and shape[2] > 1 and st[2] != shape[3]):
+        raise ValueError(f"{name} must be contiguous behind its batch and token dimensions")
+    return t.data_ptr(), st[0], st[1]
+
+
+def _index(t: Optional[torch.Tensor], name: str, n: int, dev: torch.device) -> Optional[torch.Tensor]:
+    if t is None:
+        return None
+    if t.dtype != torch.int32:
+        t = t.to(torch.int32)
+    _need(t, name, torch.int32, (n,), dev)
+    return t
+
+
+def _cuda(t: torch.Tensor, name: str) -> torch.device:
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be on a GPU")
+    return t.device
+
+
+def _conv_args(x, weight, bias, activation, sections, state, out):
+    if x.dim() != 3 or weight.dim() != 2:
+        raise ValueError("x must be [B, T, D] and weight [D, W]")
+    if activation not in (None, "silu"):
+        raise ValueError(f"activation must be None or 'silu', got {activation!r}")
+    B, T, D = x.shape
+    W = weight.shape[1]
+    dev, io = _cuda(x, "x"), x.dtype
+    code = _io_code(io)
+    _need(weight, "weight", io, (D, W), dev)
+    _need(bias, "bias", io, (D,), dev)
+    if state is not None:
+        if state.dim() != 3:
+            raise ValueError("state must be [pool, W - 1, D]")
+        _need(state, "state", io, (state.shape[0], W - 1, D), dev)
+    widths = (D,) if sections is None else tuple(int(n) for n in sections)
+    if not 1 <= len(widths) <= 3 or min(widths) <= 0 or sum(widths) != D:
+        raise ValueError(f"sections must be one to three positive widths that add up to {D}, got {widths}")
+    if out is None:
+        outs = tuple(torch.empty((B, T, n), dtype=io, device=dev) for n in widths)
+    else:
+        outs = (out,) if isinstance(out, torch.Tensor) else tuple(out)
+        if len(outs) != len(widths):
+            raise ValueError(f"out must hold {len(widths)} tensors, got {len(outs)}")
+        for i, (o, n) in enumerate(zip(outs, widths)):
+            _need(o, f"out[{i}]", io, (B, T, n), dev)
+    ptrs = [o.data_ptr() for o in outs] + [None] * (3 - len(outs))
+    return B, T, D, W, dev, code, outs, ptrs, widths + (0,) * (3 - len(widths)), _rows(x, "x", io, x.shape, dev)
+
+
+def causal_conv_fwd(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tensor] = None, *,
+                    activation: Optional[str] = "silu", sections=None, norm_dim: int = 0, norm_sections: int = 0,
+                    norm_eps: float = 1e-6, state: Optional[torch.Tensor] = None,
+                    state_indices: Optional[torch.Tensor] = None, has_state: Optional[torch.Tensor] = None,
+                    cu_seqlens: Optional[torch.Tensor] = None, out=None):
+    """Short causal depthwise convolution of prompts.  ``x`` [B,T,D] (bf16 or
+    fp32, possibly a slice of a projection's output), ``weight`` [D,W] (oldest
+    tap first, W = 2..4), ``bias`` [D].  Returns the result [B,T,D], or with
+    ``sections`` (up to three widths that add up to D) a tuple of one packed
+    tensor each, e.g. the q, k and v of a delta-rule layer.  ``activation``:
+    "silu" or None.  With ``norm_sections`` > 0 every head of ``norm_dim``
+    channels of the leading sections is divided by its L2 norm
+    (sqrt(sum + norm_eps)).
+
+    ``state`` [pool,W-1,D] is updated in place: the slot ``state_indices[n]``
+    (None = n) of each sequence gets the last W - 1 rows, and the sequence
+    continues from it where ``has_state[n]`` is not 0 (None: all sequences are
+    new).  ``cu_seqlens`` [N+1] int64 packs N sequences into B = 1; rows behind
+    the last boundary are left as they are."""
+    B, T, D, W, dev, code, outs, ptrs, widths, rows = _conv_args(x, weight, bias, activation, sections, state, out)
+    N = B
+    if cu_seqlens is not None:
+        _need(cu_seqlens, "cu_seqlens", torch.int64, None, dev)
+        N = cu_seqlens.numel() - 1
+    if state is None and (state_indices is not None or has_state is not None):
+        raise ValueError("state_indices and has_state need a state")
+    state_indices = _index(state_indices, "state_indices", N, dev)
+    has_state = _index(has_state, "has_state", N, dev)
+    _call(dev, lib().gdn_conv_fwd, *rows, weight.data_ptr(), _ptr(bias), 1 if activation else 0, *ptrs, *widths,
+          norm_dim, norm_sections, norm_eps, _ptr(state), _ptr(state_indices), _ptr(has_state),
+          0 if state is None else state.shape[0], _ptr(cu_seqlens), N, B, T, D, W, code)
+    return outs[0] if sections is None else outs
+
+
+def causal_conv_step(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tensor], state: torch.Tensor,
+                     state_indices: Optional[torch.Tensor] = None, *, activation: Optional[str] = "silu",
+                     sections=None, out=None):
+    """The convolution of ``causal_conv_fwd`` for T = 1..4 new tokens a row over
+    its pool of states: ``x`` [B,T,D], ``state`` [pool,W-1,D] updated in place
+    at the slots ``state_indices`` [B] (None = row b).  A slot outside the pool
+    gives zeros and leaves the pool alone.  Returns as ``causal_conv_fwd``."""
+    B, T, D, W, dev, code, outs, ptrs, widths, rows = _conv_args(x, weight, bias, activation, sections, state, out)
+    state_indices = _index(state_indices, "state_indices", B, dev)
+    _call(dev, lib().gdn_conv_step, *rows, weight.data_ptr(), _ptr(bias), 1 if activation else 0, *ptrs, *widths,
+          _ptr(state), _ptr(state_indices), state.shape[0], B, T, D, W, code)
+    return outs[0] if sections is None else outs
+
+
+def _ssm_args(x, dt, Bm, Cm, A_log, D, z, dt_bias, out):
+    if x.dim() != 4 or Bm.dim() != 4:
+        raise ValueError("x must be [B, T, HV, V] and Bm, Cm [B, T, Hk, K]")
+    B, T, HV, V = x.shape
+    Hk, K = Bm.shape[2:]
+    dev, io = _cuda(x, "x"), x.dtype
+    code = _io_code(io)
+    groups = (B, T, Hk, K)
+    rows = (*_rows(x, "x", io, x.shape, dev), *_rows(dt, "dt", io, (B, T, HV), dev),
+            *_rows(Bm, "Bm", io, groups, dev), *_rows(Cm, "Cm", io, groups, dev),
+            *((None, 0, 0) if z is None else _rows(z, "z", io, x.shape, dev)))
+    _need(A_log, "A_log", torch.float32, (HV,), dev)
+    _need(dt_bias, "dt_bias", torch.float32, (HV,), dev)
+    _need(D, "D", torch.float32, (HV,), dev)
+    if out is None:
+        out = torch.empty((B, T, HV, V), dtype=io, device=dev)
+    else:
+        _need(out, "out", io, (B, T, HV, V), dev)
+    return B, T, Hk, HV, K, V, dev, code, rows, (A_log.data_ptr(), _ptr(dt_bias), _ptr(D)), out
+
+
+def ssm_workspace_bytes(B: int, T: int, Hk: int, HV: int, K: int, V: int, num_seqs: int, dtype: torch.dtype,
+                        varlen: bool = False) -> int:
+    """Workspace of ``ssm_chunk_fwd``, in bytes (0: none)."""
+    return int(lib().ssm_chunk_fwd_workspace_bytes(B, T, Hk, HV, K, V, num_seqs, int(varlen), _io_code(dtype)))
+
+
+def ssm_chunk_fwd(x: torch.Tensor, dt: torch.Tensor, Bm: torch.Tensor, Cm: torch.Tensor, A_log: torch.Tensor, *,
+                  D: Optional[torch.Tensor] = None, z: Optional[torch.Tensor] = None,
+                  dt_bias: Optional[torch.Tensor] = None, dt_softplus: bool = True,
+                  h0: Optional[torch.Tensor] = None, output_final_state: bool = True,
+                  cu_seqlens: Optional[torch.Tensor] = None, chunk_size: int = 64,
+                  out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None):
+    """Selective state-space scan of prompts: with D_t = softplus(dt_t +
+    dt_bias), S_t = exp(-exp(A_log) D_t) S_{t-1} + D_t x_t Bm_t^T and
+    y_t = (S_t Cm_t + D x_t) silu(z_t).  ``x``, ``z`` [B,T,HV,V], ``dt``
+    [B,T,HV], ``Bm``, ``Cm`` [B,T,Hk,K] (bf16 or fp32; possibly slices of wider
+    tensors), ``A_log``, ``dt_bias``, ``D`` [HV] fp32.  Returns (y [B,T,HV,V],
+    ht [N,HV,V,K] fp32 or None).  ``cu_seqlens`` [N+1] int64 packs N sequences
+    into B = 1; rows behind the last boundary are left as they are.  ``h0``
+    [N,HV,V,K] fp32 is the initial state.  Without softplus dt_t + dt_bias must
+    not be negative."""
+    B, T, Hk, HV, K, V, dev, code, rows, params, y = _ssm_args(x, dt, Bm, Cm, A_log, D, z, dt_bias, out)
+    N = B
+    if cu_seqlens is not None:
+        _need(cu_seqlens, "cu_seqlens", torch.int64, None, dev)
+        N = cu_seqlens.numel() - 1
+    _need(h0, "h0", torch.float32, (N, HV, V, K), dev)
+    ht = torch.empty((N, HV, V, K), dtype=torch.float32, device=dev) if output_final_state else None
+    L = lib()
+    nbytes = int(L.ssm_chunk_fwd_workspace_bytes(B, T, Hk, HV, K, V, N, 0 if cu_seqlens is None else 1, code))
+    if nbytes:
+        if workspace is None or workspace.numel() * workspace.element_size() < nbytes:
+            workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+        else:
+            _need(workspace, "workspace", None, None, dev)
+    _call(dev, L.ssm_chunk_fwd, *rows, *params, 1 if dt_softplus else 0, _ptr(h0), _ptr(ht), _ptr(cu_seqlens), N,
+          B, T, Hk, HV, K, V, chunk_size, code, y.data_ptr(), workspace.data_ptr() if nbytes else None, nbytes)
+    return y, ht
+
+
+def ssm_step(x: torch.Tensor, dt: torch.Tensor, Bm: torch.Tensor, Cm: torch.Tensor, A_log: torch.Tensor,
+             state: torch.Tensor, *, state_indices: Optional[torch.Tensor] = None, D: Optional[torch.Tensor] = None,
+             z: Optional[torch.Tensor] = None, dt_bias: Optional[torch.Tensor] = None, dt_softplus: bool = True,
+             out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """The recurrence of ``ssm_chunk_fwd`` for T = 1..4 new tokens a row over a
+    pool of states: ``state`` [pool,HV,V,K] (fp32 or bf16) is updated in place
+    at the slots ``state_indices`` [B] (None = row b).  A slot outside the pool
+    gives y = 0 and leaves the pool alone.  Returns y [B,T,HV,V]."""
+    B, T, Hk, HV, K, V, dev, code, rows, params, y = _ssm_args(x, dt, Bm, Cm, A_log, D, z, dt_bias, out)
+    if state.dim() != 4 or state.dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError("state must be [pool, HV, V, K] fp32 or bf16")
+    _need(state, "state", None, (state.shape[0], HV, V, K), dev)
+    state_indices = _index(state_indices, "state_indices", B, dev)
+    _call(dev, lib().ssm_step, *rows, *params, 1 if dt_softplus else 0, state.data_ptr(), _dtype_code(state.dtype),
+          _ptr(state_indices), state.shape[0], B, T, Hk, HV, K, V, code, y.data_ptr())
+    return y
+
+
+def _q8_args(wide, wide_name, q8, scales, src_indices, dst_indices):
+    if wide.dim() != 4 or wide.dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError(f"{wide_name} must be [entries, HV, V, K] fp32 or bf16")
+    entries, HV, V, K = wide.shape
+    dev = _cuda(wide, wide_name)
+    _need(wide, wide_name, None, None, dev)
+    if q8.dim() != 4 or q8.dtype not in (torch.int8, torch.float8_e4m3fn):
+        raise ValueError("q8 must be [pool, HV, V, K] int8 or float8_e4m3fn")
+    pool = q8.shape[0]
+    _need(q8, "q8", None, (pool, HV, V, K), dev)
+    _need(scales, "scales", torch.float32, (pool, HV, V), dev)
+    return entries, HV, V, K, dev, pool, GDN_Q8_INT8 if q8.dtype == torch.int8 else GDN_Q8_E4M3
+
+
+def state_store_q8(src: torch.Tensor, q8: torch.Tensor, scales: torch.Tensor,
+                   src_indices: Optional[torch.Tensor] = None, dst_indices: Optional[torch.Tensor] = None) -> None:
+    """Quantise recurrent states ``src`` [entries,HV,V,K] (fp32 or bf16: final
+    states, snapshots, a decode pool) into slots of an 8-bit cache: ``q8``
+    [pool,HV,V,K] (int8 or float8_e4m3fn) and one scale per state row, ``scales``
+    [pool,HV,V] fp32, both in place.  State ``src_indices[i]`` goes to slot
+    ``dst_indices[i]`` (None = i); without either every entry of ``src`` is
+    stored."""
+    entries, HV, V, K, dev, pool, form = _q8_args(src, "src", q8, scales, src_indices, dst_indices)
+    n = entries
+    if src_indices is not None or dst_indices is not None:
+        n = (src_indices if src_indices is not None else dst_indices).numel()
+    src_indices, dst_indices = _index(src_indices, "src_indices", n, dev), _index(dst_indices, "dst_indices", n, dev)
+    _call(dev, lib().gdn_state_store_q8, src.data_ptr(), _dtype_code(src.dtype), entries, _ptr(src_indices),
+          q8.data_ptr(), form, scales.data_ptr(), pool, _ptr(dst_indices), n, HV, K, V)
+
+
+def state_load_q8(q8: torch.Tensor, scales: torch.Tensor, dst: torch.Tensor,
+                  src_indices: Optional[torch.Tensor] = None,
+                  dst_indices: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Read slots of the 8-bit state cache (see ``state_store_q8``) back into
+    ``dst`` [entries,HV,V,K] (fp32: an initial state; bf16: a decode pool), in
+    place: slot ``src_indices[i]`` into entry ``dst_indices[i]`` (None = i);
+    without either every entry of ``dst`` is read.  Returns ``dst``."""
+    entries, HV, V, K, dev, pool, form = _q8_args(dst, "dst", q8, scales, src_indices, dst_indices)
+    n = entries
+    if src_indices is not None or dst_indices is not None:
+        n = (src_indices if src_indices is not None else dst_indices).numel()
+    src_indices, dst_indices = _index(src_indices, "src_indices", n, dev), _index(dst_indices, "dst_indices", n, dev)
+    _call(dev, lib().gdn_state_load_q8, q8.data_ptr(), form, scales.data_ptr(), pool, _ptr(src_indices),
+          dst.data_ptr(), _dtype_code(dst.dtype), entries, _ptr(dst_indices), n, HV, K, V)
+    return dst

@@ -6,12 +6,12 @@
 #include <string.h>
 
 #include <mutex>
-#include <string>
 #include <vector>
 
 #include "gdn61.h"
 #include "gdn_device.h"
 #include "gdn_launch.h"
+#include "mixer_launch.h"
 
 namespace gdn {
 
@@ -23,24 +23,24 @@ hipError_t launch_scan_kda(const ChunkArgs& a, const void* qg, const void* kg, c
                            const float* dg, hipStream_t s);
 
 namespace {
+// a plain buffer: recording a failure allocates nothing and cannot throw
+thread_local char g_last_error[512] = "";
+}  // namespace
 
-thread_local std::string g_last_error;
-
-int fail(int status, const char* fmt, ...) __attribute__((format(printf, 2, 3)));
 int fail(int status, const char* fmt, ...) {
-  char buf[512];
   va_list ap;
   va_start(ap, fmt);
-  vsnprintf(buf, sizeof buf, fmt, ap);
+  vsnprintf(g_last_error, sizeof g_last_error, fmt, ap);
   va_end(ap);
-  g_last_error = buf;
   return status;
 }
 
 int ok() {
-  g_last_error.clear();
+  g_last_error[0] = 0;
   return GDN_OK;
 }
+
+namespace {
 
 bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
 
@@ -298,7 +298,7 @@ const char* gdn_status_string(int status) {
   }
 }
 
-const char* gdn_last_error(void) { return g_last_error.c_str(); }
+const char* gdn_last_error(void) { return g_last_error; }
 
 const char* gdn_version(void) { return "gdn61 0.1 gfx950"; }
 

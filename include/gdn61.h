@@ -418,6 +418,164 @@ int gdn_state_to_pool(const float* ht, const int32_t* indices, void* pool_state,
                       int N, int HV, int K, int V, int pool, void* stream);
 
 /*
+ * Short causal depthwise convolution of a prompt, with its epilogue, in front
+ * of a recurrent mixer.
+ *
+ *   c_t = bias + sum_{j<W} w_j u_{t-W+1+j}
+ *
+ * per channel, u being the sequence's rows behind the W - 1 rows of its state
+ * slot (zeros without one); then c <- c / (1 + e^-c) with silu != 0; then, in
+ * the first norm_sections sections, every head of norm_dim channels is divided
+ * by sqrt(sum of its squares + norm_eps) (the q and k of a delta-rule layer,
+ * whose prefill takes them normalised).  fp32 sums, one rounding.
+ *
+ *   x            [B, T, D]      io dtype; row t of batch b starts x_batch * b +
+ *                               x_token * t elements behind x (a slice of a
+ *                               projection's output); D channels contiguous
+ *   weight       [D, W]         io dtype, oldest tap first
+ *   bias         [D]            io dtype, or NULL
+ *   out0..2      [B, T, width]  io dtype out, packed: the channels in up to
+ *                               three sections of width0, width1, width2
+ *                               channels (0 = section not used), which add up
+ *                               to D
+ *   state        [pool, W - 1, D] io dtype, oldest row first, or NULL: the slot
+ *                               of sequence n is read where has_state[n] != 0
+ *                               and then gets the last W - 1 rows of u, IN PLACE
+ *   state_indices [N] int32 device array, or NULL for slot n (then pool >= N).
+ *                               A slot outside [0, pool): that sequence starts
+ *                               from zeros and the pool is left alone.  Two
+ *                               sequences naming the same slot race (undefined
+ *                               result).
+ *   has_state    [N] int32 device array, or NULL: every sequence is new (starts
+ *                               from zeros; its slot is still written)
+ *   cu_seqlens, num_seqs        as in gdn_chunk_fwd, but the last boundary may
+ *                               be below T: rows behind it are left as they are
+ *
+ * Supported: bf16 or fp32 io, W in 2..4, D and every section's width multiples
+ * of 8, x_token and x_batch multiples of 8, 16-byte aligned tensors; with
+ * norm_sections > 0 norm_dim 64 or 128, dividing the width of each normalised
+ * section.  Allocates nothing; asynchronous on `stream`.
+ */
+int gdn_conv_fwd(const void* x, long long x_batch, long long x_token, const void* weight, const void* bias,
+                 int silu, void* out0, void* out1, void* out2, int width0, int width1, int width2,
+                 int norm_dim, int norm_sections, float norm_eps,
+                 void* state, const int32_t* state_indices, const int32_t* has_state, int pool,
+                 const int64_t* cu_seqlens, int num_seqs, int B, int T, int D, int W, int dtype, void* stream);
+
+/*
+ * The same convolution for single tokens, T = 1..4 a call, over the pool of
+ * states that gdn_conv_fwd writes: slot state_indices[b] (or b) of batch row b
+ * is read and gets the last W - 1 rows, IN PLACE.  A slot outside [0, pool)
+ * leaves the pool untouched and writes zeros for that row.  No norm: the decode
+ * step normalises q and k itself.  Other arguments and limits as above.
+ */
+int gdn_conv_step(const void* x, long long x_batch, long long x_token, const void* weight, const void* bias,
+                  int silu, void* out0, void* out1, void* out2, int width0, int width1, int width2,
+                  void* state, const int32_t* state_indices, int pool,
+                  int B, int T, int D, int W, int dtype, void* stream);
+
+/*
+ * Selective state-space scan of prompts: per sequence and head,
+ *
+ *   D_t = softplus(dt_t + dt_bias)    (dt_softplus = 0: dt_t + dt_bias, which
+ *                                      must not be negative)
+ *   S_t = exp(-exp(A_log) D_t) S_{t-1} + D_t x_t B_t^T
+ *   y_t = (S_t C_t + D x_t) silu(z_t)
+ *
+ * with S [V, K] (softplus(a) = log(1 + e^a) for a <= 20, a beyond, as in
+ * gdn_decode).
+ *
+ *   x            [B, T, HV, V]  io dtype
+ *   dt           [B, T, HV]     io dtype
+ *   Bm, Cm       [B, T, Hk, K]  io dtype (group of head j: j / (HV / Hk))
+ *   z            [B, T, HV, V]  io dtype, or NULL (no gate)
+ *                each of these five with the strides of its batch rows and
+ *                tokens in elements (*_batch, *_token), so that slices of a
+ *                projection are taken as they are; heads and channels contiguous
+ *   A_log        [HV]           fp32
+ *   dt_bias, D   [HV]           fp32, or NULL (0)
+ *   h0           [N, HV, V, K]  fp32 initial state, or NULL for zeros
+ *   ht           [N, HV, V, K]  fp32 final state out, or NULL to skip
+ *   y            [B, T, HV, V]  io dtype out, packed
+ *   cu_seqlens, num_seqs        as in gdn_chunk_fwd, but the last boundary may
+ *                               be below T: rows behind it are left as they are
+ *   workspace    device buffer of at least ssm_chunk_fwd_workspace_bytes()
+ *                bytes, 256-byte aligned (0 bytes: NULL allowed)
+ *
+ * Supported: bf16 or fp32 io, K and V in {64, 128}, HV a multiple of Hk,
+ * chunk_size = 64; x, Bm, Cm, z and their strides in multiples of 16 bytes.
+ * Sums, gates and states are fp32 or wider; with bf16 io the products that make
+ * y take the state and the decayed scores rounded to bf16, those that make ht
+ * lose nothing to fp32.  Tokens are taken in chunks of 64 as matrix products, in
+ * which every token of a chunk is multiplied by the weights (zero or not) of the
+ * others: an infinity or NaN in x, dt, Bm or Cm makes values of that whole chunk
+ * (of the heads that read it) and behind it NaN.  Allocates nothing;
+ * asynchronous on `stream`.
+ */
+size_t ssm_chunk_fwd_workspace_bytes(int B, int T, int Hk, int HV, int K, int V, int num_seqs, int varlen,
+                                     int dtype);
+int ssm_chunk_fwd(const void* x, long long x_batch, long long x_token,
+                  const void* dt, long long dt_batch, long long dt_token,
+                  const void* Bm, long long B_batch, long long B_token,
+                  const void* Cm, long long C_batch, long long C_token,
+                  const void* z, long long z_batch, long long z_token,
+                  const float* A_log, const float* dt_bias, const float* D, int dt_softplus,
+                  const float* h0, float* ht, const int64_t* cu_seqlens, int num_seqs,
+                  int B, int T, int Hk, int HV, int K, int V, int chunk_size, int dtype,
+                  void* y, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * The same recurrence for single tokens, T = 1..4 a call, over a pool of
+ * states.  Arguments as above, and
+ *
+ *   state        [pool, HV, V, K] fp32 or bf16 (state_dtype), read and written
+ *                IN PLACE: slot state_indices[b] (or b when NULL, then pool >= B)
+ *                of batch row b.  Carried in fp32 across the T tokens; a bf16
+ *                pool gets it rounded to nearest, ties to even, once.  A slot
+ *                outside [0, pool) leaves the pool untouched and writes y = 0 for
+ *                that row.  Two rows naming the same slot race (undefined result).
+ */
+int ssm_step(const void* x, long long x_batch, long long x_token,
+             const void* dt, long long dt_batch, long long dt_token,
+             const void* Bm, long long B_batch, long long B_token,
+             const void* Cm, long long C_batch, long long C_token,
+             const void* z, long long z_batch, long long z_token,
+             const float* A_log, const float* dt_bias, const float* D, int dt_softplus,
+             void* state, int state_dtype, const int32_t* state_indices, int pool,
+             int B, int T, int Hk, int HV, int K, int V, int dtype, void* y, void* stream);
+
+/*
+ * 8-bit cache of recurrent states (of any operator of this library), one scale
+ * per state row.  gdn_state_store_q8 quantises state src_indices[i] of `src`
+ * into cache slot dst_indices[i], i = 0 .. N - 1; gdn_state_load_q8 reads cache
+ * slot src_indices[i] back into state dst_indices[i] of `dst` (NULL indices: i).
+ *
+ *   src / dst    [entries, HV, V, K] fp32 or bf16 (state_dtype): ht, h0, state
+ *                snapshots, a decode pool
+ *   q8           [pool, HV, V, K]   one byte a value: int8 (GDN_Q8_INT8) or
+ *                e4m3 (GDN_Q8_E4M3; finite values up to 448)
+ *   scales       [pool, HV, V]      fp32
+ *
+ * int8: scale = max(max|row| * r, 2^-126) in fp32, r = 1/127 rounded to fp32;
+ * code = row / scale rounded to nearest, ties to even.  e4m3: scale = the smallest power of two of
+ * at least 2^-126 with max|row| / scale <= 448; code = row / scale rounded to
+ * nearest, ties to even.  Reading: code * scale, rounded to the state's type.
+ * A row with an infinity or a NaN gets the scale NaN and codes 0 and reads back
+ * as NaN.  An index outside its array skips that state (nothing is written).
+ * Two states naming the same target race (undefined result).
+ *
+ * Supported: K in {64, 128}; 16-byte aligned tensors.  Allocates nothing;
+ * asynchronous on `stream`.
+ */
+enum { GDN_Q8_INT8 = 0, GDN_Q8_E4M3 = 1 };
+int gdn_state_store_q8(const void* src, int state_dtype, int entries, const int32_t* src_indices,
+                       void* q8, int q8_format, float* scales, int pool, const int32_t* dst_indices,
+                       int N, int HV, int K, int V, void* stream);
+int gdn_state_load_q8(const void* q8, int q8_format, const float* scales, int pool, const int32_t* src_indices,
+                      void* dst, int state_dtype, int entries, const int32_t* dst_indices,
+                      int N, int HV, int K, int V, void* stream);
+
+/*
  * Per-stage timing for measurement tools.  While enabled, every call of the
  * entry points above records a pair of HIP events on the caller's stream
  * around each kernel it launches (stage ids below); this adds two event
@@ -436,7 +594,11 @@ enum {
   GDN_STAGE_HANDOFF = 4,       /* prefill state -> decode pool (bf16)          */
   GDN_STAGE_BWD_DH = 5,        /* backward state-gradient scan                 */
   GDN_STAGE_FWD_H = 6,         /* forward decay-only state scan                */
-  GDN_STAGE_COUNT = 7
+  GDN_STAGE_CONV = 7,          /* causal convolution, prompts and single tokens */
+  GDN_STAGE_SSM_SCAN = 8,      /* selective state-space scan (both launches)   */
+  GDN_STAGE_SSM_STEP = 9,      /* selective state-space step                   */
+  GDN_STAGE_STATE_Q8 = 10,     /* 8-bit state cache, store and load            */
+  GDN_STAGE_COUNT = 11
 };
 int gdn_profile_enable(int on);
 int gdn_profile_read(double* ms, int* counts);
