@@ -119,6 +119,11 @@ int check_ssm_rows(const SsmArgs& a) {
   if (a.z.p)
     if (int st = check_rows("z", a.z, a.nb, a.T, unit)) return st;
   if (!aligned16(a.y)) return fail(GDN_ERR_INVALID_ARGUMENT, "y must be 16-byte aligned");
+  // rows of a chunk are addressed with 32-bit byte offsets
+  for (const Rows* r : {&a.x, &a.dt, &a.B, &a.C, &a.z})
+    if (a.T > 1 && r->p && r->token >= (1 << 23))
+      return fail(GDN_ERR_UNSUPPORTED, "token strides must stay below 2^23 elements");
+  if ((long long)a.HV * a.V >= (1 << 23)) return fail(GDN_ERR_UNSUPPORTED, "HV * V must stay below 2^23");
   return GDN_OK;
 }
 

@@ -14,23 +14,28 @@
 // shared by the two heads of a work-group), on the bf16 matrix cores for bf16 io
 // and the fp32 ones for fp32 io.
 //
-// Work is cut into (sequence segment, 64 or 128 value columns).  A work-group of
-// four waves walks the chunks of its segment with the state in accumulators:
-// wave w owns 16 or 32 columns and all K channels, so S^T feeds both products
-// from registers, and only the 64 x 64 matrix M passes through LDS.  The next
-// chunk's tiles are loaded into registers while this one computes.  Where
+// Work is cut into (sequence segment, 64 or 128 value columns).  A work-group walks
+// the chunks of its segment with the state in accumulators: each of its 4 or 8
+// waves owns 16 columns and all K channels, so S^T feeds both products from
+// registers.  The scores C B^T, six 16 x 32 pieces on and under the diagonal, are
+// dealt out to the waves (with tokens as columns they leave the matrix core as the
+// operand of the next product), gated for each head and passed through LDS; the
+// waves without a piece compute the next chunk's gates meanwhile.  Tiles arrive by
+// direct-to-LDS loads into one buffer: 69 KiB a work-group at K = 128, two
+// work-groups a CU (four waves a SIMD), which hide each other's latencies.  Where
 // sequences x heads are too few for the chip, sequences are split: a first
 // launch computes each segment's own final state (from zeros) and log-decay,
 // and the segment's work-group of the second launch starts from the decayed sum
 // of those before it (and h0).  That reads x and B twice but moves no
 // per-chunk states.
 //
-// Precision.  Gate sums are taken in 64 bits and used as an fp32 pair, so that a
-// difference G_t - G_s keeps its last places however strong the decay before it.
-// A state that leaves the kernel (ht, and a segment's state handed on) is formed
-// from the exact products of B with the scaled x as three bf16 terms (24 bits);
-// the state that only feeds this segment's bf16 y takes one term, and S and M
-// are rounded to bf16 as operands.
+// Precision.  Gate sums are taken in 64 bits, over log2-decays held at -160 a
+// token or more (2^-160 is 0 in fp32 already), so that with bf16 io an fp32 G is
+// good to 10240 x 2^-24 = 2^-10.7 at worst; with fp32 io G is an fp32 pair, whose
+// differences keep their last places.  A state that leaves the kernel (ht, and a
+// segment's state handed on) is formed from the exact products of B with the
+// scaled x as three bf16 terms (24 bits); the state that only feeds this
+// segment's bf16 y takes one term, and S and M are rounded to bf16 as operands.
 
 #include "gdn_device.h"
 #include "mixer_launch.h"
@@ -44,52 +49,114 @@ using tiles::BT;
 using tiles::perm_row;
 using tiles::u32x4;
 
-constexpr int NT = 256;   // four waves
 
 // ------------------------------------------------------------ LDS tiles
-// A tile of 64 rows (tokens) by COLS.  bf16: 16-byte units swizzled by row
-// (scan_tiles.h: both row fragments and transposing reads are conflict-free);
-// fp32: rows padded by one 16-byte unit.
+// A tile of 64 rows (tokens) by COLS in 16-byte units swizzled by row: for bf16 as
+// in scan_tiles.h (row fragments and transposing reads are conflict-free).  The
+// swizzle of a row is the same 4 and 32 rows further, and it is an XOR of the unit,
+// so one address a lane serves a whole tile: token blocks and halves are immediate
+// offsets, the 32-channel slab `k` an XOR with k * slab_x.
 template <typename T, int COLS> struct Tile;
 template <int COLS> struct Tile<bf16_t, COLS> {
-  static constexpr int bytes = BT * COLS * 2;
+  static constexpr int row_bytes = COLS * 2, bytes = BT * row_bytes, slab_x = 64;
   static constexpr int units = COLS / 8;   // 16-byte units of a row
   static __device__ __forceinline__ int off(int row, int u) { return tiles::qk_off<COLS>(row, u); }
-  // slots 32 slab + 8 q + e of a row
-  static __device__ __forceinline__ Frag<bf16_t> row_frag(const char* t, int row, int slab, int q) {
+  // slots 8 q + e of row perm_row(0, r)
+  static __device__ __forceinline__ int row_at(int r, int q) { return off(perm_row(0, r), q); }
+  // ... of row perm_row(blk, r)
+  static __device__ __forceinline__ Frag<bf16_t> row_frag(const char* t, int at, int blk) {
     Frag<bf16_t> f;
-    f.v = *reinterpret_cast<const bf16x8*>(t + off(row, 4 * slab + q));
+    f.v = *reinterpret_cast<const bf16x8*>(t + at + tiles::blk_rows(blk) * row_bytes);
     return f;
   }
-  // column `col(c)` + r % 4 of chunk c = r / 4 at tokens s0 + e: lane r addresses
-  // chunk r % 4 of token s0 + r / 4 and the transposing read deals the columns out
+  // Tokens 8 q + e of column col(r / 4) + r % 4: lane r addresses the 4-column
+  // chunk r % 4 of token r / 4 and the transposing read deals the columns out.
+  struct Col { int at; };
   template <typename F>
-  static __device__ __forceinline__ Frag<bf16_t> col_frag(const char* t, int s0, int r, F col) {
-    const int c = col(r & 3), row = s0 + (r >> 2);
-    const uint2 lo = tiles::ld_tr(t + off(row, c >> 3) + ((c & 4) << 1));
-    const uint2 hi = tiles::ld_tr(t + off(row + 4, c >> 3) + ((c & 4) << 1));
+  static __device__ __forceinline__ Col col_at(int r, int q, F col) {
+    const int c = col(r & 3);
+    return Col{off(8 * q + (r >> 2), c >> 3) + ((c & 4) << 1)};
+  }
+  // ... of tokens 32 j + 8 q + e, of the columns 4 further (half = 1) in slab k
+  static __device__ __forceinline__ Frag<bf16_t> col_frag(const char* t, const Col& c, int j, int k, int half) {
+    const char* p = t + (c.at ^ (k * slab_x)) + 32 * j * row_bytes + 8 * half;
+    const uint2 lo = tiles::ld_tr(p);
+    const uint2 hi = tiles::ld_tr(p + 4 * row_bytes);
     Frag<bf16_t> f;
     f.v = __builtin_bit_cast(bf16x8, u32x4{lo.x, lo.y, hi.x, hi.y});
     return f;
   }
 };
 template <int COLS> struct Tile<float, COLS> {
-  static constexpr int stride = COLS * 4 + 16;
-  static constexpr int bytes = BT * stride;
+  static constexpr int row_bytes = COLS * 4, bytes = BT * row_bytes, slab_x = 128;
   static constexpr int units = COLS / 4;
-  static __device__ __forceinline__ int off(int row, int u) { return row * stride + 16 * u; }
-  static __device__ __forceinline__ Frag<float> row_frag(const char* t, int row, int slab, int q) {
-    Frag<float> f;
-    load8(f, reinterpret_cast<const float*>(t + row * stride) + 32 * slab + 8 * q);
-    return f;
-  }
-  template <typename F>
-  static __device__ __forceinline__ Frag<float> col_frag(const char* t, int s0, int r, F col) {
-    const int c = col(r >> 2) + (r & 3);
+  static __device__ __forceinline__ int swz(int row) { return (((row & 3) << 1) | (((row >> 3) & 3) << 3)) & (units - 1); }
+  static __device__ __forceinline__ int off(int row, int u) { return row * row_bytes + ((u ^ swz(row)) << 4); }
+  static __device__ __forceinline__ int row_at(int r, int q) { return off(perm_row(0, r), 2 * q); }
+  static __device__ __forceinline__ Frag<float> row_frag(const char* t, int at, int blk) {
+    const char* p = t + at + tiles::blk_rows(blk) * row_bytes;   // the swizzle leaves a unit's lowest bit alone
+    const f32x4 a = *reinterpret_cast<const f32x4*>(p);
+    const f32x4 b = *reinterpret_cast<const f32x4*>(p + 16);
     Frag<float> f;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) f.v[e] = *reinterpret_cast<const float*>(t + (s0 + e) * stride + 4 * c);
+    for (int i = 0; i < 4; ++i) {
+      f.v[i] = a[i];
+      f.v[4 + i] = b[i];
+    }
     return f;
+  }
+  struct Col { int at[4]; };
+  template <typename F>
+  static __device__ __forceinline__ Col col_at(int r, int q, F col) {
+    const int c = col(r >> 2) + (r & 3);
+    Col k;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) k.at[e] = off(8 * q + e, c >> 2) + 4 * (c & 3);
+    return k;
+  }
+  static __device__ __forceinline__ Frag<float> col_frag(const char* t, const Col& c, int j, int k, int half) {
+    Frag<float> f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      f.v[e] = *reinterpret_cast<const float*>(t + (c.at[e & 3] ^ (k * slab_x)) + (32 * j + 4 * (e >> 2)) * row_bytes + 16 * half);
+    return f;
+  }
+};
+
+// Direct-to-LDS copy of a tile: a wave's load i brings 1 KiB, RPL whole rows from
+// row NW RPL i + w RPL on.  Rows past the sequence's end repeat its last row (their
+// weights are 0).  The lane offsets are computed anew for every chunk (the asm sees
+// to it): a few instructions against six registers held over the loop.
+template <typename T, int COLS, int NW>
+__device__ __forceinline__ void load_tile(const char* src, uint32_t stride, char* tile, int nr, int w, int lane) {
+  typedef Tile<T, COLS> TL;
+  constexpr int RPL = 64 / TL::units, N = BT / RPL / NW;
+  tiles::lchar* dst = (tiles::lchar*)tile + w * 1024;
+  int l = lane;
+  asm volatile("" : "+v"(l));
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const int t = (NW * i + w) * RPL + l / TL::units;
+    const uint32_t u = (uint32_t)(TL::off(t, l % TL::units) - t * TL::row_bytes);
+    const int ts = nr < BT && t >= nr ? nr - 1 : t;
+    tiles::dma16(src + ((uint32_t)ts * stride + u), dst + i * (NW * 1024));
+  }
+}
+
+// A uniform pointer that walks down the rows of an operand, 64 at a time.  The
+// empty asm keeps the compiler from folding it into per-lane 64-bit addresses:
+// base in scalar registers, 32-bit lane offsets.
+struct Walk {
+  const char* p;
+  uint32_t stride;   // bytes of a row
+  __device__ __forceinline__ void init(const Rows& r, long long brow, long long row, long long first, int elem) {
+    p = reinterpret_cast<const char*>(r.p) + (brow * r.batch + row * r.token + first) * elem;
+    stride = (uint32_t)r.token * (uint32_t)elem;
+  }
+  __device__ __forceinline__ const char* at(int row) const {   // uniform row
+    const char* x = p + (uint64_t)stride * (uint32_t)row;
+    asm volatile("" : "+s"(x));
+    return x;
   }
 };
 
@@ -131,19 +198,47 @@ __device__ __forceinline__ double wave_scan(double x) {
   x = dpp_add<0x143, 0xC>(x);   // row_bcast:31 into rows 2 and 3
   return x;
 }
-__device__ __forceinline__ double lane63(double x) {
+__device__ __forceinline__ double lane_of(double x, int l) {
   const uint64_t b = __builtin_bit_cast(uint64_t, x);
-  const uint32_t lo = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)b, 63);
-  const uint32_t hi = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(b >> 32), 63);
+  const uint32_t lo = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)b, l);
+  const uint32_t hi = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(b >> 32), l);
   return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
 }
 
-struct Gates {              // of one chunk and head, in LDS
-  float hi[BT], lo[BT];     // G_t as a pair
-  float dt[BT];             // D_t
-  float w[BT];              // D_t 2^{G_63 - G_t}
-  float eg[BT];             // 2^{G_t}
+// Gates of a chunk and head, in LDS.  Scores of tokens s, t in the same half of
+// the chunk are gated by 2^{G_t - G_s} D_s, those of s in the first and t in the
+// second half by u_t v_s, whose exponents are never positive.
+template <bool HALF> struct Gates {
+  float g[BT];            // G_t
+  float e[BT];            // G_s - log2 D_s (bf16 io); D_s (fp32 io)
+  float lo[HALF ? 1 : BT];   // what g leaves of G_t (fp32 io)
+  float uv[BT];           // v_s = D_s 2^{G_31 - G_s}, s < 32; u_t = 2^{G_t - G_31}, t >= 32
+  float w[BT];            // D_t 2^{G_63 - G_t}
+  float eg[BT];           // 2^{G_t}
 };
+
+// ------------------------------------------------------------ y, z and x rows
+// The lane's four consecutive columns of a row.
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+template <int BYTES> struct VecOf;
+template <> struct VecOf<8> { typedef u32x2 type; };
+template <> struct VecOf<16> { typedef u32x4 type; };
+
+template <typename T, typename V>
+__device__ __forceinline__ float elem(const V& v, int e) {
+  if constexpr (sizeof(T) == 2) {
+    const uint32_t w = v[e >> 1];
+    return __builtin_bit_cast(float, (e & 1) ? w & 0xFFFF0000u : w << 16);
+  } else {
+    return __builtin_bit_cast(float, (uint32_t)v[e]);
+  }
+}
+__device__ __forceinline__ void put_vec(bf16_t* p, const float (&y)[4]) {
+  *reinterpret_cast<u32x2*>(p) = u32x2{pack_bf2(y[0], y[1]), pack_bf2(y[2], y[3])};
+}
+__device__ __forceinline__ void put_vec(float* p, const float (&y)[4]) {
+  *reinterpret_cast<f32x4*>(p) = f32x4{y[0], y[1], y[2], y[3]};
+}
 
 // ------------------------------------------------------------ segments
 struct Segment {
@@ -203,12 +298,12 @@ __device__ __forceinline__ Segment find_segment(const SsmArgs& a, int seg, int s
 // OUT: the second (or only) launch, which writes y and ht; otherwise the first
 // launch of a split call, which writes segment states and log-decays.
 template <typename T, int K, int V, int NH, bool OUT>
-__global__ __launch_bounds__(NT, sizeof(T) == 2 ? 2 : 1) void ssm_scan_kernel(
+__global__ __launch_bounds__(4 * NH * V, sizeof(T) == 2 ? 4 : 2) void ssm_scan_kernel(
     SsmArgs a, int seg, int work, bool split, float* __restrict__ seg_state, double* __restrict__ seg_decay) {
   constexpr int CW = NH * V;            // columns of the work-group
-  constexpr int NB = CW / 64;           // 16-column blocks of a wave
+  constexpr int NW = CW / 16;           // waves
   constexpr int KB = K / 16, KS = K / 32;
-  constexpr bool HALF = sizeof(T) == 2;
+  constexpr bool HALF = sizeof(T) == 2;   // bf16 io
   typedef Tile<T, K> TK;
   typedef Tile<T, CW> TX;
   typedef Tile<T, BT> TM;
@@ -216,8 +311,10 @@ __global__ __launch_bounds__(NT, sizeof(T) == 2 ? 2 : 1) void ssm_scan_kernel(
   __shared__ __align__(16) char sC[OUT ? TK::bytes : 16];
   __shared__ __align__(16) char sX[TX::bytes];
   __shared__ __align__(16) char sM[OUT ? NH * TM::bytes : 16];
-  __shared__ Gates sG[2][NH];
+  __shared__ Gates<HALF> sG[2][NH];
   __shared__ float sDec[2][NH];
+  __shared__ double sA2[NH], sSum[NH];   // -exp(A_log) log2 e; log2-decay so far
+  __shared__ float sBias[NH];
 
   const int tid = threadIdx.x, lane = tid & 63;
   const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -237,41 +334,39 @@ __global__ __launch_bounds__(NT, sizeof(T) == 2 ? 2 : 1) void ssm_scan_kernel(
   const bool last = stop == sg.len;
   if (!OUT && last) return;                  // its state is nobody's start
 
-  // rows of this sequence
+  // rows of this sequence, from the segment's first on
   const long long brow = a.cu ? 0 : sg.n;
-  const T* xp = reinterpret_cast<const T*>(a.x.p) + brow * a.x.batch + sg.start * a.x.token + (long long)hv0 * V;
-  const T* bp = reinterpret_cast<const T*>(a.B.p) + brow * a.B.batch + sg.start * a.B.token + (long long)hk * K;
-  const T* cp = reinterpret_cast<const T*>(a.C.p) + brow * a.C.batch + sg.start * a.C.token + (long long)hk * K;
-  const T* dp = reinterpret_cast<const T*>(a.dt.p) + brow * a.dt.batch + sg.start * a.dt.token + hv0;
+  const long long row0 = sg.start + first;
+  Walk wx, wb, wc, wz, wd, wy;
+  wx.init(a.x, brow, row0, (long long)hv0 * V, sizeof(T));
+  wb.init(a.B, brow, row0, (long long)hk * K, sizeof(T));
+  wc.init(a.C, brow, row0, (long long)hk * K, sizeof(T));
+  wz.init(a.z, brow, row0, (long long)hv0 * V, sizeof(T));
+  wd.init(a.dt, brow, row0, hv0, sizeof(T));
+  wy.init(Rows{a.y, (long long)a.T * a.HV * V, (long long)a.HV * V}, brow, row0, (long long)hv0 * V, sizeof(T));
+  const int count = stop - first;   // tokens of the segment
 
-  // the lane's columns: block b holds column pcol(b) of the work-group's
-  const int hw = NH == 2 ? w >> 1 : 0;       // the wave's head
+  const int hw = 16 * w / V;        // the wave's head; its columns 16 w + 0 .. 15
   const int hv = hv0 + hw;
-  auto pcol = [&](int b) { return NB == 2 ? 32 * w + 8 * (r >> 2) + 4 * b + (r & 3) : 16 * w + r; };
-  auto pchunk = [&](int b, int c) { return NB == 2 ? 32 * w + 8 * c + 4 * b : 16 * w + 4 * c; };
 
-  // ---- the starting state
-  f32x4 S[KB][NB];
+  // ---- the starting state: lane (r, q) holds column 16 w + r, channels
+  // 32 k + 8 q + 0 .. 7 in S[2 k] and S[2 k + 1]
+  f32x4 S[KB];
 #pragma unroll
-  for (int k = 0; k < KB; ++k)
-#pragma unroll
-    for (int b = 0; b < NB; ++b) S[k][b] = zero4();
-  auto state_at = [&](long long entry, int b) -> size_t {   // element of the lane's (column, first channel)
-    return (((size_t)entry * a.HV + hv) * V + (pcol(b) - hw * V)) * K + 8 * q;
+  for (int k = 0; k < KB; ++k) S[k] = zero4();
+  auto state_at = [&](long long entry) -> size_t {
+    return (((size_t)entry * a.HV + hv) * V + (16 * w + r - hw * V)) * K + 8 * q;
   };
   auto add_state = [&](const float* base, long long entry, float f) {
+    const float* p = base + state_at(entry);
 #pragma unroll
-    for (int b = 0; b < NB; ++b) {
-      const float* p = base + state_at(entry, b);
+    for (int k = 0; k < KS; ++k) {
+      const f32x4 lo = *reinterpret_cast<const f32x4*>(p + 32 * k);
+      const f32x4 hi = *reinterpret_cast<const f32x4*>(p + 32 * k + 4);
 #pragma unroll
-      for (int k = 0; k < KS; ++k) {
-        const f32x4 lo = *reinterpret_cast<const f32x4*>(p + 32 * k);
-        const f32x4 hi = *reinterpret_cast<const f32x4*>(p + 32 * k + 4);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          S[2 * k][b][i] = fmaf(f, lo[i], S[2 * k][b][i]);
-          S[2 * k + 1][b][i] = fmaf(f, hi[i], S[2 * k + 1][b][i]);
-        }
+      for (int i = 0; i < 4; ++i) {
+        S[2 * k][i] = fmaf(f, lo[i], S[2 * k][i]);
+        S[2 * k + 1][i] = fmaf(f, hi[i], S[2 * k + 1][i]);
       }
     }
   };
@@ -288,321 +383,276 @@ __global__ __launch_bounds__(NT, sizeof(T) == 2 ? 2 : 1) void ssm_scan_kernel(
     if (a.h0 && f != 0.0f) add_state(a.h0, sg.n, f);
   }
 
-  // ---- staging: the next chunk's tiles in registers
-  constexpr int UB = TK::units * BT / NT, UX = TX::units * BT / NT;
-  u32x4 gB[UB], gC[OUT ? UB : 1], gX[UX];
-  float gdt = 0.f;
+  // ---- a chunk's tiles
   auto load_tiles = [&](int t0) {
-    const int nr = stop - t0;
-    const u32x4 none = {0, 0, 0, 0};
-    if (w < NH) gdt = lane < nr ? to_f(dp[(long long)(t0 + lane) * a.dt.token + w]) : 0.f;
-#pragma unroll
-    for (int i = 0; i < UB; ++i) {
-      const int row = (tid + NT * i) / TK::units, u = (tid + NT * i) % TK::units;
-      const bool in = row < nr;
-      gB[i] = none;
-      if (in) gB[i] = *reinterpret_cast<const u32x4*>(reinterpret_cast<const char*>(bp + (t0 + row) * a.B.token) + 16 * u);
-      if constexpr (OUT) {
-        gC[i] = none;
-        if (in) gC[i] = *reinterpret_cast<const u32x4*>(reinterpret_cast<const char*>(cp + (t0 + row) * a.C.token) + 16 * u);
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < UX; ++i) {
-      const int row = (tid + NT * i) / TX::units, u = (tid + NT * i) % TX::units;
-      gX[i] = none;
-      if (row < nr)
-        gX[i] = *reinterpret_cast<const u32x4*>(reinterpret_cast<const char*>(xp + (t0 + row) * a.x.token) + 16 * u);
-    }
-  };
-  auto put_tiles = [&]() {
-#pragma unroll
-    for (int i = 0; i < UB; ++i) {
-      const int row = (tid + NT * i) / TK::units, u = (tid + NT * i) % TK::units;
-      *reinterpret_cast<u32x4*>(sB + TK::off(row, u)) = gB[i];
-      if constexpr (OUT) *reinterpret_cast<u32x4*>(sC + TK::off(row, u)) = gC[i];
-    }
-#pragma unroll
-    for (int i = 0; i < UX; ++i) {
-      const int row = (tid + NT * i) / TX::units, u = (tid + NT * i) % TX::units;
-      *reinterpret_cast<u32x4*>(sX + TX::off(row, u)) = gX[i];
-    }
+    const int nr = count - t0;
+    load_tile<T, K, NW>(wb.at(t0), wb.stride, sB, nr, w, lane);
+    if (OUT) load_tile<T, K, NW>(wc.at(t0), wc.stride, sC, nr, w, lane);
+    load_tile<T, CW, NW>(wx.at(t0), wx.stride, sX, nr, w, lane);
   };
 
-  // ---- gates of a chunk: wave h takes head h, a token per lane
-  double A2 = 0.0, bias = 0.0, sum_decay = 0.0;
-  if (w < NH) {
-    A2 = -(double)expf(a.A_log[hv0 + w]) * 1.4426950408889634;
-    bias = a.dt_bias ? a.dt_bias[hv0 + w] : 0.f;
+  // ---- gates of a chunk: one of the last NH waves a head, a token per lane
+  const int gh = w - (NW - NH);     // the head whose gates the wave computes (< 0: none)
+  T gdt{};   // raw dt, loaded a chunk ahead
+  auto load_dt = [&](int t0) {
+    const int t = t0 + lane < count ? lane : 0;
+    gdt = *reinterpret_cast<const T*>(wd.at(t0) + (uint32_t)t * wd.stride + gh * (int)sizeof(T));
+  };
+  if (gh >= 0) {   // written and read by this wave only
+    sA2[gh] = -(double)expf(a.A_log[hv0 + gh]) * 1.4426950408889634;
+    sBias[gh] = a.dt_bias ? a.dt_bias[hv0 + gh] : 0.f;
+    sSum[gh] = 0.0;
   }
   auto gates = [&](int t0, int buf) {
-    float d = gdt + (float)bias;
+    float d = to_f(gdt) + sBias[gh];
     if (a.softplus) d = d <= 20.f ? log1pf(expf(d)) : d;
-    if (t0 + lane >= stop) d = 0.f;
-    const double G = wave_scan((double)d * A2);
-    const double tot = lane63(G);
+    if (t0 + lane >= count) d = 0.f;
+    double lg = (double)d * sA2[gh];
+    lg = lg < -160.0 ? -160.0 : lg;
+    const double G = wave_scan(lg);
+    const double tot = lane_of(G, 63), mid = lane_of(G, 31);
+    Gates<HALF>& g = sG[buf][gh];
     const float hi = (float)G;
-    Gates& g = sG[buf][w];
-    g.hi[lane] = hi;
-    g.lo[lane] = (float)(G - (double)hi);
-    g.dt[lane] = d;
+    g.g[lane] = hi;
+    if constexpr (HALF) {
+      g.e[lane] = hi - __builtin_amdgcn_logf(d);   // +inf where D is 0
+    } else {
+      g.e[lane] = d;
+      g.lo[lane] = (float)(G - (double)hi);
+    }
+    g.uv[lane] = lane < 32 ? d * ex2((float)(mid - G)) : ex2((float)(G - mid));
     g.w[lane] = d * ex2((float)(tot - G));
     g.eg[lane] = ex2(hi);
-    if (lane == 0) sDec[buf][w] = ex2((float)tot);
-    sum_decay += tot;
+    if (lane == 0) {
+      sDec[buf][gh] = ex2((float)tot);
+      sSum[gh] += tot;
+    }
   };
 
   const float skip = OUT && a.D ? a.D[hv] : 0.f;
   const bool fine = !OUT || (last && a.ht != nullptr);   // uniform: the state leaves the kernel
 
-  load_tiles(first);
-  if (w < NH) gates(first, 0);
+  typedef typename VecOf<4 * sizeof(T)>::type yvec;
+
+  if (count > 0) {
+    load_tiles(0);
+    if (gh >= 0) {
+      load_dt(0);
+      gates(0, 0);
+      if (count > BT) load_dt(BT);
+    }
+  }
 
   int buf = 0;
-  for (int t0 = first; t0 < stop; t0 += BT, buf ^= 1) {
-    const int nr = stop - t0 < BT ? stop - t0 : BT;
-    tiles::lds_barrier();   // everyone has read the last chunk's tiles
-    put_tiles();
+  for (int t0 = 0; t0 < count; t0 += BT, buf ^= 1) {
+    const int nr = count - t0 < BT ? count - t0 : BT;
+    const bool more = t0 + BT < count;
+    // this wave's share of the tiles: behind its loads lie only the four stores
+    // of the chunk before (a full one, so none was skipped)
+    if (OUT && t0 > 0) asm volatile("s_waitcnt vmcnt(4)" ::: "memory");
+    else asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     tiles::lds_barrier();
-    const bool more = t0 + BT < stop;
-    if (more) load_tiles(t0 + BT);
-    const Gates& g = sG[buf][hw];
+    const Gates<HALF>& g = sG[buf][hw];
+    // The lane's addresses in the tiles, made anew for every chunk (the asm sees to
+    // it): held over the loop they would spill.
+    int lt = lane;
+    asm volatile("" : "+v"(lt));
+    const int rt = lt & 15, qt = lt >> 4;
+    const int k_row = TK::row_at(rt, qt), m_row = TM::row_at(rt, qt);
 
-    // z of the lane's rows and columns (consecutive columns: 8, or 4)
-    constexpr int CL = 4 * NB;
-    const int p0 = NB == 2 ? 32 * w + 8 * q : 16 * w + 4 * q;
-    float Yz[OUT ? 4 : 1][CL];
-    u32x4 zr[OUT ? 4 : 1][CL * sizeof(T) > 16 ? 2 : 1];
-    f32x4 Y[OUT ? 4 : 1][NB];
+    f32x4 Y[4];
+    if (more && gh >= 0) {
+      gates(t0 + BT, buf ^ 1);
+      if (t0 + 2 * BT < count) load_dt(t0 + 2 * BT);
+    }
+
     if constexpr (OUT) {
-      if (a.z.p) {
-        const T* zp = reinterpret_cast<const T*>(a.z.p) + brow * a.z.batch + (sg.start + t0) * a.z.token +
-                      (long long)hv0 * V + p0;
+      // ---- M, tokens t of block tb by s of half j
+      for (int pc = w; pc < 6; pc += NW) {
+        const int tb = pc < 4 ? pc : pc - 2, j = pc < 4 ? 0 : 1;
+        const int c_at = tiles::blk_rows(tb) * TK::row_bytes, b_at = 32 * j * TK::row_bytes;
+        f32x4 E[2] = {zero4(), zero4()};
 #pragma unroll
-        for (int tb = 0; tb < 4; ++tb) {
-          const int t = perm_row(tb, r);
-          if (t < nr) {
-            const char* zt = reinterpret_cast<const char*>(zp + t * a.z.token);
-            if constexpr (CL * sizeof(T) == 8) {
-              const uint2 v = *reinterpret_cast<const uint2*>(zt);
-              zr[tb][0] = u32x4{v.x, v.y, 0, 0};
-            } else {
-              zr[tb][0] = *reinterpret_cast<const u32x4*>(zt);
-              if constexpr (CL * sizeof(T) == 32) zr[tb][1] = *reinterpret_cast<const u32x4*>(zt + 16);
-            }
-          }
+        for (int k = 0; k < KS; ++k) {
+          const Frag<T> cf = TK::row_frag(sC, (k_row ^ (k * TK::slab_x)) + c_at, 0);
+#pragma unroll
+          for (int h = 0; h < 2; ++h) E[h] = mma(TK::row_frag(sB, (k_row ^ (k * TK::slab_x)) + b_at, h), cf, E[h]);
         }
-      }
-
-      // ---- M of token block w: scores with tokens as columns, so that a lane
-      // gets 8 consecutive s of one t
-      {
-        const int t = perm_row(w, r);
-        Frag<T> ct[KS];
+        const int t = perm_row(0, rt) + tiles::blk_rows(tb);
 #pragma unroll
-        for (int k = 0; k < KS; ++k) ct[k] = TK::row_frag(sC, t, k, q);
-        for (int j = 0; j <= (w >> 1); ++j) {
-          f32x4 e0 = zero4(), e1 = zero4();
+        for (int hd = 0; hd < NH; ++hd) {
+          const Gates<HALF>& gg = sG[buf][hd];
+          f32x4 M[2];
+          if (j < (tb >> 1)) {
+            const float u = gg.uv[t];
 #pragma unroll
-          for (int k = 0; k < KS; ++k) {
-            e0 = mma(TK::row_frag(sB, perm_row(2 * j, r), k, q), ct[k], e0);
-            e1 = mma(TK::row_frag(sB, perm_row(2 * j + 1, r), k, q), ct[k], e1);
+            for (int h = 0; h < 2; ++h) {
+              const f32x4 v = *reinterpret_cast<const f32x4*>(gg.uv + 8 * qt + 4 * h);
+#pragma unroll
+              for (int e = 0; e < 4; ++e) M[h][e] = E[h][e] * (u * v[e]);
+            }
+          } else {
+            const float gt = gg.g[t], gl = HALF ? 0.f : gg.lo[HALF ? 0 : t];
+            const int past = t - 32 * j - 8 * qt;   // slots above it are later tokens
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const int s0 = 32 * j + 8 * qt + 4 * h;
+              const f32x4 ge = *reinterpret_cast<const f32x4*>(gg.e + s0);
+              if constexpr (HALF) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) M[h][e] = 4 * h + e <= past ? E[h][e] * ex2(gt - ge[e]) : 0.f;
+              } else {
+                const f32x4 gs = *reinterpret_cast<const f32x4*>(gg.g + s0);
+                const f32x4 gsl = *reinterpret_cast<const f32x4*>(gg.lo + s0);
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                  M[h][e] = 4 * h + e <= past ? E[h][e] * ge[e] * ex2((gt - gs[e]) + (gl - gsl[e])) : 0.f;
+              }
+            }
           }
-          const int s0 = 32 * j + 8 * q;
-#pragma unroll
-          for (int h = 0; h < NH; ++h) {
-            const Gates& gh = sG[buf][h];
-            const float th = gh.hi[t], tl = gh.lo[t];
-            f32x4 m0, m1;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const int sa = s0 + i, sb = s0 + 4 + i;
-              m0[i] = sa <= t ? e0[i] * gh.dt[sa] * ex2((th - gh.hi[sa]) + (tl - gh.lo[sa])) : 0.f;
-              m1[i] = sb <= t ? e1[i] * gh.dt[sb] * ex2((th - gh.hi[sb]) + (tl - gh.lo[sb])) : 0.f;
-            }
-            char* row = sM + h * TM::bytes;
-            const Frag<T> mf = frag_of(m0, m1, T());
-            if constexpr (HALF) {
-              *reinterpret_cast<bf16x8*>(row + TM::off(t, 4 * j + q)) = mf.v;
-            } else {
-              float* mp = reinterpret_cast<float*>(row + t * TM::stride) + s0;
-              *reinterpret_cast<f32x4*>(mp) = m0;
-              *reinterpret_cast<f32x4*>(mp + 4) = m1;
-            }
+          char* mp = sM + hd * TM::bytes + (m_row ^ (j * TM::slab_x)) + tiles::blk_rows(tb) * TM::row_bytes;
+          if constexpr (HALF) {
+            *reinterpret_cast<bf16x8*>(mp) = frag_of(M[0], M[1], T()).v;
+          } else {
+            *reinterpret_cast<f32x4*>(mp) = M[0];
+            *reinterpret_cast<f32x4*>(mp + 16) = M[1];
           }
         }
       }
 
       // ---- Y^T = 2^{G_t} S C^T
 #pragma unroll
-      for (int tb = 0; tb < 4; ++tb)
-#pragma unroll
-        for (int b = 0; b < NB; ++b) Y[tb][b] = zero4();
+      for (int tb = 0; tb < 4; ++tb) Y[tb] = zero4();
 #pragma unroll
       for (int k = 0; k < KS; ++k) {
-        Frag<T> sf[NB];
+        const Frag<T> sf = frag_of(S[2 * k], S[2 * k + 1], T());
 #pragma unroll
-        for (int b = 0; b < NB; ++b) sf[b] = frag_of(S[2 * k][b], S[2 * k + 1][b], T());
-#pragma unroll
-        for (int tb = 0; tb < 4; ++tb) {
-          const Frag<T> cf = TK::row_frag(sC, perm_row(tb, r), k, q);
-#pragma unroll
-          for (int b = 0; b < NB; ++b) Y[tb][b] = mma(sf[b], cf, Y[tb][b]);
-        }
+        for (int tb = 0; tb < 4; ++tb) Y[tb] = mma(sf, TK::row_frag(sC, k_row ^ (k * TK::slab_x), tb), Y[tb]);
       }
 #pragma unroll
-      for (int tb = 0; tb < 4; ++tb) {
-        const float eg = g.eg[perm_row(tb, r)];
+      for (int tb = 0; tb < 4; ++tb) Y[tb] *= g.eg[perm_row(0, rt) + tiles::blk_rows(tb)];
+      tiles::lds_barrier();   // M is complete
+    }
+
+    // ---- Y^T += x^T M^T + D x^T
+    const typename TX::Col x_col = TX::col_at(rt, qt, [&](int c) { return 16 * w + 4 * c; });
+    const typename TK::Col b_col = TK::col_at(rt, qt, [&](int c) { return 8 * c; });
+    Frag<T> xf[2];
 #pragma unroll
-        for (int b = 0; b < NB; ++b) Y[tb][b] *= eg;
+    for (int j = 0; j < 2; ++j) xf[j] = TX::col_frag(sX, x_col, j, 0, 0);
+    if constexpr (OUT) {
+#pragma unroll
+      for (int tb = 0; tb < 4; ++tb) {
+#pragma unroll
+        for (int j = 0; j <= (tb >> 1); ++j)
+          Y[tb] = mma(xf[j], TM::row_frag(sM + hw * TM::bytes, m_row ^ (j * TM::slab_x), tb), Y[tb]);
+      }
+      if (a.D) {
+        const int p0 = 16 * w + 4 * qt;   // the lane's four columns
+        const int x_row = TX::off(perm_row(0, rt), p0 * (int)sizeof(T) / 16) + (p0 * (int)sizeof(T) & 15);
+#pragma unroll
+        for (int tb = 0; tb < 4; ++tb) {
+          const yvec xv = *reinterpret_cast<const yvec*>(sX + x_row + tiles::blk_rows(tb) * TX::row_bytes);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) Y[tb][e] = fmaf(skip, elem<T>(xv, e), Y[tb][e]);
+        }
       }
     }
 
-    // the next chunk's gates, in the waves that had the fewest scores
-    if (more && w < NH) gates(t0 + BT, buf ^ 1);
-    if constexpr (OUT) tiles::lds_barrier();   // M is complete
-
-    // ---- x of the wave's columns; Y^T += x^T M^T
+    // ---- S <- 2^{G_63} S + (B^T) (w o x), in one or three bf16 terms of w o x
     const float dec = sDec[buf][hw];
 #pragma unroll
-    for (int k = 0; k < KB; ++k)
+    for (int k = 0; k < KB; ++k) S[k] *= dec;
+    auto update = [&](auto terms_) {
+      constexpr int terms = decltype(terms_)::value;
 #pragma unroll
-      for (int b = 0; b < NB; ++b) S[k][b] *= dec;
+      for (int j = 0; j < 2; ++j) {
+        Frag<T> xs[terms];
+        f32x4 p[2];
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      Frag<T> xf[NB], x1[NB], x2[NB], x3[NB];
+        for (int h = 0; h < 2; ++h) {
+          const f32x4 v = *reinterpret_cast<const f32x4*>(g.w + 32 * j + 8 * qt + 4 * h);
 #pragma unroll
-      for (int b = 0; b < NB; ++b) xf[b] = TX::col_frag(sX, 32 * j + 8 * q, r, [&](int c) { return pchunk(b, c); });
-      if constexpr (OUT) {
+          for (int e = 0; e < 4; ++e) p[h][e] = xf[j].get(4 * h + e) * v[e];
+        }
+#pragma unroll
+        for (int m = 0; m < terms; ++m) {
+          xs[m] = frag_of(p[0], p[1], T());
+          if (m + 1 < terms) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) p[e >> 2][e & 3] -= xs[m].get(e);
+          }
+        }
+#pragma unroll
+        for (int k = 0; k < KB; ++k) {
+          const Frag<T> bf = TK::col_frag(sB, b_col, j, k >> 1, k & 1);
+#pragma unroll
+          for (int m = 0; m < terms; ++m) S[k] = mma(bf, xs[m], S[k]);
+          // four operands in flight: with all of them the chunk's z would spill
+          if ((k & 3) == 3) __builtin_amdgcn_sched_barrier(0);
+        }
+      }
+    };
+    if (HALF && fine) update(tiles::Int<HALF ? 3 : 1>{});
+    else update(tiles::Int<1>{});
+    int le = lane;
+    asm volatile("" : "+v"(le));
+    const int t_row = perm_row(0, le & 15);            // y and z: rows t_row + blk_rows(tb), four columns
+    const uint32_t col_b = (16 * w + 4 * (le >> 4)) * (uint32_t)sizeof(T);
+    yvec zr[4];   // loaded here and not with the tiles: eight registers the products need
+    if constexpr (OUT) {
+      if (a.z.p) {
 #pragma unroll
         for (int tb = 0; tb < 4; ++tb) {
-          if (j <= (tb >> 1)) {
-            const Frag<T> mf = TM::row_frag(sM + hw * TM::bytes, perm_row(tb, r), j, q);
-#pragma unroll
-            for (int b = 0; b < NB; ++b) Y[tb][b] = mma(xf[b], mf, Y[tb][b]);
-          }
-        }
-      }
-      // ---- S += B^T (w o x)
-      float ws[8];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) ws[e] = g.w[32 * j + 8 * q + e];
-#pragma unroll
-      for (int b = 0; b < NB; ++b) {
-        f32x4 lo, hi;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          lo[i] = xf[b].get(i) * ws[i];
-          hi[i] = xf[b].get(4 + i) * ws[4 + i];
-        }
-        x1[b] = frag_of(lo, hi, T());
-        if constexpr (HALF) {
-          if (fine) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              lo[i] -= x1[b].get(i);
-              hi[i] -= x1[b].get(4 + i);
-            }
-            x2[b] = frag_of(lo, hi, T());
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              lo[i] -= x2[b].get(i);
-              hi[i] -= x2[b].get(4 + i);
-            }
-            x3[b] = frag_of(lo, hi, T());
-          }
-        }
-      }
-#pragma unroll
-      for (int k = 0; k < KB; ++k) {
-        const Frag<T> bf = TK::col_frag(sB, 32 * j + 8 * q, r,
-                                        [&](int c) { return 32 * (k >> 1) + 4 * (k & 1) + 8 * c; });
-#pragma unroll
-        for (int b = 0; b < NB; ++b) {
-          S[k][b] = mma(bf, x1[b], S[k][b]);
-          if constexpr (HALF) {
-            if (fine) {
-              S[k][b] = mma(bf, x2[b], S[k][b]);
-              S[k][b] = mma(bf, x3[b], S[k][b]);
-            }
-          }
+          const char* zt = wz.at(t0 + tiles::blk_rows(tb));
+          if (t_row + tiles::blk_rows(tb) < nr)
+            zr[tb] = *reinterpret_cast<const yvec*>(zt + ((uint32_t)t_row * wz.stride + col_b));
         }
       }
     }
+    tiles::lds_barrier();   // everyone is done with the tiles
+    if (more) load_tiles(t0 + BT);
+    asm volatile("" ::: "memory");   // the stores stay behind the loads
 
-    // ---- y
+    // ---- y, gated
     if constexpr (OUT) {
-      T* yp = reinterpret_cast<T*>(a.y) + ((brow * a.T + sg.start + t0) * a.HV + hv0) * (long long)V + p0;
+      const char* const yc = wy.at(t0);
 #pragma unroll
       for (int tb = 0; tb < 4; ++tb) {
-        const int t = perm_row(tb, r);
+        float y[4];
 #pragma unroll
-        for (int e = 0; e < CL; ++e) Yz[tb][e] = Y[tb][e >> 2][e & 3];
-        if (a.D) {
-          float xv[CL];
-          if constexpr (HALF) {
-            const bf16_t* xr = reinterpret_cast<const bf16_t*>(sX + TX::off(t, p0 >> 3)) + (p0 & 7);
-#pragma unroll
-            for (int e = 0; e < CL; ++e) xv[e] = bf2f(xr[e]);
-          } else {
-            const float* xr = reinterpret_cast<const float*>(sX + TX::off(t, p0 >> 2));
-#pragma unroll
-            for (int e = 0; e < CL; ++e) xv[e] = xr[e];
-          }
-#pragma unroll
-          for (int e = 0; e < CL; ++e) Yz[tb][e] = fmaf(skip, xv[e], Yz[tb][e]);
-        }
+        for (int e = 0; e < 4; ++e) y[e] = Y[tb][e];
         if (a.z.p) {
 #pragma unroll
-          for (int e = 0; e < CL; ++e) {
-            float z;
-            if constexpr (HALF) {
-              const uint32_t wd = zr[tb][0][e >> 1];
-              z = __builtin_bit_cast(float, (e & 1) ? wd & 0xFFFF0000u : wd << 16);
-            } else {
-              z = __builtin_bit_cast(float, (uint32_t)zr[tb][e >> 2][e & 3]);
-            }
-            Yz[tb][e] *= z * __builtin_amdgcn_rcpf(1.0f + __expf(-z));
+          for (int e = 0; e < 4; ++e) {
+            const float ze = elem<T>(zr[tb], e);
+            y[e] *= ze * __builtin_amdgcn_rcpf(1.0f + __expf(-ze));
           }
         }
-        if (t < nr) {
-          T* yt = yp + (long long)t * a.HV * V;
-          if constexpr (HALF && NB == 2) {
-            *reinterpret_cast<u32x4*>(yt) =
-                u32x4{pack_bf2(Yz[tb][0], Yz[tb][1]), pack_bf2(Yz[tb][2], Yz[tb][3]), pack_bf2(Yz[tb][4], Yz[tb][5]),
-                      pack_bf2(Yz[tb][6], Yz[tb][7])};
-          } else if constexpr (HALF) {
-            *reinterpret_cast<uint2*>(yt) = uint2{pack_bf2(Yz[tb][0], Yz[tb][1]), pack_bf2(Yz[tb][2], Yz[tb][3])};
-          } else {
-#pragma unroll
-            for (int e = 0; e < CL; e += 4)
-              *reinterpret_cast<f32x4*>(yt + e) = f32x4{Yz[tb][e], Yz[tb][e + 1], Yz[tb][e + 2], Yz[tb][e + 3]};
-          }
-        }
+        char* yt = const_cast<char*>(yc) + (uint64_t)wy.stride * (uint32_t)tiles::blk_rows(tb);
+        asm volatile("" : "+s"(yt));
+        if (t_row + tiles::blk_rows(tb) < nr)
+          put_vec(reinterpret_cast<T*>(yt + ((uint32_t)t_row * wy.stride + col_b)), y);
       }
     }
   }
 
   // ---- the final state
-  float* dst = OUT ? a.ht : seg_state;
   if (OUT ? (last && a.ht != nullptr) : true) {
+    float* p = (OUT ? a.ht : seg_state) + state_at(OUT ? sg.n : slot);
 #pragma unroll
-    for (int b = 0; b < NB; ++b) {
-      float* p = dst + state_at(OUT ? sg.n : slot, b);
-#pragma unroll
-      for (int k = 0; k < KS; ++k) {
-        *reinterpret_cast<f32x4*>(p + 32 * k) = S[2 * k][b];
-        *reinterpret_cast<f32x4*>(p + 32 * k + 4) = S[2 * k + 1][b];
-      }
+    for (int k = 0; k < KS; ++k) {
+      *reinterpret_cast<f32x4*>(p + 32 * k) = S[2 * k];
+      *reinterpret_cast<f32x4*>(p + 32 * k + 4) = S[2 * k + 1];
     }
   }
-  if (!OUT && w < NH && lane == 0) seg_decay[(size_t)slot * a.HV + hv0 + w] = sum_decay;
+  if (!OUT && gh >= 0 && lane == 0) seg_decay[(size_t)slot * a.HV + hv0 + gh] = sSum[gh];
 }
 
 template <typename T, int K, int V, int NH>
 hipError_t launch_t(const SsmArgs& a, const SsmPlan& p, hipStream_t s) {
   const int work = p.slots * (a.HV / NH);
-  const dim3 grid((unsigned)((work + 7) / 8 * 8)), block(NT);
+  const dim3 grid((unsigned)((work + 7) / 8 * 8)), block(4 * NH * V);
   float* st = reinterpret_cast<float*>(a.workspace);
   double* dec = p.split ? reinterpret_cast<double*>(reinterpret_cast<char*>(a.workspace) + p.decay_off) : nullptr;
   if (p.split) {
