@@ -232,8 +232,9 @@ int ssm_chunk_fwd(const void* x, long long x_batch, long long x_token, const voi
   }
   if (!aligned16(h0) || !aligned16(ht))
     return fail(GDN_ERR_INVALID_ARGUMENT, "h0 and ht must be 16-byte aligned");
-  // one launch indexes (segment, head) pairs, at most one segment per 64 tokens, with 32-bit integers
-  if (((long long)B * T / 64 + a.N + 8) * HV >= (1LL << 31))
+  // one launch indexes (segment, head) pairs, at most one segment per 64 tokens, or 16 blocks of a
+  // (sequence, head) with 32-bit integers
+  if (((long long)B * T / 64 + a.N + 8) * HV >= (1LL << 31) || (long long)a.N * HV * 16 >= (1LL << 31))
     return fail(GDN_ERR_UNSUPPORTED, "too many sequences x heads for one launch (N=%d HV=%d)", a.N, HV);
   const SsmPlan p = ssm_plan(B, T, Hk, HV, K, V, a.N, cu_seqlens != nullptr, a.bf16 != 0);
   if (p.bytes > 0) {

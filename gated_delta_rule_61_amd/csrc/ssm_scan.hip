@@ -24,9 +24,9 @@
 // direct-to-LDS loads into one buffer: 69 KiB a work-group at K = 128, two
 // work-groups a CU (four waves a SIMD), which hide each other's latencies.  Where
 // sequences x heads are too few for the chip, sequences are split: a first
-// launch computes each segment's own final state (from zeros) and log-decay,
-// and the segment's work-group of the second launch starts from the decayed sum
-// of those before it (and h0).  That reads x and B twice but moves no
+// launch computes each segment's own final state (from zeros) and log-decay, a
+// second one joins them with h0 in order, and the third starts each segment from
+// the state behind the one before.  That reads x and B twice but moves no
 // per-chunk states.
 //
 // Precision.  Gate sums are taken in 64 bits, over log2-decays held at -160 a
@@ -130,18 +130,56 @@ template <int COLS> struct Tile<float, COLS> {
 template <typename T, int COLS, int NW>
 __device__ __forceinline__ void load_tile(const char* src, uint32_t stride, char* tile, int nr, int w, int lane) {
   typedef Tile<T, COLS> TL;
-  constexpr int RPL = 64 / TL::units, N = BT / RPL / NW;
+  constexpr int RPL = 64 / TL::units, N = BT / RPL / NW, H = N >= 2 ? N / 2 : 1;   // H: loads of 32 rows
   tiles::lchar* dst = (tiles::lchar*)tile + w * 1024;
   int l = lane;
   asm volatile("" : "+v"(l));
+  const int t0 = w * RPL + l / TL::units;
+  if (nr >= BT) {   // the swizzle repeats every 32 rows, and so do the lane offsets
+    uint32_t off[H];
 #pragma unroll
-  for (int i = 0; i < N; ++i) {
-    const int t = (NW * i + w) * RPL + l / TL::units;
-    const uint32_t u = (uint32_t)(TL::off(t, l % TL::units) - t * TL::row_bytes);
-    const int ts = nr < BT && t >= nr ? nr - 1 : t;
-    tiles::dma16(src + ((uint32_t)ts * stride + u), dst + i * (NW * 1024));
+    for (int i = 0; i < H; ++i) {
+      const int t = t0 + NW * RPL * i;
+      off[i] = (uint32_t)t * stride + (uint32_t)(TL::off(t, l % TL::units) - t * TL::row_bytes);
+    }
+#pragma unroll
+    for (int h = 0; h < N / H; ++h) {
+      const char* sh = src + (uint64_t)stride * (uint32_t)(32 * h);
+      asm volatile("" : "+s"(sh));
+#pragma unroll
+      for (int i = 0; i < H; ++i) tiles::dma16(sh + off[i], dst + (h * H + i) * (NW * 1024));
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int t = t0 + NW * RPL * i;
+      const uint32_t u = (uint32_t)(TL::off(t, l % TL::units) - t * TL::row_bytes);
+      tiles::dma16(src + ((uint32_t)(t < nr ? t : nr - 1) * stride + u), dst + i * (NW * 1024));
+    }
   }
 }
+
+// The same through registers.
+template <typename T, int COLS, int NW>
+struct StageTile {
+  typedef Tile<T, COLS> TL;
+  static constexpr int RPL = 64 / TL::units, N = BT / RPL / NW;
+  u32x4 v[N];
+  __device__ __forceinline__ void load(const char* src, uint32_t stride, int w, int lane) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int t = (NW * i + w) * RPL + lane / TL::units;
+      v[i] = *reinterpret_cast<const u32x4*>(src + ((uint32_t)t * stride + 16u * (uint32_t)(lane % TL::units)));
+    }
+  }
+  __device__ __forceinline__ void put(char* tile, int w, int lane) const {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int t = (NW * i + w) * RPL + lane / TL::units;
+      *reinterpret_cast<u32x4*>(tile + TL::off(t, lane % TL::units)) = v[i];
+    }
+  }
+};
 
 // A uniform pointer that walks down the rows of an operand, 64 at a time.  The
 // empty asm keeps the compiler from folding it into per-lane 64-bit addresses:
@@ -208,13 +246,13 @@ __device__ __forceinline__ double lane_of(double x, int l) {
 // Gates of a chunk and head, in LDS.  Scores of tokens s, t in the same half of
 // the chunk are gated by 2^{G_t - G_s} D_s, those of s in the first and t in the
 // second half by u_t v_s, whose exponents are never positive.
-template <bool HALF> struct Gates {
+template <bool HALF> struct alignas(16) Gates {
   float g[BT];            // G_t
   float e[BT];            // G_s - log2 D_s (bf16 io); D_s (fp32 io)
-  float lo[HALF ? 1 : BT];   // what g leaves of G_t (fp32 io)
   float uv[BT];           // v_s = D_s 2^{G_31 - G_s}, s < 32; u_t = 2^{G_t - G_31}, t >= 32
   float w[BT];            // D_t 2^{G_63 - G_t}
   float eg[BT];           // 2^{G_t}
+  float lo[HALF ? 4 : BT];   // what g leaves of G_t (fp32 io)
 };
 
 // ------------------------------------------------------------ y, z and x rows
@@ -295,7 +333,7 @@ __device__ __forceinline__ Segment find_segment(const SsmArgs& a, int seg, int s
 }
 
 // ------------------------------------------------------------ the scan
-// OUT: the second (or only) launch, which writes y and ht; otherwise the first
+// OUT: the last (or only) launch, which writes y and ht; otherwise the first
 // launch of a split call, which writes segment states and log-decays.
 template <typename T, int K, int V, int NH, bool OUT>
 __global__ __launch_bounds__(4 * NH * V, sizeof(T) == 2 ? 4 : 2) void ssm_scan_kernel(
@@ -357,39 +395,30 @@ __global__ __launch_bounds__(4 * NH * V, sizeof(T) == 2 ? 4 : 2) void ssm_scan_k
   auto state_at = [&](long long entry) -> size_t {
     return (((size_t)entry * a.HV + hv) * V + (16 * w + r - hw * V)) * K + 8 * q;
   };
-  auto add_state = [&](const float* base, long long entry, float f) {
+  auto load_state = [&](const float* base, long long entry) {
     const float* p = base + state_at(entry);
 #pragma unroll
     for (int k = 0; k < KS; ++k) {
-      const f32x4 lo = *reinterpret_cast<const f32x4*>(p + 32 * k);
-      const f32x4 hi = *reinterpret_cast<const f32x4*>(p + 32 * k + 4);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        S[2 * k][i] = fmaf(f, lo[i], S[2 * k][i]);
-        S[2 * k + 1][i] = fmaf(f, hi[i], S[2 * k + 1][i]);
-      }
+      S[2 * k] = *reinterpret_cast<const f32x4*>(p + 32 * k);
+      S[2 * k + 1] = *reinterpret_cast<const f32x4*>(p + 32 * k + 4);
     }
   };
   if (OUT) {
-    // the segments before this one, nearest first; behind a decay that has
-    // underflowed nothing is left to add
-    double past = 0.0;
-    float f = 1.0f;
-    for (int i = 1; i <= sg.j && f != 0.0f; ++i) {
-      add_state(seg_state, slot - i, f);
-      past += seg_decay[(size_t)(slot - i) * a.HV + hv];
-      f = ex2((float)past);
-    }
-    if (a.h0 && f != 0.0f) add_state(a.h0, sg.n, f);
+    if (sg.j > 0) load_state(seg_state, slot - 1);   // the joined state behind the segment before
+    else if (a.h0) load_state(a.h0, sg.n);
   }
 
   // ---- a chunk's tiles
   auto load_tiles = [&](int t0) {
     const int nr = count - t0;
     load_tile<T, K, NW>(wb.at(t0), wb.stride, sB, nr, w, lane);
-    if (OUT) load_tile<T, K, NW>(wc.at(t0), wc.stride, sC, nr, w, lane);
+    load_tile<T, K, NW>(wc.at(t0), wc.stride, sC, nr, w, lane);
     load_tile<T, CW, NW>(wx.at(t0), wx.stride, sX, nr, w, lane);
   };
+  // The first launch has the registers to hold the next chunk's tiles while it
+  // computes; its segments are full, as no sequence ends in them.
+  StageTile<T, K, NW> gB;
+  StageTile<T, CW, NW> gX;
 
   // ---- gates of a chunk: one of the last NH waves a head, a token per lane
   const int gh = w - (NW - NH);     // the head whose gates the wave computes (< 0: none)
@@ -435,7 +464,12 @@ __global__ __launch_bounds__(4 * NH * V, sizeof(T) == 2 ? 4 : 2) void ssm_scan_k
   typedef typename VecOf<4 * sizeof(T)>::type yvec;
 
   if (count > 0) {
-    load_tiles(0);
+    if constexpr (OUT) {
+      load_tiles(0);
+    } else {
+      gB.load(wb.at(0), wb.stride, w, lane);
+      gX.load(wx.at(0), wx.stride, w, lane);
+    }
     if (gh >= 0) {
       load_dt(0);
       gates(0, 0);
@@ -447,11 +481,22 @@ __global__ __launch_bounds__(4 * NH * V, sizeof(T) == 2 ? 4 : 2) void ssm_scan_k
   for (int t0 = 0; t0 < count; t0 += BT, buf ^= 1) {
     const int nr = count - t0 < BT ? count - t0 : BT;
     const bool more = t0 + BT < count;
-    // this wave's share of the tiles: behind its loads lie only the four stores
-    // of the chunk before (a full one, so none was skipped)
-    if (OUT && t0 > 0) asm volatile("s_waitcnt vmcnt(4)" ::: "memory");
-    else asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    if constexpr (OUT) {
+      // this wave's share of the tiles: behind its loads lie only the four stores
+      // of the chunk before (a full one, so none was skipped)
+      if (t0 > 0) asm volatile("s_waitcnt vmcnt(4)" ::: "memory");
+      else asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    } else {
+      gB.put(sB, w, lane);
+      gX.put(sX, w, lane);
+    }
     tiles::lds_barrier();
+    if constexpr (!OUT) {
+      if (more) {
+        gB.load(wb.at(t0 + BT), wb.stride, w, lane);
+        gX.load(wx.at(t0 + BT), wx.stride, w, lane);
+      }
+    }
     const Gates<HALF>& g = sG[buf][hw];
     // The lane's addresses in the tiles, made anew for every chunk (the asm sees to
     // it): held over the loop they would spill.
@@ -611,7 +656,7 @@ __global__ __launch_bounds__(4 * NH * V, sizeof(T) == 2 ? 4 : 2) void ssm_scan_k
       }
     }
     tiles::lds_barrier();   // everyone is done with the tiles
-    if (more) load_tiles(t0 + BT);
+    if (OUT && more) load_tiles(t0 + BT);
     asm volatile("" ::: "memory");   // the stores stay behind the loads
 
     // ---- y, gated
@@ -649,6 +694,64 @@ __global__ __launch_bounds__(4 * NH * V, sizeof(T) == 2 ? 4 : 2) void ssm_scan_k
   if (!OUT && gh >= 0 && lane == 0) seg_decay[(size_t)slot * a.HV + hv0 + gh] = sSum[gh];
 }
 
+// Joins the segments of a split call: each segment's own final state (from zeros)
+// becomes the state behind it, in place (the last segment of a sequence has none).
+// A thread owns four elements of a (sequence, head) and walks down its segments,
+// the loads of four in flight together.  Memory-bound: every state once in and out.
+__global__ __launch_bounds__(256) void ssm_join_kernel(SsmArgs a, int seg, int blocks_per_head,
+                                                       float* __restrict__ seg_state,
+                                                       const double* __restrict__ seg_decay) {
+  const int lane = threadIdx.x & 63;
+  const int nh = blockIdx.x / blocks_per_head;
+  const int part = blockIdx.x - nh * blocks_per_head;
+  const int n = nh / a.HV, hv = nh - n * a.HV;
+  int slot0 = 0, segs = 1;
+  if (!a.cu) {
+    segs = a.T > seg ? (a.T + seg - 1) / seg : 1;
+    slot0 = n * segs;
+  } else {   // slots of the sequences before n, summed over the wave
+    int before = 0;
+    for (int m = lane; m <= n; m += 64) {
+      long long b0 = a.cu[m], b1 = a.cu[m + 1];
+      b0 = b0 < 0 ? 0 : (b0 > a.T ? a.T : b0);
+      b1 = b1 < b0 ? b0 : (b1 > a.T ? a.T : b1);
+      const int len = (int)(b1 - b0), c = len > seg ? (len + seg - 1) / seg : 1;
+      if (m < n) before += c;
+      else segs = c;
+    }
+#pragma unroll
+    for (int off = 32; off > 0; off >>= 1) before += __shfl_xor(before, off, 64);
+    slot0 = before;
+    segs = __shfl(segs, n & 63, 64);
+  }
+  if (segs < 2) return;
+  const size_t VK = (size_t)a.V * a.K, head = (size_t)a.HV * VK;
+  const size_t e0 = ((size_t)part * 256 + threadIdx.x) * 4;
+  f32x4 st = zero4();
+  if (a.h0) st = *reinterpret_cast<const f32x4*>(a.h0 + (size_t)n * head + hv * VK + e0);
+  float* p = seg_state + (size_t)slot0 * head + hv * VK + e0;
+  const double* d = seg_decay + (size_t)slot0 * a.HV + hv;
+  constexpr int U = 4;
+  for (int j = 0; j < segs - 1; j += U) {
+    f32x4 own[U];
+    float f[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int i = j + u < segs - 1 ? j + u : j;
+      own[u] = *reinterpret_cast<const f32x4*>(p + i * head);
+      f[u] = ex2((float)d[(size_t)i * a.HV]);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (j + u < segs - 1) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) st[e] = fmaf(f[u], st[e], own[u][e]);
+        *reinterpret_cast<f32x4*>(p + (size_t)(j + u) * head) = st;
+      }
+    }
+  }
+}
+
 template <typename T, int K, int V, int NH>
 hipError_t launch_t(const SsmArgs& a, const SsmPlan& p, hipStream_t s) {
   const int work = p.slots * (a.HV / NH);
@@ -657,7 +760,12 @@ hipError_t launch_t(const SsmArgs& a, const SsmPlan& p, hipStream_t s) {
   double* dec = p.split ? reinterpret_cast<double*>(reinterpret_cast<char*>(a.workspace) + p.decay_off) : nullptr;
   if (p.split) {
     hipLaunchKernelGGL((ssm_scan_kernel<T, K, V, NH, false>), grid, block, 0, s, a, p.seg, work, true, st, dec);
-    const hipError_t e = hipGetLastError();
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    constexpr int per_head = K * V / 1024;
+    hipLaunchKernelGGL(ssm_join_kernel, dim3((unsigned)((long long)a.N * a.HV * per_head)), dim3(256), 0, s, a, p.seg,
+                       per_head, st, dec);
+    e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
   hipLaunchKernelGGL((ssm_scan_kernel<T, K, V, NH, true>), grid, block, 0, s, a, p.seg, work, p.split, st, dec);
