@@ -698,7 +698,7 @@ __global__ __launch_bounds__(4 * NH * V, sizeof(T) == 2 ? 4 : 2) void ssm_scan_k
 // becomes the state behind it, in place (the last segment of a sequence has none).
 // A thread owns four elements of a (sequence, head) and walks down its segments,
 // the loads of four in flight together.  Memory-bound: every state once in and out.
-__global__ __launch_bounds__(256) void ssm_join_kernel(SsmArgs a, int seg, int blocks_per_head,
+__global__ __launch_bounds__(256) void ssm_join_kernel(SsmArgs a, int seg, int slots, int blocks_per_head,
                                                        float* __restrict__ seg_state,
                                                        const double* __restrict__ seg_decay) {
   const int lane = threadIdx.x & 63;
@@ -724,6 +724,8 @@ __global__ __launch_bounds__(256) void ssm_join_kernel(SsmArgs a, int seg, int b
     slot0 = before;
     segs = __shfl(segs, n & 63, 64);
   }
+  // boundaries out of order may claim more slots than there are
+  if (segs > slots - slot0) segs = slots - slot0;
   if (segs < 2) return;
   const size_t VK = (size_t)a.V * a.K, head = (size_t)a.HV * VK;
   const size_t e0 = ((size_t)part * 256 + threadIdx.x) * 4;
@@ -764,7 +766,7 @@ hipError_t launch_t(const SsmArgs& a, const SsmPlan& p, hipStream_t s) {
     if (e != hipSuccess) return e;
     constexpr int per_head = K * V / 1024;
     hipLaunchKernelGGL(ssm_join_kernel, dim3((unsigned)((long long)a.N * a.HV * per_head)), dim3(256), 0, s, a, p.seg,
-                       per_head, st, dec);
+                       p.slots, per_head, st, dec);
     e = hipGetLastError();
     if (e != hipSuccess) return e;
   }

@@ -506,10 +506,11 @@ int gdn_conv_step(const void* x, long long x_batch, long long x_token, const voi
  * chunk_size = 64; x, Bm, Cm, z and their strides in multiples of 16 bytes.
  * Sums, gates and states are fp32 or wider; with bf16 io the products that make
  * y take the state and the decayed scores rounded to bf16, those that make ht
- * lose nothing to fp32.  Tokens are taken in chunks of 64 as matrix products, in
- * which every token of a chunk is multiplied by the weights (zero or not) of the
- * others: an infinity or NaN in x, dt, Bm or Cm makes values of that whole chunk
- * (of the heads that read it) and behind it NaN.  Allocates nothing;
+ * lose nothing to fp32.  Tokens are taken in chunks of 64 (from each sequence's
+ * start) as matrix products: an infinity or NaN in x makes its channel's outputs
+ * NaN from the beginning of its chunk on, where the recurrence would from its
+ * token on; one in dt, Bm or Cm reaches the tokens the recurrence says.
+ * Allocates nothing;
  * asynchronous on `stream`.
  */
 size_t ssm_chunk_fwd_workspace_bytes(int B, int T, int Hk, int HV, int K, int V, int num_seqs, int varlen,

@@ -36,10 +36,12 @@ from .bf16 import round_to_bf16
 from .handoff import state_to_pool
 from .backward import state_grad_scan
 from .state_scan import state_scan
+from .mixer import causal_conv, head_norm, quantise_state, silu, ssm_scan
 
 __all__ = [
     "delta_rule_recurrent", "gdn_recurrent", "kda_recurrent",
     "chunk_intra_matrices", "chunk_intra_wu",
     "decode_gate", "decode_normalize", "gdn_decode",
     "round_to_bf16", "state_to_pool", "state_grad_scan", "state_scan",
+    "causal_conv", "head_norm", "quantise_state", "silu", "ssm_scan",
 ]

@@ -1,0 +1,237 @@
+"""GPU parity of the selective state-space scan (prompts) and step (single
+tokens) against the fp64 oracle."""
+
+import numpy as np
+import pytest
+import torch
+
+from gated_delta_rule_61_amd import binding
+from tests.mixer_cases import BF, DEV, U, bits, close, d, edges, f64, randn, same, ssm_bound, ssm_inputs, ssm_ref, store
+
+pytestmark = pytest.mark.gpu
+F32 = torch.float32
+
+
+def _run(p, **kw):
+    return binding.ssm_chunk_fwd(*(d(p[n]) for n in ("x", "dt", "Bm", "Cm", "A_log")), D=d(p["D"]), z=d(p["z"]),
+                                 dt_bias=d(p["dt_bias"]), h0=d(p["h0"]), **kw)
+
+
+def _check(p, lens, dtype, softplus=True, **kw):
+    y, ht = _run(p, dt_softplus=softplus, **kw)
+    torch.cuda.synchronize()
+    ry, mag, skip, rh, hm = ssm_ref(p, lens, softplus)
+    close("y", y.reshape(-1, *y.shape[2:]), ry, ssm_bound(dtype, ry, mag, skip))
+    close("ht", ht, rh, 512 * U * hm + 2.0 ** -20 * hm)
+
+
+# (dtype, lengths or (B, T), Hk, HV, K, V, z, D, h0)
+CASES = [
+    (BF, [64, 1, 63, 0, 65, 130, 2], 1, 4, 128, 64, True, True, True),
+    (F32, [64, 1, 63, 0, 65, 130, 2], 1, 4, 128, 64, True, True, True),
+    (BF, (2, 100), 3, 3, 64, 64, False, True, False),       # odd number of heads a group: one head a work-group
+    (F32, (2, 100), 3, 3, 64, 64, False, True, False),
+    (BF, (1, 200), 2, 4, 64, 128, True, False, True),
+    (F32, (1, 129), 2, 4, 128, 128, False, False, True),
+    (BF, (3, 70), 2, 2, 128, 128, True, True, False),
+    (F32, (3, 1), 1, 2, 64, 64, True, True, True),
+    (BF, (5, 1), 1, 6, 128, 64, True, True, True),
+    (BF, [3] * 150, 1, 2, 64, 64, False, False, True),      # more sequences than a wave has lanes
+    (F32, [0, 0], 1, 2, 64, 128, False, True, True),
+]
+
+
+@pytest.mark.parametrize("case", CASES, ids=lambda c: f"{str(c[0])[6:]}-{len(c[1])}seq-{c[2]}x{c[3]}-K{c[4]}V{c[5]}")
+def test_scan(case):
+    dtype, lens, Hk, HV, K, V, z, D, h0 = case
+    print(f"scan {case}", flush=True)
+    dense = isinstance(lens, tuple)
+    B, T = lens if dense else (1, sum(lens))
+    seqs = [T] * B if dense else lens
+    p = ssm_inputs(100, B, T, Hk, HV, K, V, dtype, N=len(seqs), z=z, D=D, h0=h0)
+    cu = None if dense else torch.tensor(edges(seqs), dtype=torch.int64, device=DEV)
+    _check(p, seqs, dtype, cu_seqlens=cu)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("lens", [(1, 2200), [1500, 0, 40, 700, 1], (2, 1025)])
+def test_scan_split_into_segments(dtype, lens):
+    """Few sequences and heads: segments of 256 tokens and their join."""
+    dense = isinstance(lens, tuple)
+    B, T = lens if dense else (1, sum(lens))
+    seqs = [T] * B if dense else lens
+    print(f"scan split {dtype} {lens}", flush=True)
+    assert binding.ssm_workspace_bytes(B, T, 1, 2, 64, 64, len(seqs), dtype, varlen=not dense) > 0
+    p = ssm_inputs(200, B, T, 1, 2, 64, 64, dtype, N=len(seqs))
+    cu = None if dense else torch.tensor(edges(seqs), dtype=torch.int64, device=DEV)
+    _check(p, seqs, dtype, cu_seqlens=cu)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("fast", [6.0, 25.0, -12.0])
+def test_scan_strong_and_weak_decays(dtype, fast):
+    """Step sizes of several units (every factor underflows within a chunk or a
+    segment), past the softplus threshold, and of 1e-7 (nothing decays)."""
+    print(f"scan decays {dtype} {fast}", flush=True)
+    p = ssm_inputs(300, 1, 700, 1, 2, 64, 64, dtype, fast=fast)
+    _check(p, [700], dtype)
+
+
+def test_scan_without_softplus_and_final_state():
+    print("scan plain dt", flush=True)
+    p = ssm_inputs(400, 2, 90, 1, 2, 128, 64, F32)
+    p["dt"], p["dt_bias"] = p["dt"].abs() * 0.1, torch.zeros(2)
+    p["dt"][0, 5] = 0.0           # a token that leaves the state alone and adds nothing
+    _check(p, [90, 90], F32, softplus=False)
+    y, ht = _run(p, dt_softplus=False, output_final_state=False)
+    assert ht is None
+    same([y], [_run(p, dt_softplus=False)[0]], "without the final state")
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_scan_takes_slices(dtype):
+    """x, B, C side by side in one tensor, z and dt in another, as a layer has them."""
+    print(f"scan slices {dtype}", flush=True)
+    B, T, Hk, HV, K, V = 2, 77, 2, 4, 64, 64
+    xbc, zdt = randn(1, B, T, HV * V + 2 * Hk * K + 32, dtype=dtype), randn(2, B, T, HV * V + 16, dtype=dtype)
+    p = ssm_inputs(500, B, T, Hk, HV, K, V, dtype)
+    p["x"] = xbc[..., :HV * V].unflatten(-1, (HV, V))
+    p["Bm"] = xbc[..., HV * V:HV * V + Hk * K].unflatten(-1, (Hk, K))
+    p["Cm"] = xbc[..., HV * V + Hk * K:HV * V + 2 * Hk * K].unflatten(-1, (Hk, K))
+    p["z"], p["dt"] = zdt[..., :HV * V].unflatten(-1, (HV, V)), zdt[..., HV * V:HV * V + HV]
+    gx, gz = d(xbc), d(zdt)
+    args = (gx[..., :HV * V].unflatten(-1, (HV, V)), gz[..., HV * V:HV * V + HV],
+            gx[..., HV * V:HV * V + Hk * K].unflatten(-1, (Hk, K)),
+            gx[..., HV * V + Hk * K:HV * V + 2 * Hk * K].unflatten(-1, (Hk, K)))
+    kw = dict(D=d(p["D"]), z=gz[..., :HV * V].unflatten(-1, (HV, V)), dt_bias=d(p["dt_bias"]), h0=d(p["h0"]))
+    got = binding.ssm_chunk_fwd(*args, d(p["A_log"]), **kw)
+    kw["z"] = kw["z"].contiguous()
+    packed = binding.ssm_chunk_fwd(*(a.contiguous() for a in args), d(p["A_log"]), **kw)
+    torch.cuda.synchronize()
+    same(got, packed, "slices")
+    ry, mag, skip, _, _ = ssm_ref(p, [T] * B)
+    close("y", got[0].reshape(-1, HV, V), ry, ssm_bound(dtype, ry, mag, skip))
+
+
+def test_scan_leaves_rows_behind_the_last_sequence():
+    print("scan padded batch", flush=True)
+    p = ssm_inputs(600, 1, 150, 1, 2, 64, 64, BF, N=2)
+    for n in ("x", "Bm", "Cm", "z"):
+        p[n][:, 100:] = float("nan")
+    cu = torch.tensor([0, 31, 100], dtype=torch.int64, device=DEV)
+    out = torch.full((1, 150, 2, 64), 5.0, dtype=BF, device=DEV)
+    y, ht = _run(p, cu_seqlens=cu, out=out)
+    torch.cuda.synchronize()
+    assert y is out and torch.all(out[:, 100:] == 5.0)
+    q = {n: (v[:, :100] if n in ("x", "dt", "Bm", "Cm", "z") else v) for n, v in p.items()}
+    ry, mag, skip, rh, hm = ssm_ref(q, [31, 69])
+    close("y", out[0, :100], ry, ssm_bound(BF, ry, mag, skip))
+    close("ht", ht, rh, 512 * U * hm + 2.0 ** -20 * hm)
+
+
+def test_nan_stays_in_its_sequence_and_heads():
+    print("scan nan", flush=True)
+    p = ssm_inputs(700, 1, 200, 2, 4, 64, 64, BF, N=2)
+    cu = torch.tensor([0, 90, 200], dtype=torch.int64, device=DEV)
+    clean = _run(p, cu_seqlens=cu)
+    p["x"][0, 70, 1, 3] = float("nan")       # sequence 0, head 1, one channel
+    p["Bm"][0, 150, 1, 5] = float("inf")     # sequence 1, group 1 (heads 2 and 3)
+    dirty = _run(p, cu_seqlens=cu)
+    torch.cuda.synchronize()
+    y0, y1 = clean[0].cpu(), dirty[0].cpu()
+    assert torch.equal(bits(y0[0, :90, [0, 2, 3]]), bits(y1[0, :90, [0, 2, 3]]))
+    assert torch.equal(bits(y0[0, :64, 1]), bits(y1[0, :64, 1]))          # the chunk before it
+    assert torch.all(torch.isnan(y1[0, 70:90, 1, 3]))
+    assert torch.equal(bits(y0[0, 90:, :2]), bits(y1[0, 90:, :2]))
+    assert torch.equal(bits(y0[0, 90:150, 2:]), bits(y1[0, 90:150, 2:]))   # token 150 is the first that reads it
+    other = [c for c in range(64) if c != 3]
+    assert torch.equal(bits(y0[0, :90, 1][:, other]), bits(y1[0, :90, 1][:, other]))
+    assert torch.equal(bits(clean[1].cpu()[0, [0, 2, 3]]), bits(dirty[1].cpu()[0, [0, 2, 3]]))
+
+
+def test_boundaries_out_of_order_stay_in_the_buffers():
+    """Nonsense boundaries: results unspecified, nothing outside the buffers is touched."""
+    print("scan / conv bad boundaries", flush=True)
+    p = ssm_inputs(800, 1, 300, 1, 2, 64, 64, BF, N=5)
+    cu = torch.tensor([-40, 280, 20, 700, 3, 300], dtype=torch.int64, device=DEV)
+    guard = torch.full((3, 1, 300, 2, 64), 3.0, dtype=BF, device=DEV)
+    nbytes = binding.ssm_workspace_bytes(1, 300, 1, 2, 64, 64, 5, BF, varlen=True)
+    ws = torch.zeros(nbytes + 4096, dtype=torch.uint8, device=DEV)
+    _run(p, cu_seqlens=cu, out=guard[1], workspace=ws[:max(nbytes, 256)] if nbytes else None)
+    out = torch.full((3, 1, 300, 128), 3.0, dtype=BF, device=DEV)
+    x, w = d(p["x"]).flatten(2), d(randn(801, 128, 4, dtype=BF))
+    state = torch.full((3, 5, 3, 128), 3.0, dtype=BF, device=DEV)
+    binding.causal_conv_fwd(x, w, cu_seqlens=cu, out=out[1], state=state[1])
+    torch.cuda.synchronize()
+    assert torch.all(guard[0] == 3) and torch.all(guard[2] == 3) and not ws[nbytes:].any()
+    assert torch.all(out[0] == 3) and torch.all(out[2] == 3)
+    assert torch.all(state[0] == 3) and torch.all(state[2] == 3)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("sdt", [BF, F32])
+@pytest.mark.parametrize("K,V,T,B", [(64, 64, 1, 5), (128, 64, 4, 3), (64, 128, 2, 4), (128, 128, 3, 3), (128, 128, 1, 300)])
+def test_step(dtype, sdt, K, V, T, B):
+    print(f"step {dtype} pool {sdt} K={K} V={V} T={T} B={B}", flush=True)
+    Hk, HV, n = 1, 2, min(B, 5)
+    p = ssm_inputs(900, B, T, Hk, HV, K, V, dtype, h0=False, z=T != 2, D=T != 3)
+    base = randn(901, B + 2, HV, V, K, dtype=sdt, scale=0.3)
+    idx = torch.randperm(B + 2, generator=torch.Generator().manual_seed(1))[:B].to(torch.int32)
+    idx[1] = -1
+    idx[2] = B + 2
+    pool = d(base).clone()
+    y = binding.ssm_step(*(d(p[k]) for k in ("x", "dt", "Bm", "Cm", "A_log")), pool, state_indices=d(idx), D=d(p["D"]),
+                         z=d(p["z"]), dt_bias=d(p["dt_bias"]))
+    torch.cuda.synchronize()
+    assert not y[1].any() and not y[2].any()
+    named = {int(i) for i in idx if 0 <= i < B + 2}
+    for s in range(B + 2):
+        if s not in named:
+            assert torch.equal(bits(pool[s]), bits(d(base[s])))
+    for b in sorted({*range(n), B - 1} - {1, 2}):
+        one = {k: (v[b:b + 1] if v is not None and k in ("x", "dt", "Bm", "Cm", "z") else v) for k, v in p.items()}
+        one["h0"] = base[int(idx[b])][None].float()
+        ry, mag, skip, rh, hm = ssm_ref(one, [T])
+        # no operand is rounded here: fp32 throughout, then the storage
+        close(f"y[{b}]", y[b], ry, 512 * U * mag + 2.0 ** -20 * (mag + skip) + store(dtype, ry))
+        close(f"state[{b}]", pool[int(idx[b])], rh[0], 2.0 ** -20 * hm[0] + store(sdt, rh[0]))
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_steps_continue_a_prompt(dtype):
+    print(f"prompt then steps {dtype}", flush=True)
+    p = ssm_inputs(1000, 2, 107, 1, 2, 128, 64, dtype)
+    cut = {n: (v[:, :100].contiguous() if v is not None and n in ("x", "dt", "Bm", "Cm", "z") else v) for n, v in p.items()}
+    _, ht = _run(cut)
+    pool = ht.clone()
+    ys = []
+    for lo, hi in ((100, 101), (101, 105), (105, 107)):
+        a = [d(p[n])[:, lo:hi] for n in ("x", "dt", "Bm", "Cm")]
+        ys.append(binding.ssm_step(*a, d(p["A_log"]), pool, D=d(p["D"]), z=d(p["z"])[:, lo:hi], dt_bias=d(p["dt_bias"])))
+    torch.cuda.synchronize()
+    ry, mag, skip, rh, hm = ssm_ref(p, [107, 107])
+    pick = lambda a: a.reshape(2, 107, *a.shape[1:])[:, 100:]
+    close("y", torch.cat(ys, 1), pick(ry), 512 * U * pick(mag) + 2.0 ** -20 * (pick(mag) + pick(skip)) + store(dtype, pick(ry)))
+    close("state", pool, rh, 512 * U * hm + 2.0 ** -19 * hm)
+
+
+def test_scan_offsets_past_32_bits():
+    """x, z and y of 4.6 GB each; the last sequence lies past 4 GiB and equals the
+    same sequence alone."""
+    print("scan offsets past 4 GiB", flush=True)
+    HV, V, K, T = 64, 64, 64, 560128
+    p = ssm_inputs(1100, 1, 130, 1, HV, K, V, BF, h0=False)
+    big = {n: torch.zeros((1, T, *p[n].shape[2:]), dtype=BF, device=DEV) for n in ("x", "dt", "Bm", "Cm", "z")}
+    for n in big:
+        big[n][:, -130:] = d(p[n])
+    cu = torch.tensor([0, T - 130, T], dtype=torch.int64, device=DEV)
+    y, ht = binding.ssm_chunk_fwd(big["x"], big["dt"], big["Bm"], big["Cm"], d(p["A_log"]), D=d(p["D"]), z=big["z"],
+                                  dt_bias=d(p["dt_bias"]), cu_seqlens=cu)
+    torch.cuda.synchronize()
+    assert big["x"].numel() * 2 > 1 << 32
+    ry, mag, skip, rh, hm = ssm_ref(p, [130])
+    close("y", y[0, -130:], ry, ssm_bound(BF, ry, mag, skip))
+    close("ht", ht[1:], rh, 512 * U * hm + 2.0 ** -20 * hm)
+    assert not y[:, :-130].any() and not ht[0].any()
+    del big, y
+    torch.cuda.empty_cache()
