@@ -529,9 +529,15 @@ def chunk_fwd_h(k: torch.Tensor, v: torch.Tensor, g: Optional[torch.Tensor] = No
 
 
 # ------------------------------------------------ operators around the scans
+# These are called once a layer and token while a server decodes, where a call is
+# bound by the host: the checks below are the cheap form of _need (which words the
+# failure) and hand back the pointer they looked at.
+_IO_CODES = {torch.bfloat16: GDN_DTYPE_BF16, torch.float32: GDN_DTYPE_F32}
+
+
 def _call(dev: torch.device, fn, *args) -> None:
     """One library call on the tensors' device and its current stream."""
-    if torch.cuda.current_device() != dev.index:
+    if torch._C._cuda_getDevice() != dev.index:
         with torch.cuda.device(dev):
             _check(fn(*args, torch.cuda.current_stream(dev).cuda_stream))
         return
@@ -540,18 +546,27 @@ def _call(dev: torch.device, fn, *args) -> None:
         _check(status)
 
 
+def _want(t: Optional[torch.Tensor], name: str, dtype: torch.dtype, shape: tuple, dev: torch.device) -> Optional[int]:
+    """Pointer of a packed operand (None for None); raises as _need does."""
+    if t is None:
+        return None
+    if t.dtype is not dtype or t.shape != shape or t.device != dev or not t.is_contiguous():
+        _need(t, name, dtype, shape, dev)
+    return t.data_ptr()
+
+
 def _rows(t: torch.Tensor, name: str, dtype: torch.dtype, shape: tuple, dev: torch.device):
     """(pointer, batch stride, token stride) of an operand [B, T, ...] whose
     rows may lie apart (a slice of a wider tensor); what follows B and T must be
     packed."""
-    if t.device != dev:
-        raise ValueError(f"{name} must be on {dev}")
-    if t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.shape != shape:
+    if t.dtype is not dtype or t.shape != shape or t.device != dev:
+        if t.device != dev:
+            raise ValueError(f"{name} must be on {dev}")
+        if t.dtype != dtype:
+            raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     st = t.stride()
-    if (shape[-1] > 1 and st[-1] != 1) or (len(shape) == 4 and shape[2] > 1 and st[2] != shape[3]):
+    if (st[-1] != 1 and shape[-1] > 1) or (len(shape) == 4 and st[2] != shape[3] and shape[2] > 1):
         raise ValueError(f"{name} must be contiguous behind its batch and token dimensions")
     return t.data_ptr(), st[0], st[1]
 
@@ -559,10 +574,18 @@ def _rows(t: torch.Tensor, name: str, dtype: torch.dtype, shape: tuple, dev: tor
 def _index(t: Optional[torch.Tensor], name: str, n: int, dev: torch.device) -> Optional[torch.Tensor]:
     if t is None:
         return None
-    if t.dtype != torch.int32:
+    if t.dtype is not torch.int32:
         t = t.to(torch.int32)
-    _need(t, name, torch.int32, (n,), dev)
+    _want(t, name, torch.int32, (n,), dev)
     return t
+
+
+def _seqs(cu_seqlens: Optional[torch.Tensor], B: int, dev: torch.device):
+    """(number of sequences, pointer of the boundaries)"""
+    if cu_seqlens is None:
+        return B, None
+    _need(cu_seqlens, "cu_seqlens", torch.int64, None, dev)
+    return cu_seqlens.numel() - 1, cu_seqlens.data_ptr()
 
 
 def _cuda(t: torch.Tensor, name: str) -> torch.device:
@@ -572,33 +595,42 @@ def _cuda(t: torch.Tensor, name: str) -> torch.device:
 
 
 def _conv_args(x, weight, bias, activation, sections, state, out):
+    """Checked arguments shared by the two convolutions: the call's leading and
+    trailing arguments, the outputs, and what the callers go on with."""
     if x.dim() != 3 or weight.dim() != 2:
         raise ValueError("x must be [B, T, D] and weight [D, W]")
-    if activation not in (None, "silu"):
+    if activation != "silu" and activation is not None:
         raise ValueError(f"activation must be None or 'silu', got {activation!r}")
-    B, T, D = x.shape
+    shape = x.shape
+    B, T, D = shape
     W = weight.shape[1]
     dev, io = _cuda(x, "x"), x.dtype
-    code = _io_code(io)
-    _need(weight, "weight", io, (D, W), dev)
-    _need(bias, "bias", io, (D,), dev)
+    code = _IO_CODES.get(io)
+    if code is None:
+        _io_code(io)
+    wp, bp = _want(weight, "weight", io, (D, W), dev), _want(bias, "bias", io, (D,), dev)
+    sp = None
     if state is not None:
         if state.dim() != 3:
             raise ValueError("state must be [pool, W - 1, D]")
-        _need(state, "state", io, (state.shape[0], W - 1, D), dev)
-    widths = (D,) if sections is None else tuple(int(n) for n in sections)
-    if not 1 <= len(widths) <= 3 or min(widths) <= 0 or sum(widths) != D:
+        sp = _want(state, "state", io, (state.shape[0], W - 1, D), dev)
+    widths = (D,) if sections is None else tuple(sections)
+    n = len(widths)
+    if not 1 <= n <= 3 or min(widths) <= 0 or sum(widths) != D:
         raise ValueError(f"sections must be one to three positive widths that add up to {D}, got {widths}")
     if out is None:
-        outs = tuple(torch.empty((B, T, n), dtype=io, device=dev) for n in widths)
+        outs = tuple([x.new_empty((B, T, wd)) for wd in widths])
+        ptrs = [o.data_ptr() for o in outs]
     else:
         outs = (out,) if isinstance(out, torch.Tensor) else tuple(out)
-        if len(outs) != len(widths):
-            raise ValueError(f"out must hold {len(widths)} tensors, got {len(outs)}")
-        for i, (o, n) in enumerate(zip(outs, widths)):
-            _need(o, f"out[{i}]", io, (B, T, n), dev)
-    ptrs = [o.data_ptr() for o in outs] + [None] * (3 - len(outs))
-    return B, T, D, W, dev, code, outs, ptrs, widths + (0,) * (3 - len(widths)), _rows(x, "x", io, x.shape, dev)
+        if len(outs) != n:
+            raise ValueError(f"out must hold {n} tensors, got {len(outs)}")
+        ptrs = [_want(o, f"out[{i}]", io, (B, T, wd), dev) for i, (o, wd) in enumerate(zip(outs, widths))]
+    if n < 3:
+        ptrs += [None] * (3 - n)
+        widths += (0,) * (3 - n)
+    head = (*_rows(x, "x", io, shape, dev), wp, bp, 0 if activation is None else 1, *ptrs, *widths)
+    return head, (B, T, D, W, code), outs, sp, B, dev
 
 
 def causal_conv_fwd(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tensor] = None, *,
@@ -620,18 +652,14 @@ def causal_conv_fwd(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.
     continues from it where ``has_state[n]`` is not 0 (None: all sequences are
     new).  ``cu_seqlens`` [N+1] int64 packs N sequences into B = 1; rows behind
     the last boundary are left as they are."""
-    B, T, D, W, dev, code, outs, ptrs, widths, rows = _conv_args(x, weight, bias, activation, sections, state, out)
-    N = B
-    if cu_seqlens is not None:
-        _need(cu_seqlens, "cu_seqlens", torch.int64, None, dev)
-        N = cu_seqlens.numel() - 1
+    head, tail, outs, sp, B, dev = _conv_args(x, weight, bias, activation, sections, state, out)
+    N, cu = _seqs(cu_seqlens, B, dev)
     if state is None and (state_indices is not None or has_state is not None):
         raise ValueError("state_indices and has_state need a state")
     state_indices = _index(state_indices, "state_indices", N, dev)
     has_state = _index(has_state, "has_state", N, dev)
-    _call(dev, lib().gdn_conv_fwd, *rows, weight.data_ptr(), _ptr(bias), 1 if activation else 0, *ptrs, *widths,
-          norm_dim, norm_sections, norm_eps, _ptr(state), _ptr(state_indices), _ptr(has_state),
-          0 if state is None else state.shape[0], _ptr(cu_seqlens), N, B, T, D, W, code)
+    _call(dev, lib().gdn_conv_fwd, *head, norm_dim, norm_sections, norm_eps, sp, _ptr(state_indices), _ptr(has_state),
+          0 if state is None else state.shape[0], cu, N, *tail)
     return outs[0] if sections is None else outs
 
 
@@ -642,32 +670,34 @@ def causal_conv_step(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch
     its pool of states: ``x`` [B,T,D], ``state`` [pool,W-1,D] updated in place
     at the slots ``state_indices`` [B] (None = row b).  A slot outside the pool
     gives zeros and leaves the pool alone.  Returns as ``causal_conv_fwd``."""
-    B, T, D, W, dev, code, outs, ptrs, widths, rows = _conv_args(x, weight, bias, activation, sections, state, out)
+    head, tail, outs, sp, B, dev = _conv_args(x, weight, bias, activation, sections, state, out)
     state_indices = _index(state_indices, "state_indices", B, dev)
-    _call(dev, lib().gdn_conv_step, *rows, weight.data_ptr(), _ptr(bias), 1 if activation else 0, *ptrs, *widths,
-          _ptr(state), _ptr(state_indices), state.shape[0], B, T, D, W, code)
+    _call(dev, lib().gdn_conv_step, *head, sp, _ptr(state_indices), state.shape[0], *tail)
     return outs[0] if sections is None else outs
 
 
-def _ssm_args(x, dt, Bm, Cm, A_log, D, z, dt_bias, out):
+def _ssm_args(x, dt, Bm, Cm, A_log, D, z, dt_bias, softplus, out):
+    """Checked arguments shared by the scan and the step: the call's leading
+    arguments, the output, its sizes, device and io code."""
     if x.dim() != 4 or Bm.dim() != 4:
         raise ValueError("x must be [B, T, HV, V] and Bm, Cm [B, T, Hk, K]")
-    B, T, HV, V = x.shape
+    shape = x.shape
+    B, T, HV, V = shape
     Hk, K = Bm.shape[2:]
     dev, io = _cuda(x, "x"), x.dtype
-    code = _io_code(io)
-    groups = (B, T, Hk, K)
-    rows = (*_rows(x, "x", io, x.shape, dev), *_rows(dt, "dt", io, (B, T, HV), dev),
-            *_rows(Bm, "Bm", io, groups, dev), *_rows(Cm, "Cm", io, groups, dev),
-            *((None, 0, 0) if z is None else _rows(z, "z", io, x.shape, dev)))
-    _need(A_log, "A_log", torch.float32, (HV,), dev)
-    _need(dt_bias, "dt_bias", torch.float32, (HV,), dev)
-    _need(D, "D", torch.float32, (HV,), dev)
+    code = _IO_CODES.get(io)
+    if code is None:
+        _io_code(io)
+    groups, f32, heads = (B, T, Hk, K), torch.float32, (HV,)
+    head = (*_rows(x, "x", io, shape, dev), *_rows(dt, "dt", io, (B, T, HV), dev), *_rows(Bm, "Bm", io, groups, dev),
+            *_rows(Cm, "Cm", io, groups, dev), *((None, 0, 0) if z is None else _rows(z, "z", io, shape, dev)),
+            _want(A_log, "A_log", f32, heads, dev), _want(dt_bias, "dt_bias", f32, heads, dev),
+            _want(D, "D", f32, heads, dev), 1 if softplus else 0)
     if out is None:
-        out = torch.empty((B, T, HV, V), dtype=io, device=dev)
+        out = x.new_empty(shape)
     else:
-        _need(out, "out", io, (B, T, HV, V), dev)
-    return B, T, Hk, HV, K, V, dev, code, rows, (A_log.data_ptr(), _ptr(dt_bias), _ptr(D)), out
+        _want(out, "out", io, shape, dev)
+    return head, out, (B, T, Hk, HV, K, V), dev, code
 
 
 def ssm_workspace_bytes(B: int, T: int, Hk: int, HV: int, K: int, V: int, num_seqs: int, dtype: torch.dtype,
@@ -691,22 +721,21 @@ def ssm_chunk_fwd(x: torch.Tensor, dt: torch.Tensor, Bm: torch.Tensor, Cm: torch
     into B = 1; rows behind the last boundary are left as they are.  ``h0``
     [N,HV,V,K] fp32 is the initial state.  Without softplus dt_t + dt_bias must
     not be negative."""
-    B, T, Hk, HV, K, V, dev, code, rows, params, y = _ssm_args(x, dt, Bm, Cm, A_log, D, z, dt_bias, out)
-    N = B
-    if cu_seqlens is not None:
-        _need(cu_seqlens, "cu_seqlens", torch.int64, None, dev)
-        N = cu_seqlens.numel() - 1
-    _need(h0, "h0", torch.float32, (N, HV, V, K), dev)
+    head, y, sizes, dev, code = _ssm_args(x, dt, Bm, Cm, A_log, D, z, dt_bias, dt_softplus, out)
+    HV, K, V = sizes[3:]
+    N, cu = _seqs(cu_seqlens, sizes[0], dev)
+    hp = _want(h0, "h0", torch.float32, (N, HV, V, K), dev)
     ht = torch.empty((N, HV, V, K), dtype=torch.float32, device=dev) if output_final_state else None
     L = lib()
-    nbytes = int(L.ssm_chunk_fwd_workspace_bytes(B, T, Hk, HV, K, V, N, 0 if cu_seqlens is None else 1, code))
+    nbytes = int(L.ssm_chunk_fwd_workspace_bytes(*sizes, N, 0 if cu_seqlens is None else 1, code))
+    wp = None
     if nbytes:
         if workspace is None or workspace.numel() * workspace.element_size() < nbytes:
             workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
         else:
             _need(workspace, "workspace", None, None, dev)
-    _call(dev, L.ssm_chunk_fwd, *rows, *params, 1 if dt_softplus else 0, _ptr(h0), _ptr(ht), _ptr(cu_seqlens), N,
-          B, T, Hk, HV, K, V, chunk_size, code, y.data_ptr(), workspace.data_ptr() if nbytes else None, nbytes)
+        wp = workspace.data_ptr()
+    _call(dev, L.ssm_chunk_fwd, *head, hp, _ptr(ht), cu, N, *sizes, chunk_size, code, y.data_ptr(), wp, nbytes)
     return y, ht
 
 
@@ -718,28 +747,36 @@ def ssm_step(x: torch.Tensor, dt: torch.Tensor, Bm: torch.Tensor, Cm: torch.Tens
     pool of states: ``state`` [pool,HV,V,K] (fp32 or bf16) is updated in place
     at the slots ``state_indices`` [B] (None = row b).  A slot outside the pool
     gives y = 0 and leaves the pool alone.  Returns y [B,T,HV,V]."""
-    B, T, Hk, HV, K, V, dev, code, rows, params, y = _ssm_args(x, dt, Bm, Cm, A_log, D, z, dt_bias, out)
-    if state.dim() != 4 or state.dtype not in (torch.float32, torch.bfloat16):
+    head, y, sizes, dev, code = _ssm_args(x, dt, Bm, Cm, A_log, D, z, dt_bias, dt_softplus, out)
+    scode = _IO_CODES.get(state.dtype)
+    if state.dim() != 4 or scode is None:
         raise ValueError("state must be [pool, HV, V, K] fp32 or bf16")
-    _need(state, "state", None, (state.shape[0], HV, V, K), dev)
-    state_indices = _index(state_indices, "state_indices", B, dev)
-    _call(dev, lib().ssm_step, *rows, *params, 1 if dt_softplus else 0, state.data_ptr(), _dtype_code(state.dtype),
-          _ptr(state_indices), state.shape[0], B, T, Hk, HV, K, V, code, y.data_ptr())
+    pool = state.shape[0]
+    sp = _want(state, "state", state.dtype, (pool, sizes[3], sizes[5], sizes[4]), dev)
+    state_indices = _index(state_indices, "state_indices", sizes[0], dev)
+    _call(dev, lib().ssm_step, *head, sp, scode, _ptr(state_indices), pool, *sizes, code, y.data_ptr())
     return y
 
 
 def _q8_args(wide, wide_name, q8, scales, src_indices, dst_indices):
-    if wide.dim() != 4 or wide.dtype not in (torch.float32, torch.bfloat16):
+    scode = _IO_CODES.get(wide.dtype)
+    if wide.dim() != 4 or scode is None:
         raise ValueError(f"{wide_name} must be [entries, HV, V, K] fp32 or bf16")
-    entries, HV, V, K = wide.shape
+    shape = wide.shape
+    entries, HV, V, K = shape
     dev = _cuda(wide, wide_name)
-    _need(wide, wide_name, None, None, dev)
+    wp = _want(wide, wide_name, wide.dtype, shape, dev)
     if q8.dim() != 4 or q8.dtype not in (torch.int8, torch.float8_e4m3fn):
         raise ValueError("q8 must be [pool, HV, V, K] int8 or float8_e4m3fn")
     pool = q8.shape[0]
-    _need(q8, "q8", None, (pool, HV, V, K), dev)
-    _need(scales, "scales", torch.float32, (pool, HV, V), dev)
-    return entries, HV, V, K, dev, pool, GDN_Q8_INT8 if q8.dtype == torch.int8 else GDN_Q8_E4M3
+    qp = _want(q8, "q8", q8.dtype, (pool, HV, V, K), dev)
+    sp = _want(scales, "scales", torch.float32, (pool, HV, V), dev)
+    n = entries
+    if src_indices is not None or dst_indices is not None:
+        n = (src_indices if src_indices is not None else dst_indices).numel()
+    src, dst = _index(src_indices, "src_indices", n, dev), _index(dst_indices, "dst_indices", n, dev)
+    form = GDN_Q8_INT8 if q8.dtype is torch.int8 else GDN_Q8_E4M3
+    return dev, (wp, scode, entries), (qp, form, sp, pool), src, dst, (n, HV, K, V)
 
 
 def state_store_q8(src: torch.Tensor, q8: torch.Tensor, scales: torch.Tensor,
@@ -750,13 +787,8 @@ def state_store_q8(src: torch.Tensor, q8: torch.Tensor, scales: torch.Tensor,
     [pool,HV,V] fp32, both in place.  State ``src_indices[i]`` goes to slot
     ``dst_indices[i]`` (None = i); without either every entry of ``src`` is
     stored."""
-    entries, HV, V, K, dev, pool, form = _q8_args(src, "src", q8, scales, src_indices, dst_indices)
-    n = entries
-    if src_indices is not None or dst_indices is not None:
-        n = (src_indices if src_indices is not None else dst_indices).numel()
-    src_indices, dst_indices = _index(src_indices, "src_indices", n, dev), _index(dst_indices, "dst_indices", n, dev)
-    _call(dev, lib().gdn_state_store_q8, src.data_ptr(), _dtype_code(src.dtype), entries, _ptr(src_indices),
-          q8.data_ptr(), form, scales.data_ptr(), pool, _ptr(dst_indices), n, HV, K, V)
+    dev, wide, cache, s, t, dims = _q8_args(src, "src", q8, scales, src_indices, dst_indices)
+    _call(dev, lib().gdn_state_store_q8, *wide, _ptr(s), *cache, _ptr(t), *dims)
 
 
 def state_load_q8(q8: torch.Tensor, scales: torch.Tensor, dst: torch.Tensor,
@@ -766,11 +798,6 @@ def state_load_q8(q8: torch.Tensor, scales: torch.Tensor, dst: torch.Tensor,
     ``dst`` [entries,HV,V,K] (fp32: an initial state; bf16: a decode pool), in
     place: slot ``src_indices[i]`` into entry ``dst_indices[i]`` (None = i);
     without either every entry of ``dst`` is read.  Returns ``dst``."""
-    entries, HV, V, K, dev, pool, form = _q8_args(dst, "dst", q8, scales, src_indices, dst_indices)
-    n = entries
-    if src_indices is not None or dst_indices is not None:
-        n = (src_indices if src_indices is not None else dst_indices).numel()
-    src_indices, dst_indices = _index(src_indices, "src_indices", n, dev), _index(dst_indices, "dst_indices", n, dev)
-    _call(dev, lib().gdn_state_load_q8, q8.data_ptr(), form, scales.data_ptr(), pool, _ptr(src_indices),
-          dst.data_ptr(), _dtype_code(dst.dtype), entries, _ptr(dst_indices), n, HV, K, V)
+    dev, wide, cache, s, t, dims = _q8_args(dst, "dst", q8, scales, src_indices, dst_indices)
+    _call(dev, lib().gdn_state_load_q8, *cache, _ptr(s), *wide, _ptr(t), *dims)
     return dst

@@ -23,7 +23,8 @@ def test_convolution_in_front_of_the_delta_rule():
     sec = (Hk * K, Hk * K, HV * K)
     D, T, N = sum(sec), sum(lens), len(lens)
     proj, w = randn(1, 1, T, D + 64, dtype=BF), randn(2, D, 4, dtype=BF, scale=0.5)
-    g, beta = -torch.rand(1, T, HV, generator=torch.Generator().manual_seed(3)) * 0.2, torch.rand(1, T, HV)
+    gen = torch.Generator().manual_seed(3)
+    g, beta = -torch.rand(1, T, HV, generator=gen) * 0.2, torch.rand(1, T, HV, generator=gen)
     cu = torch.tensor([0, 70, 70, 103], dtype=torch.int64)
     conv_pool, slots = torch.zeros((5, 3, D), dtype=BF, device=DEV), torch.tensor([4, 1, 2], dtype=torch.int32, device=DEV)
     q, k, v = binding.causal_conv_fwd(d(proj)[..., :D], d(w), sections=sec, norm_dim=K, norm_sections=2, norm_eps=EPS,
