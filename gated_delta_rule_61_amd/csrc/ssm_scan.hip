@@ -19,9 +19,11 @@
 // waves owns 16 columns and all K channels, so S^T feeds both products from
 // registers.  The scores C B^T, six 16 x 32 pieces on and under the diagonal, are
 // dealt out to the waves (with tokens as columns they leave the matrix core as the
-// operand of the next product), gated for each head and passed through LDS; the
-// waves without a piece compute the next chunk's gates meanwhile.  Tiles arrive by
-// direct-to-LDS loads into one buffer: 69 KiB a work-group at K = 128, two
+// operand of the next product), gated for each head and passed through LDS.  Gates
+// come in groups: each wave computes those of one chunk and head, a token per lane,
+// for the next 4 or 8 chunks at once (a chain of exponentials and 64-bit sums that
+// one or two waves would have everyone else wait for at every chunk).  Tiles arrive
+// by direct-to-LDS loads into one buffer: 74 KiB a work-group at K = 128, two
 // work-groups a CU (four waves a SIMD), which hide each other's latencies.  Where
 // sequences x heads are too few for the chip, sequences are split: a first
 // launch computes each segment's own final state (from zeros) and log-decay, a
@@ -48,6 +50,8 @@ namespace {
 using tiles::BT;
 using tiles::perm_row;
 using tiles::u32x4;
+
+constexpr int NW = 4;   // waves of a work-group
 
 
 // ------------------------------------------------------------ LDS tiles
@@ -127,7 +131,7 @@ template <int COLS> struct Tile<float, COLS> {
 // row NW RPL i + w RPL on.  Rows past the sequence's end repeat its last row (their
 // weights are 0).  The lane offsets are computed anew for every chunk (the asm sees
 // to it): a few instructions against six registers held over the loop.
-template <typename T, int COLS, int NW>
+template <typename T, int COLS>
 __device__ __forceinline__ void load_tile(const char* src, uint32_t stride, char* tile, int nr, int w, int lane) {
   typedef Tile<T, COLS> TL;
   constexpr int RPL = 64 / TL::units, N = BT / RPL / NW, H = N >= 2 ? N / 2 : 1;   // H: loads of 32 rows
@@ -160,7 +164,7 @@ __device__ __forceinline__ void load_tile(const char* src, uint32_t stride, char
 }
 
 // The same through registers.
-template <typename T, int COLS, int NW>
+template <typename T, int COLS>
 struct StageTile {
   typedef Tile<T, COLS> TL;
   static constexpr int RPL = 64 / TL::units, N = BT / RPL / NW;
@@ -243,24 +247,23 @@ __device__ __forceinline__ double lane_of(double x, int l) {
   return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
 }
 
-// Gates of a chunk and head, in LDS.  Scores of tokens s, t in the same half of
-// the chunk are gated by 2^{G_t - G_s} D_s, those of s in the first and t in the
-// second half by u_t v_s, whose exponents are never positive.
+// Gates of a chunk and head, in LDS.  Scores are gated by 2^{G_t - G_s} D_s.
 template <bool HALF> struct alignas(16) Gates {
   float g[BT];            // G_t
   float e[BT];            // G_s - log2 D_s (bf16 io); D_s (fp32 io)
-  float uv[BT];           // v_s = D_s 2^{G_31 - G_s}, s < 32; u_t = 2^{G_t - G_31}, t >= 32
   float w[BT];            // D_t 2^{G_63 - G_t}
   float eg[BT];           // 2^{G_t}
   float lo[HALF ? 4 : BT];   // what g leaves of G_t (fp32 io)
 };
 
 // ------------------------------------------------------------ y, z and x rows
-// The lane's four consecutive columns of a row.
+// The lane's four or eight consecutive columns of a row.
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x8 __attribute__((ext_vector_type(8)));
 template <int BYTES> struct VecOf;
 template <> struct VecOf<8> { typedef u32x2 type; };
 template <> struct VecOf<16> { typedef u32x4 type; };
+template <> struct VecOf<32> { typedef u32x8 type; };
 
 template <typename T, typename V>
 __device__ __forceinline__ float elem(const V& v, int e) {
@@ -271,11 +274,29 @@ __device__ __forceinline__ float elem(const V& v, int e) {
     return __builtin_bit_cast(float, (uint32_t)v[e]);
   }
 }
-__device__ __forceinline__ void put_vec(bf16_t* p, const float (&y)[4]) {
-  *reinterpret_cast<u32x2*>(p) = u32x2{pack_bf2(y[0], y[1]), pack_bf2(y[2], y[3])};
+// from a tile: one 16-byte unit (or half of one), or two neighbours
+template <typename V>
+__device__ __forceinline__ V lds_vec(const char* p) {
+  if constexpr (sizeof(V) == 32) {
+    const u32x4 a = *reinterpret_cast<const u32x4*>(p), b = *reinterpret_cast<const u32x4*>(p + 16);
+    return V{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
+  } else {
+    return *reinterpret_cast<const V*>(p);
+  }
 }
-__device__ __forceinline__ void put_vec(float* p, const float (&y)[4]) {
-  *reinterpret_cast<f32x4*>(p) = f32x4{y[0], y[1], y[2], y[3]};
+template <int N>
+__device__ __forceinline__ void put_vec(bf16_t* p, const float (&y)[N]) {
+  if constexpr (N == 8) {
+    *reinterpret_cast<u32x4*>(p) =
+        u32x4{pack_bf2(y[0], y[1]), pack_bf2(y[2], y[3]), pack_bf2(y[4], y[5]), pack_bf2(y[6], y[7])};
+  } else {
+    *reinterpret_cast<u32x2*>(p) = u32x2{pack_bf2(y[0], y[1]), pack_bf2(y[2], y[3])};
+  }
+}
+template <int N>
+__device__ __forceinline__ void put_vec(float* p, const float (&y)[N]) {
+#pragma unroll
+  for (int e = 0; e < N; e += 4) *reinterpret_cast<f32x4*>(p + e) = f32x4{y[e], y[e + 1], y[e + 2], y[e + 3]};
 }
 
 // ------------------------------------------------------------ segments
@@ -336,10 +357,10 @@ __device__ __forceinline__ Segment find_segment(const SsmArgs& a, int seg, int s
 // OUT: the last (or only) launch, which writes y and ht; otherwise the first
 // launch of a split call, which writes segment states and log-decays.
 template <typename T, int K, int V, int NH, bool OUT>
-__global__ __launch_bounds__(4 * NH * V, sizeof(T) == 2 ? 4 : 2) void ssm_scan_kernel(
+__global__ __launch_bounds__(64 * NW, sizeof(T) == 2 ? 2 : 1) void ssm_scan_kernel(
     SsmArgs a, int seg, int work, bool split, float* __restrict__ seg_state, double* __restrict__ seg_decay) {
   constexpr int CW = NH * V;            // columns of the work-group
-  constexpr int NW = CW / 16;           // waves
+  constexpr int NB = CW / 16 / NW;      // 16-column blocks of a wave
   constexpr int KB = K / 16, KS = K / 32;
   constexpr bool HALF = sizeof(T) == 2;   // bf16 io
   typedef Tile<T, K> TK;
@@ -349,10 +370,10 @@ __global__ __launch_bounds__(4 * NH * V, sizeof(T) == 2 ? 4 : 2) void ssm_scan_k
   __shared__ __align__(16) char sC[OUT ? TK::bytes : 16];
   __shared__ __align__(16) char sX[TX::bytes];
   __shared__ __align__(16) char sM[OUT ? NH * TM::bytes : 16];
-  __shared__ Gates<HALF> sG[2][NH];
-  __shared__ float sDec[2][NH];
-  __shared__ double sA2[NH], sSum[NH];   // -exp(A_log) log2 e; log2-decay so far
-  __shared__ float sBias[NH];
+  constexpr int GC = NW / NH;           // chunks of a group of gates
+  __shared__ Gates<HALF> sG[GC][NH];
+  __shared__ float sDec[GC][NH];
+  __shared__ double sSum[NW];           // log2-decay of the chunks whose gates the wave computed
 
   const int tid = threadIdx.x, lane = tid & 63;
   const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -384,23 +405,30 @@ __global__ __launch_bounds__(4 * NH * V, sizeof(T) == 2 ? 4 : 2) void ssm_scan_k
   wy.init(Rows{a.y, (long long)a.T * a.HV * V, (long long)a.HV * V}, brow, row0, (long long)hv0 * V, sizeof(T));
   const int count = stop - first;   // tokens of the segment
 
-  const int hw = 16 * w / V;        // the wave's head; its columns 16 w + 0 .. 15
+  const int hw = 16 * NB * w / V;   // the wave's head
   const int hv = hv0 + hw;
 
-  // ---- the starting state: lane (r, q) holds column 16 w + r, channels
-  // 32 k + 8 q + 0 .. 7 in S[2 k] and S[2 k + 1]
-  f32x4 S[KB];
+  // ---- the starting state: lane (r, q) holds column col(b), channels
+  // 32 k + 8 q + 0 .. 7 in S[2 k][b] and S[2 k + 1][b].  Two blocks of a wave are
+  // interleaved so that the lanes' accumulator rows are 8 consecutive columns.
+  auto col = [&](int b) { return NB == 2 ? 32 * w + 8 * (r >> 2) + 4 * b + (r & 3) : 16 * w + r; };
+  f32x4 S[KB][NB];
 #pragma unroll
-  for (int k = 0; k < KB; ++k) S[k] = zero4();
-  auto state_at = [&](long long entry) -> size_t {
-    return (((size_t)entry * a.HV + hv) * V + (16 * w + r - hw * V)) * K + 8 * q;
+  for (int k = 0; k < KB; ++k)
+#pragma unroll
+    for (int b = 0; b < NB; ++b) S[k][b] = zero4();
+  auto state_at = [&](long long entry, int b) -> size_t {
+    return (((size_t)entry * a.HV + hv) * V + (col(b) - hw * V)) * K + 8 * q;
   };
   auto load_state = [&](const float* base, long long entry) {
-    const float* p = base + state_at(entry);
 #pragma unroll
-    for (int k = 0; k < KS; ++k) {
-      S[2 * k] = *reinterpret_cast<const f32x4*>(p + 32 * k);
-      S[2 * k + 1] = *reinterpret_cast<const f32x4*>(p + 32 * k + 4);
+    for (int b = 0; b < NB; ++b) {
+      const float* p = base + state_at(entry, b);
+#pragma unroll
+      for (int k = 0; k < KS; ++k) {
+        S[2 * k][b] = *reinterpret_cast<const f32x4*>(p + 32 * k);
+        S[2 * k + 1][b] = *reinterpret_cast<const f32x4*>(p + 32 * k + 4);
+      }
     }
   };
   if (OUT) {
@@ -411,76 +439,72 @@ __global__ __launch_bounds__(4 * NH * V, sizeof(T) == 2 ? 4 : 2) void ssm_scan_k
   // ---- a chunk's tiles
   auto load_tiles = [&](int t0) {
     const int nr = count - t0;
-    load_tile<T, K, NW>(wb.at(t0), wb.stride, sB, nr, w, lane);
-    load_tile<T, K, NW>(wc.at(t0), wc.stride, sC, nr, w, lane);
-    load_tile<T, CW, NW>(wx.at(t0), wx.stride, sX, nr, w, lane);
+    load_tile<T, K>(wb.at(t0), wb.stride, sB, nr, w, lane);
+    load_tile<T, K>(wc.at(t0), wc.stride, sC, nr, w, lane);
+    load_tile<T, CW>(wx.at(t0), wx.stride, sX, nr, w, lane);
   };
   // The first launch has the registers to hold the next chunk's tiles while it
   // computes; its segments are full, as no sequence ends in them.
-  StageTile<T, K, NW> gB;
-  StageTile<T, CW, NW> gX;
-
-  // ---- gates of a chunk: one of the last NH waves a head, a token per lane
-  const int gh = w - (NW - NH);     // the head whose gates the wave computes (< 0: none)
-  T gdt{};   // raw dt, loaded a chunk ahead
-  auto load_dt = [&](int t0) {
-    const int t = t0 + lane < count ? lane : 0;
-    gdt = *reinterpret_cast<const T*>(wd.at(t0) + (uint32_t)t * wd.stride + gh * (int)sizeof(T));
+  StageTile<T, K> gB;
+  StageTile<T, CW> gX;
+  auto stage = [&](int t0) {
+    gB.load(wb.at(t0), wb.stride, w, lane);
+    gX.load(wx.at(t0), wx.stride, w, lane);
   };
-  if (gh >= 0) {   // written and read by this wave only
-    sA2[gh] = -(double)expf(a.A_log[hv0 + gh]) * 1.4426950408889634;
-    sBias[gh] = a.dt_bias ? a.dt_bias[hv0 + gh] : 0.f;
-    sSum[gh] = 0.0;
-  }
-  auto gates = [&](int t0, int buf) {
-    float d = to_f(gdt) + sBias[gh];
+
+  // ---- gates of the wave's chunk and head of a group, a token per lane
+  const int gc = w / NH, gh = w - gc * NH;
+  T gdt{};   // raw dt, loaded a group ahead
+  auto load_dt = [&](int t0) {   // t0: first token of the group
+    const int t = t0 + BT * gc + lane;
+    gdt = *reinterpret_cast<const T*>(wd.at(0) + (uint64_t)(uint32_t)(t < count ? t : 0) * wd.stride + gh * (int)sizeof(T));
+  };
+  if (lane == 0) sSum[w] = 0.0;   // written and read by this wave only, up to the end
+  auto gates = [&](int t0) {
+    const double A2 = -(double)expf(a.A_log[hv0 + gh]) * 1.4426950408889634;
+    float d = to_f(gdt) + (a.dt_bias ? a.dt_bias[hv0 + gh] : 0.f);
     if (a.softplus) d = d <= 20.f ? log1pf(expf(d)) : d;
-    if (t0 + lane >= count) d = 0.f;
-    double lg = (double)d * sA2[gh];
+    if (t0 + BT * gc + lane >= count) d = 0.f;
+    double lg = (double)d * A2;
     lg = lg < -160.0 ? -160.0 : lg;
     const double G = wave_scan(lg);
-    const double tot = lane_of(G, 63), mid = lane_of(G, 31);
-    Gates<HALF>& g = sG[buf][gh];
+    const double tot = lane_of(G, 63);
+    Gates<HALF>& g = sG[gc][gh];
     const float hi = (float)G;
-    g.g[lane] = hi;
-    if constexpr (HALF) {
-      g.e[lane] = hi - __builtin_amdgcn_logf(d);   // +inf where D is 0
-    } else {
-      g.e[lane] = d;
-      g.lo[lane] = (float)(G - (double)hi);
+    if constexpr (OUT) {
+      g.g[lane] = hi;
+      if constexpr (HALF) {
+        g.e[lane] = hi - __builtin_amdgcn_logf(d);   // +inf where D is 0
+      } else {
+        g.e[lane] = d;
+        g.lo[lane] = (float)(G - (double)hi);
+      }
+      g.eg[lane] = ex2(hi);
     }
-    g.uv[lane] = lane < 32 ? d * ex2((float)(mid - G)) : ex2((float)(G - mid));
     g.w[lane] = d * ex2((float)(tot - G));
-    g.eg[lane] = ex2(hi);
     if (lane == 0) {
-      sDec[buf][gh] = ex2((float)tot);
-      sSum[gh] += tot;
+      sDec[gc][gh] = ex2((float)tot);
+      sSum[w] += tot;
     }
   };
 
   const float skip = OUT && a.D ? a.D[hv] : 0.f;
   const bool fine = !OUT || (last && a.ht != nullptr);   // uniform: the state leaves the kernel
 
-  typedef typename VecOf<4 * sizeof(T)>::type yvec;
+  constexpr int CL = 4 * NB;        // consecutive columns of the lane in y, z and x
+  typedef typename VecOf<CL * sizeof(T)>::type yvec;
 
   if (count > 0) {
-    if constexpr (OUT) {
-      load_tiles(0);
-    } else {
-      gB.load(wb.at(0), wb.stride, w, lane);
-      gX.load(wx.at(0), wx.stride, w, lane);
-    }
-    if (gh >= 0) {
-      load_dt(0);
-      gates(0, 0);
-      if (count > BT) load_dt(BT);
-    }
+    if constexpr (OUT) load_tiles(0);
+    else stage(0);
+    load_dt(0);
   }
 
-  int buf = 0;
-  for (int t0 = 0; t0 < count; t0 += BT, buf ^= 1) {
+  int buf = 0;   // chunk of the group
+  for (int t0 = 0; t0 < count; t0 += BT, buf = buf + 1 < GC ? buf + 1 : 0) {
     const int nr = count - t0 < BT ? count - t0 : BT;
     const bool more = t0 + BT < count;
+    if (buf == 0) gates(t0);
     if constexpr (OUT) {
       // this wave's share of the tiles: behind its loads lie only the four stores
       // of the chunk before (a full one, so none was skipped)
@@ -491,11 +515,9 @@ __global__ __launch_bounds__(4 * NH * V, sizeof(T) == 2 ? 4 : 2) void ssm_scan_k
       gX.put(sX, w, lane);
     }
     tiles::lds_barrier();
+    if (buf == 0 && t0 + GC * BT < count) load_dt(t0 + GC * BT);
     if constexpr (!OUT) {
-      if (more) {
-        gB.load(wb.at(t0 + BT), wb.stride, w, lane);
-        gX.load(wx.at(t0 + BT), wx.stride, w, lane);
-      }
+      if (more) stage(t0 + BT);
     }
     const Gates<HALF>& g = sG[buf][hw];
     // The lane's addresses in the tiles, made anew for every chunk (the asm sees to
@@ -505,101 +527,109 @@ __global__ __launch_bounds__(4 * NH * V, sizeof(T) == 2 ? 4 : 2) void ssm_scan_k
     const int rt = lt & 15, qt = lt >> 4;
     const int k_row = TK::row_at(rt, qt), m_row = TM::row_at(rt, qt);
 
-    f32x4 Y[4];
-    if (more && gh >= 0) {
-      gates(t0 + BT, buf ^ 1);
-      if (t0 + 2 * BT < count) load_dt(t0 + 2 * BT);
-    }
-
+    f32x4 Y[4][NB];
     if constexpr (OUT) {
-      // ---- M, tokens t of block tb by s of half j
-      for (int pc = w; pc < 6; pc += NW) {
-        const int tb = pc < 4 ? pc : pc - 2, j = pc < 4 ? 0 : 1;
-        const int c_at = tiles::blk_rows(tb) * TK::row_bytes, b_at = 32 * j * TK::row_bytes;
-        f32x4 E[2] = {zero4(), zero4()};
+      // ---- M: the wave's three of the 12 blocks of 16 x 16 on and under the
+      // diagonal of 32 x 32 blocks, 3 w + i in the order (tb, sb) = (0, 0), (0, 1),
+      // (1, 0), (1, 1), (2, 0) .. (2, 3), (3, 0) .. (3, 3)
+      f32x4 E[3];
+      int tbs[3], sbs[3];
 #pragma unroll
-        for (int k = 0; k < KS; ++k) {
-          const Frag<T> cf = TK::row_frag(sC, (k_row ^ (k * TK::slab_x)) + c_at, 0);
+      for (int i = 0; i < 3; ++i) {
+        const int n = 3 * w + i;
+        tbs[i] = n < 4 ? n >> 1 : n < 8 ? 2 : 3;
+        sbs[i] = n < 4 ? n & 1 : n & 3;
+        E[i] = zero4();
+      }
 #pragma unroll
-          for (int h = 0; h < 2; ++h) E[h] = mma(TK::row_frag(sB, (k_row ^ (k * TK::slab_x)) + b_at, h), cf, E[h]);
+      for (int k = 0; k < KS; ++k)
+#pragma unroll
+        for (int i = 0; i < 3; ++i) {
+          const int at = k_row ^ (k * TK::slab_x);
+          E[i] = mma(TK::row_frag(sB, at + tiles::blk_rows(sbs[i]) * TK::row_bytes, 0),
+                     TK::row_frag(sC, at + tiles::blk_rows(tbs[i]) * TK::row_bytes, 0), E[i]);
         }
-        const int t = perm_row(0, rt) + tiles::blk_rows(tb);
+#pragma unroll
+      for (int i = 0; i < 3; ++i) {
+        const int t = perm_row(0, rt) + tiles::blk_rows(tbs[i]);
+        const int s0 = 8 * qt + tiles::blk_rows(sbs[i]);
+        const int past = t - s0;   // slots above it are later tokens
 #pragma unroll
         for (int hd = 0; hd < NH; ++hd) {
           const Gates<HALF>& gg = sG[buf][hd];
-          f32x4 M[2];
-          if (j < (tb >> 1)) {
-            const float u = gg.uv[t];
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const f32x4 v = *reinterpret_cast<const f32x4*>(gg.uv + 8 * qt + 4 * h);
-#pragma unroll
-              for (int e = 0; e < 4; ++e) M[h][e] = E[h][e] * (u * v[e]);
-            }
-          } else {
-            const float gt = gg.g[t], gl = HALF ? 0.f : gg.lo[HALF ? 0 : t];
-            const int past = t - 32 * j - 8 * qt;   // slots above it are later tokens
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const int s0 = 32 * j + 8 * qt + 4 * h;
-              const f32x4 ge = *reinterpret_cast<const f32x4*>(gg.e + s0);
-              if constexpr (HALF) {
-#pragma unroll
-                for (int e = 0; e < 4; ++e) M[h][e] = 4 * h + e <= past ? E[h][e] * ex2(gt - ge[e]) : 0.f;
-              } else {
-                const f32x4 gs = *reinterpret_cast<const f32x4*>(gg.g + s0);
-                const f32x4 gsl = *reinterpret_cast<const f32x4*>(gg.lo + s0);
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                  M[h][e] = 4 * h + e <= past ? E[h][e] * ge[e] * ex2((gt - gs[e]) + (gl - gsl[e])) : 0.f;
-              }
-            }
-          }
-          char* mp = sM + hd * TM::bytes + (m_row ^ (j * TM::slab_x)) + tiles::blk_rows(tb) * TM::row_bytes;
+          const float gt = gg.g[t];
+          const f32x4 ge = *reinterpret_cast<const f32x4*>(gg.e + s0);
+          f32x4 M;
           if constexpr (HALF) {
-            *reinterpret_cast<bf16x8*>(mp) = frag_of(M[0], M[1], T()).v;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) M[e] = e <= past ? E[i][e] * ex2(gt - ge[e]) : 0.f;
           } else {
-            *reinterpret_cast<f32x4*>(mp) = M[0];
-            *reinterpret_cast<f32x4*>(mp + 16) = M[1];
+            const float gl = gg.lo[t];
+            const f32x4 gs = *reinterpret_cast<const f32x4*>(gg.g + s0);
+            const f32x4 gsl = *reinterpret_cast<const f32x4*>(gg.lo + s0);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) M[e] = e <= past ? E[i][e] * ge[e] * ex2((gt - gs[e]) + (gl - gsl[e])) : 0.f;
           }
+          // columns s0 .. s0 + 3 of row t
+          char* mp = sM + hd * TM::bytes + (m_row ^ ((sbs[i] >> 1) * TM::slab_x)) + tiles::blk_rows(tbs[i]) * TM::row_bytes +
+                     4 * (int)sizeof(T) * (sbs[i] & 1);
+          const float m[4] = {M[0], M[1], M[2], M[3]};
+          put_vec(reinterpret_cast<T*>(mp), m);
         }
       }
 
       // ---- Y^T = 2^{G_t} S C^T
 #pragma unroll
-      for (int tb = 0; tb < 4; ++tb) Y[tb] = zero4();
+      for (int tb = 0; tb < 4; ++tb)
+#pragma unroll
+        for (int b = 0; b < NB; ++b) Y[tb][b] = zero4();
 #pragma unroll
       for (int k = 0; k < KS; ++k) {
-        const Frag<T> sf = frag_of(S[2 * k], S[2 * k + 1], T());
+        Frag<T> sf[NB];
 #pragma unroll
-        for (int tb = 0; tb < 4; ++tb) Y[tb] = mma(sf, TK::row_frag(sC, k_row ^ (k * TK::slab_x), tb), Y[tb]);
+        for (int b = 0; b < NB; ++b) sf[b] = frag_of(S[2 * k][b], S[2 * k + 1][b], T());
+#pragma unroll
+        for (int tb = 0; tb < 4; ++tb) {
+          const Frag<T> cf = TK::row_frag(sC, k_row ^ (k * TK::slab_x), tb);
+#pragma unroll
+          for (int b = 0; b < NB; ++b) Y[tb][b] = mma(sf[b], cf, Y[tb][b]);
+        }
       }
 #pragma unroll
-      for (int tb = 0; tb < 4; ++tb) Y[tb] *= g.eg[perm_row(0, rt) + tiles::blk_rows(tb)];
+      for (int tb = 0; tb < 4; ++tb) {
+        const float eg = g.eg[perm_row(0, rt) + tiles::blk_rows(tb)];
+#pragma unroll
+        for (int b = 0; b < NB; ++b) Y[tb][b] *= eg;
+      }
       tiles::lds_barrier();   // M is complete
     }
 
     // ---- Y^T += x^T M^T + D x^T
-    const typename TX::Col x_col = TX::col_at(rt, qt, [&](int c) { return 16 * w + 4 * c; });
+    const typename TX::Col x_col = TX::col_at(rt, qt, [&](int c) { return NB == 2 ? 32 * w + 8 * c : 16 * w + 4 * c; });
     const typename TK::Col b_col = TK::col_at(rt, qt, [&](int c) { return 8 * c; });
-    Frag<T> xf[2];
+    const int p0 = 16 * NB * w + CL * qt;   // the lane's columns
+    Frag<T> xf[2][NB];
 #pragma unroll
-    for (int j = 0; j < 2; ++j) xf[j] = TX::col_frag(sX, x_col, j, 0, 0);
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+      for (int b = 0; b < NB; ++b) xf[j][b] = TX::col_frag(sX, x_col, j, 0, b);
     if constexpr (OUT) {
 #pragma unroll
       for (int tb = 0; tb < 4; ++tb) {
 #pragma unroll
-        for (int j = 0; j <= (tb >> 1); ++j)
-          Y[tb] = mma(xf[j], TM::row_frag(sM + hw * TM::bytes, m_row ^ (j * TM::slab_x), tb), Y[tb]);
+        for (int j = 0; j <= (tb >> 1); ++j) {
+          const Frag<T> mf = TM::row_frag(sM + hw * TM::bytes, m_row ^ (j * TM::slab_x), tb);
+#pragma unroll
+          for (int b = 0; b < NB; ++b) Y[tb][b] = mma(xf[j][b], mf, Y[tb][b]);
+        }
       }
       if (a.D) {
-        const int p0 = 16 * w + 4 * qt;   // the lane's four columns
         const int x_row = TX::off(perm_row(0, rt), p0 * (int)sizeof(T) / 16) + (p0 * (int)sizeof(T) & 15);
 #pragma unroll
         for (int tb = 0; tb < 4; ++tb) {
-          const yvec xv = *reinterpret_cast<const yvec*>(sX + x_row + tiles::blk_rows(tb) * TX::row_bytes);
+          const yvec xv = lds_vec<yvec>(sX + x_row + tiles::blk_rows(tb) * TX::row_bytes);
 #pragma unroll
-          for (int e = 0; e < 4; ++e) Y[tb][e] = fmaf(skip, elem<T>(xv, e), Y[tb][e]);
+          for (int e = 0; e < CL; ++e) Y[tb][e >> 2][e & 3] = fmaf(skip, elem<T>(xv, e), Y[tb][e >> 2][e & 3]);
         }
       }
     }
@@ -607,34 +637,38 @@ __global__ __launch_bounds__(4 * NH * V, sizeof(T) == 2 ? 4 : 2) void ssm_scan_k
     // ---- S <- 2^{G_63} S + (B^T) (w o x), in one or three bf16 terms of w o x
     const float dec = sDec[buf][hw];
 #pragma unroll
-    for (int k = 0; k < KB; ++k) S[k] *= dec;
+    for (int k = 0; k < KB; ++k)
+#pragma unroll
+      for (int b = 0; b < NB; ++b) S[k][b] *= dec;
     auto update = [&](auto terms_) {
       constexpr int terms = decltype(terms_)::value;
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        Frag<T> xs[terms];
-        f32x4 p[2];
+        Frag<T> xs[terms][NB];
+        f32x4 v[2];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const f32x4 v = *reinterpret_cast<const f32x4*>(g.w + 32 * j + 8 * qt + 4 * h);
+        for (int h = 0; h < 2; ++h) v[h] = *reinterpret_cast<const f32x4*>(g.w + 32 * j + 8 * qt + 4 * h);
 #pragma unroll
-          for (int e = 0; e < 4; ++e) p[h][e] = xf[j].get(4 * h + e) * v[e];
-        }
+        for (int b = 0; b < NB; ++b) {
+          f32x4 p[2];
 #pragma unroll
-        for (int m = 0; m < terms; ++m) {
-          xs[m] = frag_of(p[0], p[1], T());
-          if (m + 1 < terms) {
+          for (int e = 0; e < 8; ++e) p[e >> 2][e & 3] = xf[j][b].get(e) * v[e >> 2][e & 3];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) p[e >> 2][e & 3] -= xs[m].get(e);
+          for (int m = 0; m < terms; ++m) {
+            xs[m][b] = frag_of(p[0], p[1], T());
+            if (m + 1 < terms) {
+#pragma unroll
+              for (int e = 0; e < 8; ++e) p[e >> 2][e & 3] -= xs[m][b].get(e);
+            }
           }
         }
 #pragma unroll
         for (int k = 0; k < KB; ++k) {
           const Frag<T> bf = TK::col_frag(sB, b_col, j, k >> 1, k & 1);
 #pragma unroll
-          for (int m = 0; m < terms; ++m) S[k] = mma(bf, xs[m], S[k]);
-          // four operands in flight: with all of them the chunk's z would spill
-          if ((k & 3) == 3) __builtin_amdgcn_sched_barrier(0);
+          for (int m = 0; m < terms; ++m)
+#pragma unroll
+            for (int b = 0; b < NB; ++b) S[k][b] = mma(bf, xs[m][b], S[k][b]);
         }
       }
     };
@@ -642,8 +676,8 @@ __global__ __launch_bounds__(4 * NH * V, sizeof(T) == 2 ? 4 : 2) void ssm_scan_k
     else update(tiles::Int<1>{});
     int le = lane;
     asm volatile("" : "+v"(le));
-    const int t_row = perm_row(0, le & 15);            // y and z: rows t_row + blk_rows(tb), four columns
-    const uint32_t col_b = (16 * w + 4 * (le >> 4)) * (uint32_t)sizeof(T);
+    const int t_row = perm_row(0, le & 15);            // y and z: rows t_row + blk_rows(tb)
+    const uint32_t col_b = (16 * NB * w + CL * (le >> 4)) * (uint32_t)sizeof(T);
     yvec zr[4];   // loaded here and not with the tiles: eight registers the products need
     if constexpr (OUT) {
       if (a.z.p) {
@@ -664,12 +698,12 @@ __global__ __launch_bounds__(4 * NH * V, sizeof(T) == 2 ? 4 : 2) void ssm_scan_k
       const char* const yc = wy.at(t0);
 #pragma unroll
       for (int tb = 0; tb < 4; ++tb) {
-        float y[4];
+        float y[CL];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) y[e] = Y[tb][e];
+        for (int e = 0; e < CL; ++e) y[e] = Y[tb][e >> 2][e & 3];
         if (a.z.p) {
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
+          for (int e = 0; e < CL; ++e) {
             const float ze = elem<T>(zr[tb], e);
             y[e] *= ze * __builtin_amdgcn_rcpf(1.0f + __expf(-ze));
           }
@@ -684,14 +718,25 @@ __global__ __launch_bounds__(4 * NH * V, sizeof(T) == 2 ? 4 : 2) void ssm_scan_k
 
   // ---- the final state
   if (OUT ? (last && a.ht != nullptr) : true) {
-    float* p = (OUT ? a.ht : seg_state) + state_at(OUT ? sg.n : slot);
 #pragma unroll
-    for (int k = 0; k < KS; ++k) {
-      *reinterpret_cast<f32x4*>(p + 32 * k) = S[2 * k];
-      *reinterpret_cast<f32x4*>(p + 32 * k + 4) = S[2 * k + 1];
+    for (int b = 0; b < NB; ++b) {
+      float* p = (OUT ? a.ht : seg_state) + state_at(OUT ? sg.n : slot, b);
+#pragma unroll
+      for (int k = 0; k < KS; ++k) {
+        *reinterpret_cast<f32x4*>(p + 32 * k) = S[2 * k][b];
+        *reinterpret_cast<f32x4*>(p + 32 * k + 4) = S[2 * k + 1][b];
+      }
     }
   }
-  if (!OUT && gh >= 0 && lane == 0) seg_decay[(size_t)slot * a.HV + hv0 + gh] = sSum[gh];
+  if constexpr (!OUT) {   // the waves' shares of the log-decay, in order
+    tiles::lds_barrier();
+    if (tid < NH) {
+      double sum = 0.0;
+#pragma unroll
+      for (int i = 0; i < GC; ++i) sum += sSum[i * NH + tid];
+      seg_decay[(size_t)slot * a.HV + hv0 + tid] = sum;
+    }
+  }
 }
 
 // Joins the segments of a split call: each segment's own final state (from zeros)
@@ -757,7 +802,7 @@ __global__ __launch_bounds__(256) void ssm_join_kernel(SsmArgs a, int seg, int s
 template <typename T, int K, int V, int NH>
 hipError_t launch_t(const SsmArgs& a, const SsmPlan& p, hipStream_t s) {
   const int work = p.slots * (a.HV / NH);
-  const dim3 grid((unsigned)((work + 7) / 8 * 8)), block(4 * NH * V);
+  const dim3 grid((unsigned)((work + 7) / 8 * 8)), block(64 * NW);
   float* st = reinterpret_cast<float*>(a.workspace);
   double* dec = p.split ? reinterpret_cast<double*>(reinterpret_cast<char*>(a.workspace) + p.decay_off) : nullptr;
   if (p.split) {
