@@ -169,10 +169,11 @@ struct StageTile {
   typedef Tile<T, COLS> TL;
   static constexpr int RPL = 64 / TL::units, N = BT / RPL / NW;
   u32x4 v[N];
-  __device__ __forceinline__ void load(const char* src, uint32_t stride, int w, int lane) {
+  __device__ __forceinline__ void load(const char* src, uint32_t stride, int w, int lane, int nr) {
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      const int t = (NW * i + w) * RPL + lane / TL::units;
+      int t = (NW * i + w) * RPL + lane / TL::units;
+      if (nr < BT) t = t < nr ? t : nr - 1;   // rows past the end repeat the last one
       v[i] = *reinterpret_cast<const u32x4*>(src + ((uint32_t)t * stride + 16u * (uint32_t)(lane % TL::units)));
     }
   }
@@ -391,7 +392,7 @@ __global__ __launch_bounds__(64 * NW, sizeof(T) == 2 ? 2 : 1) void ssm_scan_kern
   const int first = split ? sg.j * seg : 0;   // first token of the segment in its sequence
   const int stop = split && first + seg < sg.len ? first + seg : sg.len;
   const bool last = stop == sg.len;
-  if (!OUT && last) return;                  // its state is nobody's start
+  if (!OUT && last && !a.ht) return;         // its state is nobody's start, and not asked for
 
   // rows of this sequence, from the segment's first on
   const long long brow = a.cu ? 0 : sg.n;
@@ -444,12 +445,12 @@ __global__ __launch_bounds__(64 * NW, sizeof(T) == 2 ? 2 : 1) void ssm_scan_kern
     load_tile<T, CW>(wx.at(t0), wx.stride, sX, nr, w, lane);
   };
   // The first launch has the registers to hold the next chunk's tiles while it
-  // computes; its segments are full, as no sequence ends in them.
+  // computes.
   StageTile<T, K> gB;
   StageTile<T, CW> gX;
   auto stage = [&](int t0) {
-    gB.load(wb.at(t0), wb.stride, w, lane);
-    gX.load(wx.at(t0), wx.stride, w, lane);
+    gB.load(wb.at(t0), wb.stride, w, lane, count - t0);
+    gX.load(wx.at(t0), wx.stride, w, lane, count - t0);
   };
 
   // ---- gates of the wave's chunk and head of a group, a token per lane
@@ -489,7 +490,9 @@ __global__ __launch_bounds__(64 * NW, sizeof(T) == 2 ? 2 : 1) void ssm_scan_kern
   };
 
   const float skip = OUT && a.D ? a.D[hv] : 0.f;
-  const bool fine = !OUT || (last && a.ht != nullptr);   // uniform: the state leaves the kernel
+  // uniform: the state leaves the kernel (the join has a split call's final state)
+  const bool out_ht = OUT && !split && a.ht != nullptr;
+  const bool fine = !OUT || out_ht;
 
   constexpr int CL = 4 * NB;        // consecutive columns of the lane in y, z and x
   typedef typename VecOf<CL * sizeof(T)>::type yvec;
@@ -717,7 +720,7 @@ __global__ __launch_bounds__(64 * NW, sizeof(T) == 2 ? 2 : 1) void ssm_scan_kern
   }
 
   // ---- the final state
-  if (OUT ? (last && a.ht != nullptr) : true) {
+  if (!OUT || out_ht) {
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
       float* p = (OUT ? a.ht : seg_state) + state_at(OUT ? sg.n : slot, b);
@@ -740,7 +743,8 @@ __global__ __launch_bounds__(64 * NW, sizeof(T) == 2 ? 2 : 1) void ssm_scan_kern
 }
 
 // Joins the segments of a split call: each segment's own final state (from zeros)
-// becomes the state behind it, in place (the last segment of a sequence has none).
+// becomes the state behind it, in place; the last one's is ht (its slot holds
+// nothing where ht is not asked for).
 // A thread owns four elements of a (sequence, head) and walks down its segments,
 // the loads of four in flight together.  Memory-bound: every state once in and out.
 __global__ __launch_bounds__(256) void ssm_join_kernel(SsmArgs a, int seg, int slots, int blocks_per_head,
@@ -771,7 +775,8 @@ __global__ __launch_bounds__(256) void ssm_join_kernel(SsmArgs a, int seg, int s
   }
   // boundaries out of order may claim more slots than there are
   if (segs > slots - slot0) segs = slots - slot0;
-  if (segs < 2) return;
+  if (segs < 1) return;
+  const int own_states = segs - (a.ht ? 0 : 1);
   const size_t VK = (size_t)a.V * a.K, head = (size_t)a.HV * VK;
   const size_t e0 = ((size_t)part * 256 + threadIdx.x) * 4;
   f32x4 st = zero4();
@@ -779,24 +784,25 @@ __global__ __launch_bounds__(256) void ssm_join_kernel(SsmArgs a, int seg, int s
   float* p = seg_state + (size_t)slot0 * head + hv * VK + e0;
   const double* d = seg_decay + (size_t)slot0 * a.HV + hv;
   constexpr int U = 4;
-  for (int j = 0; j < segs - 1; j += U) {
+  for (int j = 0; j < own_states; j += U) {
     f32x4 own[U];
     float f[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int i = j + u < segs - 1 ? j + u : j;
+      const int i = j + u < own_states ? j + u : j;
       own[u] = *reinterpret_cast<const f32x4*>(p + i * head);
       f[u] = ex2((float)d[(size_t)i * a.HV]);
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      if (j + u < segs - 1) {
+      if (j + u < own_states) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) st[e] = fmaf(f[u], st[e], own[u][e]);
-        *reinterpret_cast<f32x4*>(p + (size_t)(j + u) * head) = st;
+        if (j + u < segs - 1) *reinterpret_cast<f32x4*>(p + (size_t)(j + u) * head) = st;
       }
     }
   }
+  if (a.ht) *reinterpret_cast<f32x4*>(a.ht + (size_t)n * head + hv * VK + e0) = st;
 }
 
 template <typename T, int K, int V, int NH>
