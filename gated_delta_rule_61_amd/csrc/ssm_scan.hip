@@ -15,21 +15,22 @@
 // and the fp32 ones for fp32 io.
 //
 // Work is cut into (sequence segment, 64 or 128 value columns).  A work-group walks
-// the chunks of its segment with the state in accumulators: each of its 4 or 8
-// waves owns 16 columns and all K channels, so S^T feeds both products from
-// registers.  The scores C B^T, six 16 x 32 pieces on and under the diagonal, are
-// dealt out to the waves (with tokens as columns they leave the matrix core as the
-// operand of the next product), gated for each head and passed through LDS.  Gates
-// come in groups: each wave computes those of one chunk and head, a token per lane,
-// for the next 4 or 8 chunks at once (a chain of exponentials and 64-bit sums that
-// one or two waves would have everyone else wait for at every chunk).  Tiles arrive
-// by direct-to-LDS loads into one buffer: 74 KiB a work-group at K = 128, two
-// work-groups a CU (four waves a SIMD), which hide each other's latencies.  Where
-// sequences x heads are too few for the chip, sequences are split: a first
-// launch computes each segment's own final state (from zeros) and log-decay, a
-// second one joins them with h0 in order, and the third starts each segment from
-// the state behind the one before.  That reads x and B twice but moves no
-// per-chunk states.
+// the chunks of its segment with the state in accumulators: each of its 4 waves owns
+// 16 or 32 columns and all K channels, so S^T feeds both products from registers.
+// The scores C B^T, 12 blocks of 16 x 16 on and under the diagonal, are dealt out
+// three to a wave (with tokens as columns they leave the matrix core as the operand
+// of the next product), gated for each head and passed through LDS.  Gates come in
+// groups: each wave computes those of one chunk and head, a token per lane, for the
+// next 2 or 4 chunks at once (a chain of exponentials and 64-bit sums that one or
+// two waves would have everyone else wait for at every chunk).  Tiles arrive by
+// direct-to-LDS loads into one buffer: up to 69 KiB a work-group in bf16 at K = 128,
+// two work-groups a CU (two waves a SIMD), which hide each other's latencies.  Eight
+// waves of 16 columns took the same time: more waves to hide latency, but every
+// fragment of B, C and M read from LDS twice as often.  Where sequences x heads are
+// too few for the chip, sequences are split: a first launch computes each segment's
+// own final state (from zeros) and log-decay, a second one joins them with h0 in
+// order, and the third starts each segment from the state behind the one before.
+// That reads x and B twice but moves no per-chunk states.
 //
 // Precision.  Gate sums are taken in 64 bits, over log2-decays held at -160 a
 // token or more (2^-160 is 0 in fp32 already), so that with bf16 io an fp32 G is
@@ -38,6 +39,8 @@
 // segment's state handed on) is formed from the exact products of B with the
 // scaled x as three bf16 terms (24 bits); the state that only feeds this
 // segment's bf16 y takes one term, and S and M are rounded to bf16 as operands.
+
+#include <math.h>
 
 #include "gdn_device.h"
 #include "mixer_launch.h"
@@ -52,7 +55,6 @@ using tiles::perm_row;
 using tiles::u32x4;
 
 constexpr int NW = 4;   // waves of a work-group
-
 
 // ------------------------------------------------------------ LDS tiles
 // A tile of 64 rows (tokens) by COLS in 16-byte units swizzled by row: for bf16 as
@@ -392,7 +394,10 @@ __global__ __launch_bounds__(64 * NW, sizeof(T) == 2 ? 2 : 1) void ssm_scan_kern
   const int first = split ? sg.j * seg : 0;   // first token of the segment in its sequence
   const int stop = split && first + seg < sg.len ? first + seg : sg.len;
   const bool last = stop == sg.len;
-  if (!OUT && last && !a.ht) return;         // its state is nobody's start, and not asked for
+  // a sequence of one segment needs no join; elsewhere the last segment's state is
+  // nobody's start and made only for ht
+  const bool alone = !split || sg.len <= seg;
+  if (!OUT && (alone || (last && !a.ht))) return;
 
   // rows of this sequence, from the segment's first on
   const long long brow = a.cu ? 0 : sg.n;
@@ -490,8 +495,8 @@ __global__ __launch_bounds__(64 * NW, sizeof(T) == 2 ? 2 : 1) void ssm_scan_kern
   };
 
   const float skip = OUT && a.D ? a.D[hv] : 0.f;
-  // uniform: the state leaves the kernel (the join has a split call's final state)
-  const bool out_ht = OUT && !split && a.ht != nullptr;
+  // uniform: the state leaves the kernel (the join writes a split sequence's ht)
+  const bool out_ht = OUT && alone && a.ht != nullptr;
   const bool fine = !OUT || out_ht;
 
   constexpr int CL = 4 * NB;        // consecutive columns of the lane in y, z and x
@@ -509,8 +514,8 @@ __global__ __launch_bounds__(64 * NW, sizeof(T) == 2 ? 2 : 1) void ssm_scan_kern
     const bool more = t0 + BT < count;
     if (buf == 0) gates(t0);
     if constexpr (OUT) {
-      // this wave's share of the tiles: behind its loads lie only the four stores
-      // of the chunk before (a full one, so none was skipped)
+      // this wave's share of the tiles: behind its loads lie only the stores of the
+      // chunk before, four or more (it was a full one, so none was skipped)
       if (t0 > 0) asm volatile("s_waitcnt vmcnt(4)" ::: "memory");
       else asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     } else {
@@ -775,7 +780,7 @@ __global__ __launch_bounds__(256) void ssm_join_kernel(SsmArgs a, int seg, int s
   }
   // boundaries out of order may claim more slots than there are
   if (segs > slots - slot0) segs = slots - slot0;
-  if (segs < 1) return;
+  if (segs < 2) return;
   const int own_states = segs - (a.ht ? 0 : 1);
   const size_t VK = (size_t)a.V * a.K, head = (size_t)a.HV * VK;
   const size_t e0 = ((size_t)part * 256 + threadIdx.x) * 4;
@@ -840,11 +845,19 @@ SsmPlan ssm_plan(int nb, int T, int Hk, int HV, int K, int V, int N, bool varlen
   p.nh = V == 64 && (HV / Hk) % 2 == 0 ? 2 : 1;
   const long long tokens = (long long)nb * T;
   const long long tiles = HV / p.nh;
-  // work-groups resident on 256 CUs: two a CU, one with fp32 tiles
+  // One round of work-groups on 256 CUs: two a CU, one with fp32 tiles (bf16, one
+  // prompt of 8192 tokens x 64 heads: 256 work-groups 168 us, 512 135, 768 166, 1024
+  // 152).  But no segment shorter than 2 sqrt(T) tokens: halving the segments
+  // saves two launches the half of their chunks and costs the join as many steps
+  // (2048 tokens x 32 heads: 64-token segments 44 us, 128 39, 256 51; 700 x 16
+  // heads: 64 27, 128 32, 256 44).
   const long long want = bf16 ? 512 : 256;
   long long seg = ((tokens * tiles + want - 1) / want + 63) / 64 * 64;
-  seg = seg < 256 ? 256 : seg;
-  if (seg >= T) seg = ((long long)T + 63) / 64 * 64;
+  const long long least = ((long long)(2.0 * sqrt((double)T)) + 63) / 64 * 64;
+  seg = seg < least ? least : seg;
+  // nor two chunks alone: they cost less than two more launches (128 tokens x 8 heads
+  // 17.9 us in one launch, 20.8 in three; 192 tokens 24.1 and 21.4)
+  if (seg >= T || T <= 128) seg = ((long long)T + 63) / 64 * 64;
   p.split = seg < T;
   p.seg = seg > 64 ? (int)seg : 64;
   p.slots = !p.split ? N : (varlen ? (int)(tokens / seg) + N : N * (int)((T + seg - 1) / seg));

@@ -56,7 +56,7 @@ def test_scan(case):
 @pytest.mark.parametrize("dtype", [BF, F32])
 @pytest.mark.parametrize("lens", [(1, 2200), [1500, 0, 40, 700, 1], (2, 1025)])
 def test_scan_split_into_segments(dtype, lens):
-    """Few sequences and heads: segments of 256 tokens and their join."""
+    """Few sequences and heads: short segments and their join."""
     dense = isinstance(lens, tuple)
     B, T = lens if dense else (1, sum(lens))
     seqs = [T] * B if dense else lens
