@@ -309,49 +309,73 @@ struct Segment {
   int len;               // tokens of the sequence
 };
 
-// Which segment slot `slot` is.  Same result in every lane.
-__device__ __forceinline__ Segment find_segment(const SsmArgs& a, int seg, int slot, int lane) {
-  Segment g;
-  if (!a.cu) {
-    const int per = a.T > seg ? (a.T + seg - 1) / seg : 1;
-    g.n = slot / per;
-    g.j = slot - g.n * per;
-    g.start = 0;
-    g.len = a.T;
-    return g;
-  }
-  g.n = -1;
-  g.j = 0;
-  g.start = 0;
-  g.len = 0;
-  int run = 0;
-  for (int base = 0; base < a.N; base += 64) {
-    const int n = base + lane;
-    long long b0 = 0, b1 = 0;
+// Packed sequences are looked at 64 at a time, one a lane.
+struct Packed {
+  long long b0;    // first token
+  int len, segs;   // tokens and segments, 0 behind the last sequence
+  int incl, all;   // segments up to and with this one, of all 64
+  __device__ __forceinline__ Packed(const SsmArgs& a, int seg, int n, int lane) {
+    long long b1 = 0;
+    b0 = 0;
     if (n < a.N) {
       b0 = a.cu[n];
       b1 = a.cu[n + 1];
       b0 = b0 < 0 ? 0 : (b0 > a.T ? a.T : b0);
       b1 = b1 < b0 ? b0 : (b1 > a.T ? a.T : b1);
     }
-    const int len = (int)(b1 - b0);
-    const int segs = n < a.N ? (len > seg ? (len + seg - 1) / seg : 1) : 0;
-    int incl = segs;
+    len = (int)(b1 - b0);
+    segs = n < a.N ? (len > seg ? (len + seg - 1) / seg : 1) : 0;
+    incl = segs;
 #pragma unroll
     for (int off = 1; off < 64; off <<= 1) {
       const int y = __shfl_up(incl, off, 64);
       if (lane >= off) incl += y;
     }
-    const int all = __builtin_amdgcn_readlane(incl, 63);
-    if (slot < run + all) {
-      const int l = __ffsll((unsigned long long)__ballot(incl > slot - run)) - 1;
+    all = __builtin_amdgcn_readlane(incl, 63);
+  }
+};
+
+// The segment and head tile of work-group `wg` of 8 XCDs: the tiles of a segment
+// (which share B and C) run next to each other on one XCD, and every XCD gets an
+// equal run of the segments that there are (packed sequences seldom fill the slots
+// the host counts).  Same result in every lane; n < 0: none.
+__device__ __forceinline__ Segment find_segment(const SsmArgs& a, int seg, int slots, int tiles, int wg, int lane,
+                                                int& slot, int& tile) {
+  Segment g;
+  g.n = -1;
+  g.j = 0;
+  g.start = 0;
+  g.len = 0;
+  Packed p(a, seg, a.cu ? lane : a.N, lane);
+  if (a.cu) {
+    int used = p.all;
+    for (int base = 64; base < a.N; base += 64) used += Packed(a, seg, base + lane, lane).all;
+    slots = used < slots ? used : slots;   // boundaries out of order may claim more
+  }
+  const int work = slots * tiles, per_xcd = (work + 7) / 8;
+  const int id = (wg & 7) * per_xcd + (wg >> 3);
+  slot = id / tiles;
+  tile = id - slot * tiles;
+  if ((wg >> 3) >= per_xcd || id >= work) return g;
+  if (!a.cu) {
+    const int per = a.T > seg ? (a.T + seg - 1) / seg : 1;
+    g.n = slot / per;
+    g.j = slot - g.n * per;
+    g.len = a.T;
+    return g;
+  }
+  int run = 0;
+  for (int base = 0; base < a.N; base += 64) {
+    if (base > 0) p = Packed(a, seg, base + lane, lane);
+    if (slot < run + p.all) {
+      const int l = __ffsll((unsigned long long)__ballot(p.incl > slot - run)) - 1;
       g.n = base + l;
-      g.j = slot - run - (__builtin_amdgcn_readlane(incl, l) - __builtin_amdgcn_readlane(segs, l));
-      g.start = __builtin_amdgcn_readlane((int)b0, l);
-      g.len = __builtin_amdgcn_readlane(len, l);
+      g.j = slot - run - (__builtin_amdgcn_readlane(p.incl, l) - __builtin_amdgcn_readlane(p.segs, l));
+      g.start = __builtin_amdgcn_readlane((int)p.b0, l);
+      g.len = __builtin_amdgcn_readlane(p.len, l);
       return g;
     }
-    run += all;
+    run += p.all;
   }
   return g;
 }
@@ -361,7 +385,7 @@ __device__ __forceinline__ Segment find_segment(const SsmArgs& a, int seg, int s
 // launch of a split call, which writes segment states and log-decays.
 template <typename T, int K, int V, int NH, bool OUT>
 __global__ __launch_bounds__(64 * NW, sizeof(T) == 2 ? 2 : 1) void ssm_scan_kernel(
-    SsmArgs a, int seg, int work, bool split, float* __restrict__ seg_state, double* __restrict__ seg_decay) {
+    SsmArgs a, int seg, int slots, bool split, float* __restrict__ seg_state, double* __restrict__ seg_decay) {
   constexpr int CW = NH * V;            // columns of the work-group
   constexpr int NB = CW / 16 / NW;      // 16-column blocks of a wave
   constexpr int KB = K / 16, KS = K / 32;
@@ -381,16 +405,11 @@ __global__ __launch_bounds__(64 * NW, sizeof(T) == 2 ? 2 : 1) void ssm_scan_kern
   const int tid = threadIdx.x, lane = tid & 63;
   const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int r = lane & 15, q = lane >> 4;
-  // heads of one segment (which share B and C) run next to each other on one XCD
-  const int ht_count = a.HV / NH;
-  const int per_xcd = (work + 7) / 8;
-  const int id = (blockIdx.x & 7) * per_xcd + (blockIdx.x >> 3);
-  if ((int)(blockIdx.x >> 3) >= per_xcd || id >= work) return;
-  const int slot = id / ht_count;
-  const int hv0 = (id - slot * ht_count) * NH;
-  const int hk = hv0 / (a.HV / a.Hk);
-  const Segment sg = find_segment(a, seg, slot, lane);
+  int slot, tile;
+  const Segment sg = find_segment(a, seg, slots, a.HV / NH, blockIdx.x, lane, slot, tile);
   if (sg.n < 0) return;
+  const int hv0 = tile * NH;
+  const int hk = hv0 / (a.HV / a.Hk);
   const int first = split ? sg.j * seg : 0;   // first token of the segment in its sequence
   const int stop = split && first + seg < sg.len ? first + seg : sg.len;
   const bool last = stop == sg.len;
@@ -817,7 +836,7 @@ hipError_t launch_t(const SsmArgs& a, const SsmPlan& p, hipStream_t s) {
   float* st = reinterpret_cast<float*>(a.workspace);
   double* dec = p.split ? reinterpret_cast<double*>(reinterpret_cast<char*>(a.workspace) + p.decay_off) : nullptr;
   if (p.split) {
-    hipLaunchKernelGGL((ssm_scan_kernel<T, K, V, NH, false>), grid, block, 0, s, a, p.seg, work, true, st, dec);
+    hipLaunchKernelGGL((ssm_scan_kernel<T, K, V, NH, false>), grid, block, 0, s, a, p.seg, p.slots, true, st, dec);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     constexpr int per_head = K * V / 1024;
@@ -826,7 +845,7 @@ hipError_t launch_t(const SsmArgs& a, const SsmPlan& p, hipStream_t s) {
     e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
-  hipLaunchKernelGGL((ssm_scan_kernel<T, K, V, NH, true>), grid, block, 0, s, a, p.seg, work, p.split, st, dec);
+  hipLaunchKernelGGL((ssm_scan_kernel<T, K, V, NH, true>), grid, block, 0, s, a, p.seg, p.slots, p.split, st, dec);
   return hipGetLastError();
 }
 
@@ -852,7 +871,9 @@ SsmPlan ssm_plan(int nb, int T, int Hk, int HV, int K, int V, int N, bool varlen
   // (2048 tokens x 32 heads: 64-token segments 44 us, 128 39, 256 51; 700 x 16
   // heads: 64 27, 128 32, 256 44).
   const long long want = bf16 ? 512 : 256;
-  long long seg = ((tokens * tiles + want - 1) / want + 63) / 64 * 64;
+  // packed sequences end in half a segment on average, up to half of the work-groups
+  const long long tails = !varlen ? 0 : tiles * N < want ? tiles * N / 2 : want / 2;
+  long long seg = ((tokens * tiles + want - tails - 1) / (want - tails) + 63) / 64 * 64;
   const long long least = ((long long)(2.0 * sqrt((double)T)) + 63) / 64 * 64;
   seg = seg < least ? least : seg;
   // nor two chunks alone: they cost less than two more launches (128 tokens x 8 heads
