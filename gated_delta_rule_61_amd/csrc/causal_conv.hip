@@ -16,6 +16,11 @@
 // and its loads and stores are whole 1 KiB pieces of a row.  Nothing is shared
 // between waves: no LDS, no barriers.  Sums are fp32; the result is rounded
 // once to the io type.
+//
+// Measured: 16001 packed tokens x 8192 channels, bf16, with norms: 524 MB in 107 us,
+// 4.9 TB/s (a large copy 5.1); 2048 tokens 16 us; 100 tokens 5.0 us.
+// Steps: 256 rows x 4 tokens x 8192 channels 59 MB in 11 us, 5.2 TB/s (rows and
+// states partly from the caches); one row 3 us, a launch.
 
 #include "gdn_device.h"
 #include "mixer_launch.h"
@@ -358,7 +363,13 @@ hipError_t launch_conv_fwd(const ConvArgs& a, hipStream_t s) {
   const long long total = (long long)a.B * a.T;
   if (a.N == 0 || (total == 0 && !a.state)) return hipSuccess;
   const int cblocks = (a.D / 8 + 63) / 64;
-  const int run = 16;
+  // Longer runs repeat less (the taps, and the W - 1 rows in front), shorter ones
+  // give the chip more waves: the shortest of 4, 8, 16 tokens that makes at most 4096
+  // (8192 channels, W = 4, runs of 4 / 8 / 16: 100 tokens 5.0 / 6.4 / 9.4 us, 700
+  // 8.5 / 9.3 / 11.3, 2048 17.1 / 16.2 / 17.4, 4096 28.7 / 28.1 / 26.4; of 32 and 64
+  // for 16001 tokens 110 and 111, of 16 109).
+  const long long units = total * cblocks;
+  const int run = units <= 4 * 4096 ? 4 : units <= 8 * 4096 ? 8 : 16;
   const int runs = total > 0 ? (int)((total + run - 1) / run) : 1;
   if (a.bf16) {
     if (a.W == 2) return fwd_w<bf16_t, 2>(a, s, run, runs, cblocks);

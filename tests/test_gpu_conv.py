@@ -23,6 +23,8 @@ CASES = [
     (F32, 3, [15, 1, 1, 15, 64, 7], (24, 40), 0, 0, False, False, True, 0),
     (BF, 4, (4, 16), (256, 256, 512), 128, 3, True, False, True, 0),
     (BF, 4, [3] * 300 + [29], (16,), 0, 0, True, False, True, 0),        # more sequences than a wave has lanes
+    (BF, 4, [7, 15990, 0, 1, 2, 4003], (64, 8), 64, 1, True, True, True, 0),     # enough tokens for runs of 8
+    (F32, 4, [16, 33000, 15, 1, 0, 3, 7002, 1], (24,), 0, 0, True, False, True, 8),   # ... of 16
 ]
 
 
