@@ -17,7 +17,12 @@
 // Memory-bound: 5 bytes per element with fp32 states (3 with bf16), ~10 VALU
 // operations.  8 elements of a row per lane (two 16-byte accesses of fp32, 8
 // bytes of codes), K / 8 lanes a row, the row's maximum by 3 or 4 in-row DPP
-// steps; two rows per lane, all loads issued before the first maximum.
+// steps; large stores take two rows a lane, whose loads are issued before the first
+// maximum.
+//
+// Measured, states of 32 heads of 128 x 128: 128 fp32 ones stored as e4m3 60 us, 5.6
+// TB/s (int8 64 us; a large copy 5.1 TB/s); 256 read back into bf16 78 us, 5.2 TB/s;
+// one stored 3 us, one read 2.5.
 
 #include "gdn_device.h"
 #include "mixer_launch.h"
@@ -25,8 +30,6 @@
 namespace gdn {
 
 namespace {
-
-constexpr int ROWS = 2;   // rows per lane
 
 template <typename T> struct Wide8;
 template <> struct Wide8<bf16_t> {
@@ -93,7 +96,8 @@ __device__ __forceinline__ Place place(const StateQ8Args& a, long long row, long
   return p;
 }
 
-template <typename T, int K, bool E4M3>
+// ROWS: rows of a lane
+template <typename T, int K, bool E4M3, int ROWS>
 __global__ __launch_bounds__(256) void state_store_q8_kernel(StateQ8Args a, long long rows, long long per) {
   constexpr int LPR = K / 8, RPB = 256 / LPR;
   const int cl = threadIdx.x % LPR;
@@ -152,59 +156,57 @@ __global__ __launch_bounds__(256) void state_store_q8_kernel(StateQ8Args a, long
   }
 }
 
+// One row a lane: with nothing between a load and its store, more waves hide the
+// latency better than two rows do (256 states into bf16 78 us, two rows 85).
 template <typename T, int K, bool E4M3>
 __global__ __launch_bounds__(256) void state_load_q8_kernel(StateQ8Args a, long long rows, long long per) {
   constexpr int LPR = K / 8, RPB = 256 / LPR;
   const int cl = threadIdx.x % LPR;
-  const long long row0 = (long long)blockIdx.x * (RPB * ROWS) + threadIdx.x / LPR;
   typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
-  Place p[ROWS];
-  u32x2 raw[ROWS];
-  float scale[ROWS];
+  const Place p = place<false>(a, (long long)blockIdx.x * RPB + threadIdx.x / LPR, rows, per);
+  if (!p.ok) return;
+  const u32x2 raw = __builtin_nontemporal_load(
+      reinterpret_cast<const u32x2*>(reinterpret_cast<const uint8_t*>(a.q8) + p.code * K + 8 * cl));
+  const float scale = a.scales[p.code];
+  float f[8];
 #pragma unroll
-  for (int i = 0; i < ROWS; ++i) {
-    p[i] = place<false>(a, row0 + i * RPB, rows, per);
-    if (p[i].ok) {
-      raw[i] = __builtin_nontemporal_load(
-          reinterpret_cast<const u32x2*>(reinterpret_cast<const uint8_t*>(a.q8) + p[i].code * K + 8 * cl));
-      scale[i] = a.scales[p[i].code];
+  for (int h = 0; h < 2; ++h) {
+    if constexpr (E4M3) {
+      const f32x2_t lo = __builtin_amdgcn_cvt_pk_f32_fp8((int)raw[h], false);
+      const f32x2_t hi = __builtin_amdgcn_cvt_pk_f32_fp8((int)raw[h], true);
+      f[4 * h] = lo[0]; f[4 * h + 1] = lo[1]; f[4 * h + 2] = hi[0]; f[4 * h + 3] = hi[1];
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) f[4 * h + e] = (float)(int8_t)(raw[h] >> (8 * e));
     }
   }
 #pragma unroll
-  for (int i = 0; i < ROWS; ++i) {
-    if (!p[i].ok) continue;
-    float f[8];
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      if constexpr (E4M3) {
-        const f32x2_t lo = __builtin_amdgcn_cvt_pk_f32_fp8((int)raw[i][h], false);
-        const f32x2_t hi = __builtin_amdgcn_cvt_pk_f32_fp8((int)raw[i][h], true);
-        f[4 * h] = lo[0]; f[4 * h + 1] = lo[1]; f[4 * h + 2] = hi[0]; f[4 * h + 3] = hi[1];
-      } else {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) f[4 * h + e] = (float)(int8_t)(raw[i][h] >> (8 * e));
-      }
-    }
-#pragma unroll
-    for (int e = 0; e < 8; ++e) f[e] *= scale[i];
-    T* dst = reinterpret_cast<T*>(a.wide) + p[i].wide + 8 * cl;
-    if constexpr (sizeof(T) == 2) {
-      typedef uint32_t u4 __attribute__((ext_vector_type(4)));
-      store_nt16(dst, u4{pack_bf2(f[0], f[1]), pack_bf2(f[2], f[3]), pack_bf2(f[4], f[5]), pack_bf2(f[6], f[7])});
-    } else {
-      store_nt16(dst, f32x4{f[0], f[1], f[2], f[3]});
-      store_nt16(dst + 4, f32x4{f[4], f[5], f[6], f[7]});
-    }
+  for (int e = 0; e < 8; ++e) f[e] *= scale;
+  T* dst = reinterpret_cast<T*>(a.wide) + p.wide + 8 * cl;
+  if constexpr (sizeof(T) == 2) {
+    typedef uint32_t u4 __attribute__((ext_vector_type(4)));
+    store_nt16(dst, u4{pack_bf2(f[0], f[1]), pack_bf2(f[2], f[3]), pack_bf2(f[4], f[5]), pack_bf2(f[6], f[7])});
+  } else {
+    store_nt16(dst, f32x4{f[0], f[1], f[2], f[3]});
+    store_nt16(dst + 4, f32x4{f[4], f[5], f[6], f[7]});
   }
 }
 
 template <bool STORE, typename T, int K, bool E4M3>
 hipError_t launch(const StateQ8Args& a, hipStream_t s) {
   const long long per = (long long)a.HV * a.V, rows = per * a.N;
-  constexpr int PER_BLOCK = 256 / (K / 8) * ROWS;
-  const dim3 grid((unsigned)((rows + PER_BLOCK - 1) / PER_BLOCK)), block(256);
-  if constexpr (STORE) hipLaunchKernelGGL((state_store_q8_kernel<T, K, E4M3>), grid, block, 0, s, a, rows, per);
-  else hipLaunchKernelGGL((state_load_q8_kernel<T, K, E4M3>), grid, block, 0, s, a, rows, per);
+  // Stores of fewer than 2^17 rows take one row a lane (states of 4096 rows of 128
+  // fp32 as int8, one / two rows: 1 state 3.0 / 4.1 us, 16 10.6 / 10.7, 32
+  // 19.4 / 19.2, 128 66 / 64).
+  const int per_lane = STORE && rows >= (1 << 17) ? 2 : 1;
+  const int per_block = 256 / (K / 8) * per_lane;
+  const dim3 grid((unsigned)((rows + per_block - 1) / per_block)), block(256);
+  if constexpr (STORE) {
+    if (per_lane == 2) hipLaunchKernelGGL((state_store_q8_kernel<T, K, E4M3, 2>), grid, block, 0, s, a, rows, per);
+    else hipLaunchKernelGGL((state_store_q8_kernel<T, K, E4M3, 1>), grid, block, 0, s, a, rows, per);
+  } else {
+    hipLaunchKernelGGL((state_load_q8_kernel<T, K, E4M3>), grid, block, 0, s, a, rows, per);
+  }
   return hipGetLastError();
 }
 

@@ -54,6 +54,24 @@ def test_store_bit_exact(form, dtype, HV, V, K):
     assert np.array_equal(_num(q8), codes)
 
 
+@pytest.mark.parametrize("form,dtype,K", [("int8", BF, 64), ("int8", torch.float32, 128), ("e4m3", torch.float32, 64),
+                                          ("e4m3", BF, 128)])
+def test_store_of_many_rows(form, dtype, K):
+    """Over 2^17 rows, the last work-group's half empty; read back."""
+    print(f"q8 store many {form} {dtype} K={K}", flush=True)
+    x = _states(K, 1, 3, 43693, K, dtype)
+    q8, sc = _store(x, form, 2, dst=torch.tensor([1], dtype=torch.int32, device=DEV))
+    codes, scale = oracle.quantise_state(f64(x), form)
+    assert np.array_equal(sc[1:].cpu().double().numpy(), scale, equal_nan=True)
+    assert np.array_equal(_num(q8[1:]), codes)
+    assert torch.all(q8[0].float() == 3) and torch.all(sc[0] == 7)
+    out = binding.state_load_q8(q8, sc, torch.zeros(x.shape, dtype=dtype, device=DEV),
+                                torch.tensor([1], dtype=torch.int32, device=DEV))
+    want = (q8[1:].float() * sc[1:, ..., None]).to(dtype)
+    torch.cuda.synchronize()
+    assert torch.equal(bits(out), bits(want))
+
+
 @pytest.mark.parametrize("form", ["int8", "e4m3"])
 @pytest.mark.parametrize("dtype", [torch.float32, BF])
 def test_load_is_code_times_scale(form, dtype):
