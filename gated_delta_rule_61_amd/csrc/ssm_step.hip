@@ -14,6 +14,9 @@
 // K / 8 lanes of a DPP row hold whole state rows: the C product is a 3- or
 // 4-step in-row reduction, without LDS or barriers, and every state access is
 // 16 bytes a lane.  The state's loads are issued before everything else.
+//
+// Measured, 32 heads of 128 x 128: 256 rows over an fp32 pool 1.08 GB in 214 us,
+// 5.1 TB/s (a large copy's rate); over a bf16 pool 112 us, 4.9 TB/s; one row 3.6 us.
 
 #include "gdn_device.h"
 #include "mixer_launch.h"
@@ -190,9 +193,10 @@ template <typename T, typename S, int K, int TT>
 hipError_t launch_t(const SsmArgs& a, hipStream_t s) {
   const long long pairs = (long long)a.nb * a.HV;
   const int threads = a.V * (K / 8) / 8;   // 64, 128 or 256 threads hold a state
-  // fewer (row, head) pairs than fill the 256 CUs, or a small state:
-  // work-groups of one wave
-  if (pairs < 512 || threads < 256) {
+  // fewer (row, head) pairs than CUs, or a small state: work-groups of one wave
+  // (fp32 pool, 32 heads of 128 x 128, one wave / four: 1 row 3.6 / 4.3 us, 4 rows
+  // 5.0 / 5.3, 8 rows 7.5 / 7.0, 256 rows 216 / 214)
+  if (pairs < 256 || threads < 256) {
     const int parts = threads / 64;
     hipLaunchKernelGGL((ssm_step_kernel<T, S, K, TT, 64>), dim3((unsigned)(pairs * parts)), dim3(64), 0, s, a, parts);
   } else {
