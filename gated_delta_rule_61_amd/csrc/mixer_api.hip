@@ -127,6 +127,9 @@ int check_ssm_rows(const SsmArgs& a) {
   return GDN_OK;
 }
 
+// A launch has fewer than 2^32 threads.
+bool too_many(long long groups, int threads) { return groups >= (1LL << 32) / threads; }
+
 int done(hipError_t e) {
   if (e != hipSuccess) return fail(GDN_ERR_LAUNCH, "HIP launch failed: %s", hipGetErrorString(e));
   return ok();
@@ -168,7 +171,7 @@ int gdn_conv_fwd(const void* x, long long x_batch, long long x_token, const void
   if (a.N == 0 || (!tokens && !state)) return ok();
   if (int st = check_conv_ptrs(a, tokens)) return st;
   if (int st = check_rows("x", a.x, B, T, 8)) return st;
-  if (((long long)B * T / 16 + 1) * (D / 512 + 1) >= (1LL << 31))
+  if (too_many(((long long)B * T / 16 + 4096) * (D / 512 + 1), 64))   // runs of 16 tokens, or 4096 shorter ones
     return fail(GDN_ERR_UNSUPPORTED, "too many tokens x channels for one launch");
   return timed(GDN_STAGE_CONV, stream, [&](hipStream_t s) { return launch_conv_fwd(a, s); });
 }
@@ -193,7 +196,7 @@ int gdn_conv_step(const void* x, long long x_batch, long long x_token, const voi
   if (!state) return fail(GDN_ERR_INVALID_ARGUMENT, "state is required");
   if (int st = check_conv_ptrs(a, true)) return st;
   if (int st = check_rows("x", a.x, B, T, 8)) return st;
-  if ((long long)B * (D / 512 + 1) >= (1LL << 31))
+  if (too_many((long long)B * (D / 512 + 1), 64))
     return fail(GDN_ERR_UNSUPPORTED, "too many rows x channels for one launch");
   return timed(GDN_STAGE_CONV, stream, [&](hipStream_t s) { return launch_conv_step(a, s); });
 }
@@ -203,7 +206,7 @@ size_t ssm_chunk_fwd_workspace_bytes(int B, int T, int Hk, int HV, int K, int V,
   if (B < 0 || T < 0 || Hk <= 0 || HV <= 0 || HV % Hk || K <= 0 || V <= 0 || num_seqs < 0) return 0;
   if (dtype != GDN_DTYPE_F32 && dtype != GDN_DTYPE_BF16) return 0;
   const int N = varlen ? num_seqs : B;
-  if (N == 0) return 0;
+  if (N == 0 || too_many((long long)N * HV, 256)) return 0;
   return ssm_plan(B, T, Hk, HV, K, V, N, varlen != 0, dtype == GDN_DTYPE_BF16).bytes;
 }
 
@@ -232,9 +235,9 @@ int ssm_chunk_fwd(const void* x, long long x_batch, long long x_token, const voi
   }
   if (!aligned16(h0) || !aligned16(ht))
     return fail(GDN_ERR_INVALID_ARGUMENT, "h0 and ht must be 16-byte aligned");
-  // one launch indexes (segment, head) pairs, at most one segment per 64 tokens, or 16 blocks of a
-  // (sequence, head) with 32-bit integers
-  if (((long long)B * T / 64 + a.N + 8) * HV >= (1LL << 31) || (long long)a.N * HV * 16 >= (1LL << 31))
+  // one launch has a work-group per (segment, head), at most one segment per 64 tokens
+  // and one more for each sequence
+  if (too_many(((long long)B * T / 64 + a.N + 8) * HV, 256))
     return fail(GDN_ERR_UNSUPPORTED, "too many sequences x heads for one launch (N=%d HV=%d)", a.N, HV);
   const SsmPlan p = ssm_plan(B, T, Hk, HV, K, V, a.N, cu_seqlens != nullptr, a.bf16 != 0);
   if (p.bytes > 0) {
@@ -274,8 +277,7 @@ int ssm_step(const void* x, long long x_batch, long long x_token, const void* dt
   if (int st = check_ssm_rows(a)) return st;
   if (!aligned16(state)) return fail(GDN_ERR_INVALID_ARGUMENT, "state must be 16-byte aligned");
   if ((long long)pool * HV * V * K >= (1LL << 40)) return fail(GDN_ERR_UNSUPPORTED, "state pool too large");
-  // up to four work-groups per (batch row, head), indexed with 32-bit integers
-  if ((long long)B * HV * 4 >= (1LL << 31))
+  if (too_many((long long)B * HV, 256))
     return fail(GDN_ERR_UNSUPPORTED, "too many batch rows x heads for one launch (B=%d HV=%d)", B, HV);
   return timed(GDN_STAGE_SSM_STEP, stream, [&](hipStream_t s) { return launch_ssm_step(a, s); });
 }
@@ -302,7 +304,7 @@ static int state_q8(bool store, void* wide, int state_dtype, int entries, void* 
   if (!wide || !q8 || !scales) return fail(GDN_ERR_INVALID_ARGUMENT, "the states, q8 and scales are required");
   if (!aligned16(wide) || !aligned16(q8) || !aligned16(scales))
     return fail(GDN_ERR_INVALID_ARGUMENT, "tensor pointers must be 16-byte aligned");
-  if ((long long)N * HV * V / 16 >= (1LL << 31) - 1)
+  if (too_many((long long)N * HV * V / (2048 / K) + 1, 256))   // K / 8 threads a row
     return fail(GDN_ERR_UNSUPPORTED, "too many state rows for one launch");
   StateQ8Args a{};
   a.wide = wide; a.wide_bf16 = state_dtype == GDN_DTYPE_BF16; a.wide_n = entries;

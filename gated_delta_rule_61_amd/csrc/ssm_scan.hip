@@ -878,7 +878,9 @@ SsmPlan ssm_plan(int nb, int T, int Hk, int HV, int K, int V, int N, bool varlen
   seg = seg < least ? least : seg;
   // nor two chunks alone: they cost less than two more launches (128 tokens x 8 heads
   // 17.9 us in one launch, 20.8 in three; 192 tokens 24.1 and 21.4)
-  if (seg >= T || T <= 128) seg = ((long long)T + 63) / 64 * 64;
+  // nor so many sequences that the join's launch would have 2^32 threads
+  const bool join = (long long)N * HV * (K * V / 1024) < (1 << 24);
+  if (seg >= T || T <= 128 || !join) seg = ((long long)T + 63) / 64 * 64;
   p.split = seg < T;
   p.seg = seg > 64 ? (int)seg : 64;
   p.slots = !p.split ? N : (varlen ? (int)(tokens / seg) + N : N * (int)((T + seg - 1) / seg));

@@ -510,8 +510,9 @@ int gdn_conv_step(const void* x, long long x_batch, long long x_token, const voi
  * start) as matrix products: an infinity or NaN in x makes its channel's outputs
  * NaN from the beginning of its chunk on, where the recurrence would from its
  * token on; one in dt, Bm or Cm reaches the tokens the recurrence says.
- * Allocates nothing;
- * asynchronous on `stream`.
+ * Fewer than 2^24 (64-token chunk or sequence, head) pairs.  Calls that share a
+ * workspace (captured graphs too) must not run at the same time.  Allocates
+ * nothing; asynchronous on `stream`.
  */
 size_t ssm_chunk_fwd_workspace_bytes(int B, int T, int Hk, int HV, int K, int V, int num_seqs, int varlen,
                                      int dtype);
@@ -558,15 +559,16 @@ int ssm_step(const void* x, long long x_batch, long long x_token,
  *   scales       [pool, HV, V]      fp32
  *
  * int8: scale = max(max|row| * r, 2^-126) in fp32, r = 1/127 rounded to fp32;
- * code = row / scale rounded to nearest, ties to even.  e4m3: scale = the smallest power of two of
- * at least 2^-126 with max|row| / scale <= 448; code = row / scale rounded to
- * nearest, ties to even.  Reading: code * scale, rounded to the state's type.
+ * code = row / scale rounded to nearest, ties to even.  e4m3: scale = the
+ * smallest power of two of at least 2^-126 with max|row| / scale <= 448;
+ * code = row / scale rounded to nearest, ties to even.  Reading: code * scale,
+ * rounded to the state's type.
  * A row with an infinity or a NaN gets the scale NaN and codes 0 and reads back
  * as NaN.  An index outside its array skips that state (nothing is written).
  * Two states naming the same target race (undefined result).
  *
- * Supported: K in {64, 128}; 16-byte aligned tensors.  Allocates nothing;
- * asynchronous on `stream`.
+ * Supported: K in {64, 128}; N * HV * V * K / 8 below 2^32; 16-byte aligned
+ * tensors.  Allocates nothing; asynchronous on `stream`.
  */
 enum { GDN_Q8_INT8 = 0, GDN_Q8_E4M3 = 1 };
 int gdn_state_store_q8(const void* src, int state_dtype, int entries, const int32_t* src_indices,
@@ -596,7 +598,7 @@ enum {
   GDN_STAGE_BWD_DH = 5,        /* backward state-gradient scan                 */
   GDN_STAGE_FWD_H = 6,         /* forward decay-only state scan                */
   GDN_STAGE_CONV = 7,          /* causal convolution, prompts and single tokens */
-  GDN_STAGE_SSM_SCAN = 8,      /* selective state-space scan (both launches)   */
+  GDN_STAGE_SSM_SCAN = 8,      /* selective state-space scan (all launches)    */
   GDN_STAGE_SSM_STEP = 9,      /* selective state-space step                   */
   GDN_STAGE_STATE_Q8 = 10,     /* 8-bit state cache, store and load            */
   GDN_STAGE_COUNT = 11

@@ -60,6 +60,7 @@ def _conv(L, step=False, **kw):
     (dict(has=FAKE), 1, b"needs a state"),
     (dict(st=FAKE, pool=1), 1, b"pool >= N"),
     (dict(B=1 << 13, T=1 << 13), 2, b"too large"),
+    (dict(B=1, T=1 << 24, D=1 << 16, w0=1 << 16, xt=1 << 16), 2, b"one launch"),
 ])
 def test_conv_fwd_refuses(L, kw, status, msg):
     assert _conv(L, **kw) == status
@@ -73,6 +74,7 @@ def test_conv_fwd_refuses(L, kw, status, msg):
     (dict(st=None), 1, b"state"),
     (dict(W=7), 2, b"taps"),
     (dict(xb=12), 2, b"strides"),
+    (dict(B=1 << 20, idx=FAKE, D=1 << 16, w0=1 << 16), 2, b"one launch"),
 ])
 def test_conv_step_refuses(L, kw, status, msg):
     assert _conv(L, step=True, **kw) == status
@@ -129,6 +131,7 @@ def test_ssm_refuses(L, step, kw, status, msg):
     (dict(T=8192, B=1, ws=FAKE + 16), 1, b"256-byte"),
     (dict(B=1 << 13, T=1 << 13), 2, b"too large"),
     (dict(B=1, T=1, cu=FAKE, n=1 << 28, HV=8), 2, b"one launch"),
+    (dict(B=1, T=1, cu=FAKE, n=1 << 21, HV=8), 2, b"one launch"),
 ])
 def test_ssm_chunk_fwd_refuses(L, kw, status, msg):
     assert _ssm(L, **kw) == status
@@ -142,6 +145,7 @@ def test_ssm_chunk_fwd_refuses(L, kw, status, msg):
     (dict(sdt=4), 1, b"state dtype"),
     (dict(st=FAKE + 8), 1, b"aligned"),
     (dict(pool=-1), 1, b"sizes"),
+    (dict(B=1 << 21, HV=8, idx=FAKE), 2, b"one launch"),
 ])
 def test_ssm_step_refuses(L, kw, status, msg):
     assert _ssm(L, True, **kw) == status
@@ -161,6 +165,7 @@ def test_ssm_step_refuses(L, kw, status, msg):
     (dict(scales=FAKE + 4), 1, b"aligned"),
     (dict(pool=1 << 30), 2, b"too large"),
     (dict(N=1 << 24, pool=1 << 14, entries=1 << 14, src=FAKE, dst=FAKE, HV=128, K=64), 2, b"too"),
+    (dict(N=1 << 22, src=FAKE, dst=FAKE), 2, b"one launch"),
 ])
 def test_state_q8_refuses(L, store, kw, status, msg):
     a = dict(wide=FAKE, sdt=0, entries=4, src=None, q8=FAKE, form=0, scales=FAKE, pool=4, dst=None, N=2, HV=2, K=64, V=64)
@@ -215,3 +220,10 @@ def test_binding_wants_gpu_tensors_and_shapes():
         binding.state_store_q8(torch.zeros(2, 1, 64, 64), q8, sc)
     with pytest.raises(ValueError, match="fp32 or bf16"):
         binding.state_load_q8(q8, sc, torch.zeros((2, 1, 64, 64), dtype=torch.float16))
+
+
+def test_sequences_past_the_joins_launch_are_not_split(L):
+    """Packed prompts of a length that is split, but too many of them to join."""
+    few = L.ssm_chunk_fwd_workspace_bytes(1, 1 << 20, 8, 64, 128, 64, 1000, 1, 1)
+    assert few > 0
+    assert L.ssm_chunk_fwd_workspace_bytes(1, 1 << 20, 8, 64, 128, 64, 1 << 16, 1, 1) == 0
