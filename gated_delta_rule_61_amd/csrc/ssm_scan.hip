@@ -32,6 +32,19 @@
 // order, and the third starts each segment from the state behind the one before.
 // That reads x and B twice but moves no per-chunk states.
 //
+// Measured (bf16, K = 128).  One prompt of 8192 tokens x 64 heads of 64, gated:
+// launches of 44 + 13 + 80 us, 128 us a call for 209 MB (41 us at a large copy's 5.1
+// TB/s).  Eight packed prompts of 5003 tokens, 32 heads of 128, initial and final
+// states: 34 + 12 + 52 us, 88 a call, 137 MB (27 us).  The same 8192 tokens as 16
+// prompts, one launch: 72 us.  fp32, 4096 tokens x 32 heads of 64: 121 us.  What
+// bounds it is no one unit: of the last launch's cycles the vector ALU issues in 37 %,
+// LDS in 17 % with 10 % more of bank conflicts (the transposing reads and the stores
+// of M take one half of every 16-byte unit at a time, so half of the banks), the
+// matrix cores work in 12 %, between three barriers a chunk.  Left out one at a time,
+// scores save 14 us of 72, the tile loads, the state update and the stores 10 each,
+// silu 6, the gates 3; twice the waves or prefetched tiles save nothing.  In the first
+// launch two of the three terms of the state update cost 10 us of 44.
+//
 // Precision.  Gate sums are taken in 64 bits, over log2-decays held at -160 a
 // token or more (2^-160 is 0 in fp32 already), so that with bf16 io an fp32 G is
 // good to 10240 x 2^-24 = 2^-10.7 at worst; with fp32 io G is an fp32 pair, whose
@@ -547,6 +560,9 @@ __global__ __launch_bounds__(64 * NW, sizeof(T) == 2 ? 2 : 1) void ssm_scan_kern
       if (more) stage(t0 + BT);
     }
     const Gates<HALF>& g = sG[buf][hw];
+    // the products go before the other work-group's loads and stores on the SIMD (packed
+    // prompts above 91 -> 88 us, the long one 135 -> 133)
+    __builtin_amdgcn_s_setprio(1);
     // The lane's addresses in the tiles, made anew for every chunk (the asm sees to
     // it): held over the loop they would spill.
     int lt = lane;
@@ -716,6 +732,7 @@ __global__ __launch_bounds__(64 * NW, sizeof(T) == 2 ? 2 : 1) void ssm_scan_kern
         }
       }
     }
+    __builtin_amdgcn_s_setprio(0);
     tiles::lds_barrier();   // everyone is done with the tiles
     if (OUT && more) load_tiles(t0 + BT);
     asm volatile("" ::: "memory");   // the stores stay behind the loads
@@ -770,7 +787,10 @@ __global__ __launch_bounds__(64 * NW, sizeof(T) == 2 ? 2 : 1) void ssm_scan_kern
 // becomes the state behind it, in place; the last one's is ht (its slot holds
 // nothing where ht is not asked for).
 // A thread owns four elements of a (sequence, head) and walks down its segments,
-// the loads of four in flight together.  Memory-bound: every state once in and out.
+// the loads of four in flight together.  Memory-bound: every state once in and out
+// (16 segments x 64 heads of 64 x 128: 67 MB in 13 us, 5.2 TB/s).  Each segment's
+// work-groups joining what lies before them instead, in the last launch, took 5 us
+// off 5 segments a prompt and added 37 to 16 (their reads are serial and repeated).
 __global__ __launch_bounds__(256) void ssm_join_kernel(SsmArgs a, int seg, int slots, int blocks_per_head,
                                                        float* __restrict__ seg_state,
                                                        const double* __restrict__ seg_decay) {
