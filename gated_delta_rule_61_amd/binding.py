@@ -651,7 +651,8 @@ def causal_conv_fwd(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.
     (None = n) of each sequence gets the last W - 1 rows, and the sequence
     continues from it where ``has_state[n]`` is not 0 (None: all sequences are
     new).  ``cu_seqlens`` [N+1] int64 packs N sequences into B = 1; rows behind
-    the last boundary are left as they are."""
+    the last boundary are left as they are.  ``out``: the tensors to write, which
+    must not overlap ``x``."""
     head, tail, outs, sp, B, dev = _conv_args(x, weight, bias, activation, sections, state, out)
     N, cu = _seqs(cu_seqlens, B, dev)
     if state is None and (state_indices is not None or has_state is not None):
@@ -720,7 +721,8 @@ def ssm_chunk_fwd(x: torch.Tensor, dt: torch.Tensor, Bm: torch.Tensor, Cm: torch
     ht [N,HV,V,K] fp32 or None).  ``cu_seqlens`` [N+1] int64 packs N sequences
     into B = 1; rows behind the last boundary are left as they are.  ``h0``
     [N,HV,V,K] fp32 is the initial state.  Without softplus dt_t + dt_bias must
-    not be negative."""
+    not be negative.  ``out`` must not overlap an input.  A ``workspace`` (of
+    ``ssm_workspace_bytes``; else allocated) serves one call at a time."""
     head, y, sizes, dev, code = _ssm_args(x, dt, Bm, Cm, A_log, D, z, dt_bias, dt_softplus, out)
     HV, K, V = sizes[3:]
     N, cu = _seqs(cu_seqlens, sizes[0], dev)

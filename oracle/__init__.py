@@ -22,6 +22,9 @@ Sources (cited by page and function in each module):
   state (gate, q/k normalisation, per-token state update) and its state pool,
   into which a prefill's final state is handed over.
 
+The operators around the scans (``mixer``) follow their definitions in
+``include/gdn61.h``.
+
 Pins: every function here is checked in ``tests/test_oracle_*.py`` against
 something other than itself (brute-force products of the per-token transition
 matrices, an independently written chunked form, closed forms of degenerate
