@@ -68,6 +68,34 @@ def test_scan_split_into_segments(dtype, lens):
 
 
 @pytest.mark.parametrize("dtype", [BF, F32])
+def test_split_scan_reads_no_workspace_it_has_not_written(dtype):
+    """Long sequences among more short ones than a wave has lanes, over a
+    workspace of NaN; without ht the last segments' states are nobody's."""
+    print(f"scan split over a poisoned workspace {dtype}", flush=True)
+    seqs = [3] * 70 + [300] + [5, 0] * 35 + [200, 0, 129, 64]
+    T, Hk, HV, K, V = sum(seqs), 1, 2, 128, 64
+    p = ssm_inputs(140, 1, T, Hk, HV, K, V, dtype, N=len(seqs))
+    cu = torch.tensor(edges(seqs), dtype=torch.int64, device=DEV)
+    nbytes = binding.ssm_workspace_bytes(1, T, Hk, HV, K, V, len(seqs), dtype, varlen=True)
+    assert nbytes > 0
+    ry, mag, skip, rh, hm = ssm_ref(p, seqs, True)
+    bound = ssm_bound(dtype, ry, mag, skip)
+    runs = []
+    for fill, ht_too in ((0xFF, True), (0, True), (0xFF, False)):
+        ws = torch.full((nbytes + 64,), fill, dtype=torch.uint8, device=DEV)
+        y, ht = _run(p, cu_seqlens=cu, workspace=ws[:nbytes], output_final_state=ht_too)
+        torch.cuda.synchronize()
+        close("y", y.reshape(-1, *y.shape[2:]), ry, bound)
+        assert torch.all(ws[nbytes:] == fill)
+        if ht_too:
+            close("ht", ht, rh, 512 * U * hm + 2.0 ** -20 * hm)
+            runs.append([y, ht])
+        else:
+            assert ht is None
+    same(*runs, "0xFF against zeroed workspace")
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
 @pytest.mark.parametrize("fast", [6.0, 25.0, -12.0])
 def test_scan_strong_and_weak_decays(dtype, fast):
     """Step sizes of several units (every factor underflows within a chunk or a
