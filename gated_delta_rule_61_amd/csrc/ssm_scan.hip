@@ -105,6 +105,10 @@ template <int COLS> struct Tile<bf16_t, COLS> {
     f.v = __builtin_bit_cast(bf16x8, u32x4{lo.x, lo.y, hi.x, hi.y});
     return f;
   }
+  // ... of the 16 columns 16 n further, where col(i) = 4 i
+  static __device__ __forceinline__ Frag<bf16_t> col_blk(const char* t, const Col& c, int j, int n) {
+    return col_frag(t, Col{c.at ^ (n * (slab_x / 2))}, j, 0, 0);
+  }
 };
 template <int COLS> struct Tile<float, COLS> {
   static constexpr int row_bytes = COLS * 4, bytes = BT * row_bytes, slab_x = 128;
@@ -138,6 +142,13 @@ template <int COLS> struct Tile<float, COLS> {
 #pragma unroll
     for (int e = 0; e < 8; ++e)
       f.v[e] = *reinterpret_cast<const float*>(t + (c.at[e & 3] ^ (k * slab_x)) + (32 * j + 4 * (e >> 2)) * row_bytes + 16 * half);
+    return f;
+  }
+  static __device__ __forceinline__ Frag<float> col_blk(const char* t, const Col& c, int j, int n) {
+    Frag<float> f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      f.v[e] = *reinterpret_cast<const float*>(t + (c.at[e & 3] ^ (n * (slab_x / 2))) + (32 * j + 4 * (e >> 2)) * row_bytes);
     return f;
   }
 };
@@ -178,6 +189,18 @@ __device__ __forceinline__ void load_tile(const char* src, uint32_t stride, char
   }
 }
 
+// Global memory by pointers whose origin the compiler cannot see (below): as flat
+// accesses they would count among the LDS ones, and every wait for an LDS read would
+// wait for them.
+template <typename V>
+__device__ __forceinline__ V gload(const char* p) {
+  return *(const __attribute__((address_space(1))) V*)p;
+}
+template <typename V>
+__device__ __forceinline__ void gstore(char* p, V v) {
+  *(__attribute__((address_space(1))) V*)p = v;
+}
+
 // The same through registers.
 template <typename T, int COLS>
 struct StageTile {
@@ -189,7 +212,7 @@ struct StageTile {
     for (int i = 0; i < N; ++i) {
       int t = (NW * i + w) * RPL + lane / TL::units;
       if (nr < BT) t = t < nr ? t : nr - 1;   // rows past the end repeat the last one
-      v[i] = *reinterpret_cast<const u32x4*>(src + ((uint32_t)t * stride + 16u * (uint32_t)(lane % TL::units)));
+      v[i] = gload<u32x4>(src + ((uint32_t)t * stride + 16u * (uint32_t)(lane % TL::units)));
     }
   }
   __device__ __forceinline__ void put(char* tile, int w, int lane) const {
@@ -275,7 +298,7 @@ template <bool HALF> struct alignas(16) Gates {
 // ------------------------------------------------------------ y, z and x rows
 // The lane's four or eight consecutive columns of a row.
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
-typedef uint32_t u32x8 __attribute__((ext_vector_type(8)));
+typedef uint32_t u32x8 __attribute__((ext_vector_type(8), aligned(16)));
 template <int BYTES> struct VecOf;
 template <> struct VecOf<8> { typedef u32x2 type; };
 template <> struct VecOf<16> { typedef u32x4 type; };
@@ -301,18 +324,16 @@ __device__ __forceinline__ V lds_vec(const char* p) {
   }
 }
 template <int N>
-__device__ __forceinline__ void put_vec(bf16_t* p, const float (&y)[N]) {
-  if constexpr (N == 8) {
-    *reinterpret_cast<u32x4*>(p) =
-        u32x4{pack_bf2(y[0], y[1]), pack_bf2(y[2], y[3]), pack_bf2(y[4], y[5]), pack_bf2(y[6], y[7])};
-  } else {
-    *reinterpret_cast<u32x2*>(p) = u32x2{pack_bf2(y[0], y[1]), pack_bf2(y[2], y[3])};
-  }
+__device__ __forceinline__ typename VecOf<2 * N>::type pack(const float (&y)[N], bf16_t) {
+  if constexpr (N == 8) return u32x4{pack_bf2(y[0], y[1]), pack_bf2(y[2], y[3]), pack_bf2(y[4], y[5]), pack_bf2(y[6], y[7])};
+  else return u32x2{pack_bf2(y[0], y[1]), pack_bf2(y[2], y[3])};
 }
 template <int N>
-__device__ __forceinline__ void put_vec(float* p, const float (&y)[N]) {
+__device__ __forceinline__ typename VecOf<4 * N>::type pack(const float (&y)[N], float) {
+  typename VecOf<4 * N>::type v;
 #pragma unroll
-  for (int e = 0; e < N; e += 4) *reinterpret_cast<f32x4*>(p + e) = f32x4{y[e], y[e + 1], y[e + 2], y[e + 3]};
+  for (int e = 0; e < N; ++e) v[e] = __builtin_bit_cast(uint32_t, y[e]);
+  return v;
 }
 
 // ------------------------------------------------------------ segments
@@ -448,15 +469,17 @@ __global__ __launch_bounds__(64 * NW, sizeof(T) == 2 ? 2 : 1) void ssm_scan_kern
 
   // ---- the starting state: lane (r, q) holds column col(b), channels
   // 32 k + 8 q + 0 .. 7 in S[2 k][b] and S[2 k + 1][b].  Two blocks of a wave are
-  // interleaved so that the lanes' accumulator rows are 8 consecutive columns.
-  auto col = [&](int b) { return NB == 2 ? 32 * w + 8 * (r >> 2) + 4 * b + (r & 3) : 16 * w + r; };
+  // interleaved so that the lanes' accumulator rows are 8 consecutive columns.  The
+  // first launch, which makes no y, has its blocks of 16 columns and channels in order:
+  // transposing reads then take whole units, without bank conflicts.
+  auto col = [&](int b) { return OUT && NB == 2 ? 32 * w + 8 * (r >> 2) + 4 * b + (r & 3) : 16 * (NB * w + b) + r; };
   f32x4 S[KB][NB];
 #pragma unroll
   for (int k = 0; k < KB; ++k)
 #pragma unroll
     for (int b = 0; b < NB; ++b) S[k][b] = zero4();
   auto state_at = [&](long long entry, int b) -> size_t {
-    return (((size_t)entry * a.HV + hv) * V + (col(b) - hw * V)) * K + 8 * q;
+    return (((size_t)entry * a.HV + hv) * V + (col(b) - hw * V)) * K + (OUT ? 8 : 4) * q;
   };
   auto load_state = [&](const float* base, long long entry) {
 #pragma unroll
@@ -495,7 +518,7 @@ __global__ __launch_bounds__(64 * NW, sizeof(T) == 2 ? 2 : 1) void ssm_scan_kern
   T gdt{};   // raw dt, loaded a group ahead
   auto load_dt = [&](int t0) {   // t0: first token of the group
     const int t = t0 + BT * gc + lane;
-    gdt = *reinterpret_cast<const T*>(wd.at(0) + (uint64_t)(uint32_t)(t < count ? t : 0) * wd.stride + gh * (int)sizeof(T));
+    gdt = gload<T>(wd.at(0) + (uint64_t)(uint32_t)(t < count ? t : 0) * wd.stride + gh * (int)sizeof(T));
   };
   if (lane == 0) sSum[w] = 0.0;   // written and read by this wave only, up to the end
   auto gates = [&](int t0) {
@@ -534,30 +557,40 @@ __global__ __launch_bounds__(64 * NW, sizeof(T) == 2 ? 2 : 1) void ssm_scan_kern
   constexpr int CL = 4 * NB;        // consecutive columns of the lane in y, z and x
   typedef typename VecOf<CL * sizeof(T)>::type yvec;
 
+  // The first launch walks its chunks backwards: with the decays of the chunks behind
+  // in the weights, the state only grows and is not scaled 64 registers at a time.
+  const int chunks = (count + BT - 1) / BT;
+  const int c0 = OUT ? 0 : chunks - 1;
+  float after = 1.f;   // decay of the chunks behind
   if (count > 0) {
     if constexpr (OUT) load_tiles(0);
-    else stage(0);
-    load_dt(0);
+    else stage(c0 * BT);
+    load_dt(c0 / GC * GC * BT);
   }
 
-  int buf = 0;   // chunk of the group
-  for (int t0 = 0; t0 < count; t0 += BT, buf = buf + 1 < GC ? buf + 1 : 0) {
+  for (int i = 0; i < chunks; ++i) {
+    const int t0 = (OUT ? i : c0 - i) * BT;
+    const int buf = (t0 / BT) % GC;   // chunk of the group
     const int nr = count - t0 < BT ? count - t0 : BT;
-    const bool more = t0 + BT < count;
-    if (buf == 0) gates(t0);
+    const bool more = i + 1 < chunks;
+    const bool enter = OUT ? buf == 0 : i == 0 || buf == GC - 1;
+    if (enter) gates(t0 - buf * BT);
     if constexpr (OUT) {
       // this wave's share of the tiles: behind its loads lie only the stores of the
       // chunk before, four or more (it was a full one, so none was skipped)
-      if (t0 > 0) asm volatile("s_waitcnt vmcnt(4)" ::: "memory");
+      if (i > 0) asm volatile("s_waitcnt vmcnt(4)" ::: "memory");
       else asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     } else {
       gB.put(sB, w, lane);
       gX.put(sX, w, lane);
     }
     tiles::lds_barrier();
-    if (buf == 0 && t0 + GC * BT < count) load_dt(t0 + GC * BT);
-    if constexpr (!OUT) {
-      if (more) stage(t0 + BT);
+    if constexpr (OUT) {
+      if (enter && t0 + GC * BT < count) load_dt(t0 + GC * BT);
+    } else {
+      const int before = t0 - (buf + GC) * BT;
+      if (enter && before >= 0) load_dt(before);
+      if (more) stage(t0 - BT);
     }
     const Gates<HALF>& g = sG[buf][hw];
     // the products go before the other work-group's loads and stores on the SIMD (packed
@@ -617,7 +650,7 @@ __global__ __launch_bounds__(64 * NW, sizeof(T) == 2 ? 2 : 1) void ssm_scan_kern
           char* mp = sM + hd * TM::bytes + (m_row ^ ((sbs[i] >> 1) * TM::slab_x)) + tiles::blk_rows(tbs[i]) * TM::row_bytes +
                      4 * (int)sizeof(T) * (sbs[i] & 1);
           const float m[4] = {M[0], M[1], M[2], M[3]};
-          put_vec(reinterpret_cast<T*>(mp), m);
+          *reinterpret_cast<typename VecOf<4 * sizeof(T)>::type*>(mp) = pack(m, T());
         }
       }
 
@@ -648,14 +681,14 @@ __global__ __launch_bounds__(64 * NW, sizeof(T) == 2 ? 2 : 1) void ssm_scan_kern
     }
 
     // ---- Y^T += x^T M^T + D x^T
-    const typename TX::Col x_col = TX::col_at(rt, qt, [&](int c) { return NB == 2 ? 32 * w + 8 * c : 16 * w + 4 * c; });
-    const typename TK::Col b_col = TK::col_at(rt, qt, [&](int c) { return 8 * c; });
+    const typename TX::Col x_col = TX::col_at(rt, qt, [&](int c) { return !OUT ? 4 * c : NB == 2 ? 32 * w + 8 * c : 16 * w + 4 * c; });
+    const typename TK::Col b_col = TK::col_at(rt, qt, [&](int c) { return (OUT ? 8 : 4) * c; });
     const int p0 = 16 * NB * w + CL * qt;   // the lane's columns
     Frag<T> xf[2][NB];
 #pragma unroll
     for (int j = 0; j < 2; ++j)
 #pragma unroll
-      for (int b = 0; b < NB; ++b) xf[j][b] = TX::col_frag(sX, x_col, j, 0, b);
+      for (int b = 0; b < NB; ++b) xf[j][b] = OUT ? TX::col_frag(sX, x_col, j, 0, b) : TX::col_blk(sX, x_col, j, NB * w + b);
     if constexpr (OUT) {
 #pragma unroll
       for (int tb = 0; tb < 4; ++tb) {
@@ -679,10 +712,12 @@ __global__ __launch_bounds__(64 * NW, sizeof(T) == 2 ? 2 : 1) void ssm_scan_kern
 
     // ---- S <- 2^{G_63} S + (B^T) (w o x), in one or three bf16 terms of w o x
     const float dec = sDec[buf][hw];
+    if constexpr (OUT) {
 #pragma unroll
-    for (int k = 0; k < KB; ++k)
+      for (int k = 0; k < KB; ++k)
 #pragma unroll
-      for (int b = 0; b < NB; ++b) S[k][b] *= dec;
+        for (int b = 0; b < NB; ++b) S[k][b] *= dec;
+    }
     auto update = [&](auto terms_) {
       constexpr int terms = decltype(terms_)::value;
 #pragma unroll
@@ -690,7 +725,10 @@ __global__ __launch_bounds__(64 * NW, sizeof(T) == 2 ? 2 : 1) void ssm_scan_kern
         Frag<T> xs[terms][NB];
         f32x4 v[2];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) v[h] = *reinterpret_cast<const f32x4*>(g.w + 32 * j + 8 * qt + 4 * h);
+        for (int h = 0; h < 2; ++h) {
+          v[h] = *reinterpret_cast<const f32x4*>(g.w + 32 * j + 8 * qt + 4 * h);
+          if constexpr (!OUT) v[h] *= after;
+        }
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
           f32x4 p[2];
@@ -707,7 +745,7 @@ __global__ __launch_bounds__(64 * NW, sizeof(T) == 2 ? 2 : 1) void ssm_scan_kern
         }
 #pragma unroll
         for (int k = 0; k < KB; ++k) {
-          const Frag<T> bf = TK::col_frag(sB, b_col, j, k >> 1, k & 1);
+          const Frag<T> bf = OUT ? TK::col_frag(sB, b_col, j, k >> 1, k & 1) : TK::col_blk(sB, b_col, j, k);
 #pragma unroll
           for (int m = 0; m < terms; ++m)
 #pragma unroll
@@ -717,6 +755,7 @@ __global__ __launch_bounds__(64 * NW, sizeof(T) == 2 ? 2 : 1) void ssm_scan_kern
     };
     if (HALF && fine) update(tiles::Int<HALF ? 3 : 1>{});
     else update(tiles::Int<1>{});
+    if constexpr (!OUT) after *= dec;
     int le = lane;
     asm volatile("" : "+v"(le));
     const int t_row = perm_row(0, le & 15);            // y and z: rows t_row + blk_rows(tb)
@@ -728,7 +767,7 @@ __global__ __launch_bounds__(64 * NW, sizeof(T) == 2 ? 2 : 1) void ssm_scan_kern
         for (int tb = 0; tb < 4; ++tb) {
           const char* zt = wz.at(t0 + tiles::blk_rows(tb));
           if (t_row + tiles::blk_rows(tb) < nr)
-            zr[tb] = *reinterpret_cast<const yvec*>(zt + ((uint32_t)t_row * wz.stride + col_b));
+            zr[tb] = gload<yvec>(zt + ((uint32_t)t_row * wz.stride + col_b));
         }
       }
     }
@@ -755,7 +794,7 @@ __global__ __launch_bounds__(64 * NW, sizeof(T) == 2 ? 2 : 1) void ssm_scan_kern
         char* yt = const_cast<char*>(yc) + (uint64_t)wy.stride * (uint32_t)tiles::blk_rows(tb);
         asm volatile("" : "+s"(yt));
         if (t_row + tiles::blk_rows(tb) < nr)
-          put_vec(reinterpret_cast<T*>(yt + ((uint32_t)t_row * wy.stride + col_b)), y);
+          gstore<yvec>(yt + ((uint32_t)t_row * wy.stride + col_b), pack(y, T()));
       }
     }
   }
@@ -766,10 +805,8 @@ __global__ __launch_bounds__(64 * NW, sizeof(T) == 2 ? 2 : 1) void ssm_scan_kern
     for (int b = 0; b < NB; ++b) {
       float* p = (OUT ? a.ht : seg_state) + state_at(OUT ? sg.n : slot, b);
 #pragma unroll
-      for (int k = 0; k < KS; ++k) {
-        *reinterpret_cast<f32x4*>(p + 32 * k) = S[2 * k][b];
-        *reinterpret_cast<f32x4*>(p + 32 * k + 4) = S[2 * k + 1][b];
-      }
+      for (int k = 0; k < KB; ++k)
+        *reinterpret_cast<f32x4*>(p + (OUT ? 32 * (k >> 1) + 4 * (k & 1) : 16 * k)) = S[k][b];
     }
   }
   if constexpr (!OUT) {   // the waves' shares of the log-decay, in order
