@@ -194,11 +194,13 @@ __device__ __forceinline__ void load_tile(const char* src, uint32_t stride, char
 // wait for them.
 template <typename V>
 __device__ __forceinline__ V gload(const char* p) {
-  return *(const __attribute__((address_space(1))) V*)p;
+  typedef V U __attribute__((aligned(sizeof(V) < 16 ? sizeof(V) : 16)));
+  return *(const __attribute__((address_space(1))) U*)p;
 }
 template <typename V>
 __device__ __forceinline__ void gstore(char* p, V v) {
-  *(__attribute__((address_space(1))) V*)p = v;
+  typedef V U __attribute__((aligned(sizeof(V) < 16 ? sizeof(V) : 16)));
+  *(__attribute__((address_space(1))) U*)p = v;
 }
 
 // The same through registers.
@@ -258,6 +260,12 @@ __device__ __forceinline__ Frag<float> frag_of(f32x4 a, f32x4 b, float) {
   return f;
 }
 
+// Waits until at most N memory accesses of the wave are in flight.
+template <int N>
+__device__ __forceinline__ void wait_vm() {
+  __builtin_amdgcn_s_waitcnt((N & 15) | (N >> 4) << 14 | 0x0F70);
+}
+
 __device__ __forceinline__ float ex2(float x) { return __builtin_amdgcn_exp2f(x); }
 
 // ------------------------------------------------------------ gates
@@ -298,7 +306,7 @@ template <bool HALF> struct alignas(16) Gates {
 // ------------------------------------------------------------ y, z and x rows
 // The lane's four or eight consecutive columns of a row.
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
-typedef uint32_t u32x8 __attribute__((ext_vector_type(8), aligned(16)));
+typedef uint32_t u32x8 __attribute__((ext_vector_type(8)));
 template <int BYTES> struct VecOf;
 template <> struct VecOf<8> { typedef u32x2 type; };
 template <> struct VecOf<16> { typedef u32x4 type; };
@@ -521,9 +529,10 @@ __global__ __launch_bounds__(64 * NW, sizeof(T) == 2 ? 2 : 1) void ssm_scan_kern
     gdt = gload<T>(wd.at(0) + (uint64_t)(uint32_t)(t < count ? t : 0) * wd.stride + gh * (int)sizeof(T));
   };
   if (lane == 0) sSum[w] = 0.0;   // written and read by this wave only, up to the end
+  const double A2 = -(double)expf(a.A_log[hv0 + gh]) * 1.4426950408889634;
+  const float dt_bias = a.dt_bias ? a.dt_bias[hv0 + gh] : 0.f;
   auto gates = [&](int t0) {
-    const double A2 = -(double)expf(a.A_log[hv0 + gh]) * 1.4426950408889634;
-    float d = to_f(gdt) + (a.dt_bias ? a.dt_bias[hv0 + gh] : 0.f);
+    float d = to_f(gdt) + dt_bias;
     if (a.softplus) d = d <= 20.f ? log1pf(expf(d)) : d;
     if (t0 + BT * gc + lane >= count) d = 0.f;
     double lg = (double)d * A2;
@@ -566,9 +575,10 @@ __global__ __launch_bounds__(64 * NW, sizeof(T) == 2 ? 2 : 1) void ssm_scan_kern
     if constexpr (OUT) load_tiles(0);
     else stage(c0 * BT);
     load_dt(c0 / GC * GC * BT);
+    if constexpr (OUT) wait_vm<0>();
   }
 
-  for (int i = 0; i < chunks; ++i) {
+  for (int i = 0; OUT ? chunks > 0 : i < chunks; ++i) {
     const int t0 = (OUT ? i : c0 - i) * BT;
     const int buf = (t0 / BT) % GC;   // chunk of the group
     const int nr = count - t0 < BT ? count - t0 : BT;
@@ -576,10 +586,10 @@ __global__ __launch_bounds__(64 * NW, sizeof(T) == 2 ? 2 : 1) void ssm_scan_kern
     const bool enter = OUT ? buf == 0 : i == 0 || buf == GC - 1;
     if (enter) gates(t0 - buf * BT);
     if constexpr (OUT) {
-      // this wave's share of the tiles: behind its loads lie only the stores of the
-      // chunk before, four or more (it was a full one, so none was skipped)
-      if (i > 0) asm volatile("s_waitcnt vmcnt(4)" ::: "memory");
-      else asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+      // This wave's share of the tiles: behind its loads lie only the stores of the
+      // chunk before, four or more.  With every wait where the compiler can count what
+      // is behind it, it adds none for these stores, or for the next tiles below.
+      wait_vm<4>();
     } else {
       gB.put(sB, w, lane);
       gX.put(sX, w, lane);
@@ -760,42 +770,46 @@ __global__ __launch_bounds__(64 * NW, sizeof(T) == 2 ? 2 : 1) void ssm_scan_kern
     asm volatile("" : "+v"(le));
     const int t_row = perm_row(0, le & 15);            // y and z: rows t_row + blk_rows(tb)
     const uint32_t col_b = (16 * NB * w + CL * (le >> 4)) * (uint32_t)sizeof(T);
-    yvec zr[4];   // loaded here and not with the tiles: eight registers the products need
-    if constexpr (OUT) {
-      if (a.z.p) {
+    yvec zr[4];   // not with the tiles: registers that the products need
+    if (OUT && a.z.p) {
 #pragma unroll
-        for (int tb = 0; tb < 4; ++tb) {
-          const char* zt = wz.at(t0 + tiles::blk_rows(tb));
-          if (t_row + tiles::blk_rows(tb) < nr)
-            zr[tb] = gload<yvec>(zt + ((uint32_t)t_row * wz.stride + col_b));
-        }
+      for (int tb = 0; tb < 4; ++tb) {
+        const char* zt = wz.at(t0 + tiles::blk_rows(tb));
+        if (t_row + tiles::blk_rows(tb) < nr) zr[tb] = gload<yvec>(zt + ((uint32_t)t_row * wz.stride + col_b));
       }
     }
     __builtin_amdgcn_s_setprio(0);
+    if constexpr (OUT) wait_vm<0>();   // z: behind the next tiles' loads the compiler would wait for those too
     tiles::lds_barrier();   // everyone is done with the tiles
-    if (OUT && more) load_tiles(t0 + BT);
-    asm volatile("" ::: "memory");   // the stores stay behind the loads
-
-    // ---- y, gated
     if constexpr (OUT) {
+      // ---- y, gated
       const char* const yc = wy.at(t0);
+      auto finish = [&](auto full_) {
 #pragma unroll
-      for (int tb = 0; tb < 4; ++tb) {
-        float y[CL];
+        for (int tb = 0; tb < 4; ++tb) {
+          float y[CL];
 #pragma unroll
-        for (int e = 0; e < CL; ++e) y[e] = Y[tb][e >> 2][e & 3];
-        if (a.z.p) {
+          for (int e = 0; e < CL; ++e) y[e] = Y[tb][e >> 2][e & 3];
+          if (a.z.p) {
 #pragma unroll
-          for (int e = 0; e < CL; ++e) {
-            const float ze = elem<T>(zr[tb], e);
-            y[e] *= ze * __builtin_amdgcn_rcpf(1.0f + __expf(-ze));
+            for (int e = 0; e < CL; ++e) {
+              const float ze = elem<T>(zr[tb], e);
+              y[e] *= ze * __builtin_amdgcn_rcpf(1.0f + __expf(-ze));
+            }
           }
+          char* yt = const_cast<char*>(yc) + (uint64_t)wy.stride * (uint32_t)tiles::blk_rows(tb);
+          asm volatile("" : "+s"(yt));
+          if (decltype(full_)::value || t_row + tiles::blk_rows(tb) < nr)
+            gstore<yvec>(yt + ((uint32_t)t_row * wy.stride + col_b), pack(y, T()));
         }
-        char* yt = const_cast<char*>(yc) + (uint64_t)wy.stride * (uint32_t)tiles::blk_rows(tb);
-        asm volatile("" : "+s"(yt));
-        if (t_row + tiles::blk_rows(tb) < nr)
-          gstore<yvec>(yt + ((uint32_t)t_row * wy.stride + col_b), pack(y, T()));
+      };
+      if (!more) {
+        finish(tiles::Int<0>{});
+        break;
       }
+      load_tiles(t0 + BT);
+      asm volatile("" ::: "memory");   // the stores stay behind the loads
+      finish(tiles::Int<1>{});
     }
   }
 
