@@ -266,6 +266,11 @@ __device__ __forceinline__ void wait_vm() {
   __builtin_amdgcn_s_waitcnt((N & 15) | (N >> 4) << 14 | 0x0F70);
 }
 
+// Fragments are read from LDS one product ahead of their use: left alone, the compiler
+// has every product wait for its own (long prompt: output launch 75 -> 72 us).  LDS
+// accesses stay on their side of this, everything else may cross.
+__device__ __forceinline__ void ahead() { __builtin_amdgcn_sched_barrier(1); }
+
 __device__ __forceinline__ float ex2(float x) { return __builtin_amdgcn_exp2f(x); }
 
 // ------------------------------------------------------------ gates
@@ -575,8 +580,8 @@ __global__ __launch_bounds__(64 * NW, sizeof(T) == 2 ? 2 : 1) void ssm_scan_kern
     if constexpr (OUT) load_tiles(0);
     else stage(c0 * BT);
     load_dt(c0 / GC * GC * BT);
-    if constexpr (OUT) wait_vm<0>();
   }
+  if constexpr (OUT) wait_vm<0>();
 
   for (int i = 0; OUT ? chunks > 0 : i < chunks; ++i) {
     const int t0 = (OUT ? i : c0 - i) * BT;
@@ -627,14 +632,20 @@ __global__ __launch_bounds__(64 * NW, sizeof(T) == 2 ? 2 : 1) void ssm_scan_kern
         sbs[i] = n < 4 ? n & 1 : n & 3;
         E[i] = zero4();
       }
+      auto score_frag = [&](const char* tile, int n, const int (&blk)[3]) {
+        return TK::row_frag(tile, (k_row ^ (n / 3 * TK::slab_x)) + tiles::blk_rows(blk[n % 3]) * TK::row_bytes, 0);
+      };
+      Frag<T> bn = score_frag(sB, 0, sbs), cn = score_frag(sC, 0, tbs);
 #pragma unroll
-      for (int k = 0; k < KS; ++k)
-#pragma unroll
-        for (int i = 0; i < 3; ++i) {
-          const int at = k_row ^ (k * TK::slab_x);
-          E[i] = mma(TK::row_frag(sB, at + tiles::blk_rows(sbs[i]) * TK::row_bytes, 0),
-                     TK::row_frag(sC, at + tiles::blk_rows(tbs[i]) * TK::row_bytes, 0), E[i]);
+      for (int n = 0; n < 3 * KS; ++n) {
+        const Frag<T> bf = bn, cf = cn;
+        if (n + 1 < 3 * KS) {
+          bn = score_frag(sB, n + 1, sbs);
+          cn = score_frag(sC, n + 1, tbs);
+          ahead();
         }
+        E[n % 3] = mma(bf, cf, E[n % 3]);
+      }
 #pragma unroll
       for (int i = 0; i < 3; ++i) {
         const int t = perm_row(0, rt) + tiles::blk_rows(tbs[i]);
@@ -665,6 +676,7 @@ __global__ __launch_bounds__(64 * NW, sizeof(T) == 2 ? 2 : 1) void ssm_scan_kern
       }
 
       // ---- Y^T = 2^{G_t} S C^T
+      Frag<T> cnext = TK::row_frag(sC, k_row, 0);
 #pragma unroll
       for (int tb = 0; tb < 4; ++tb)
 #pragma unroll
@@ -676,7 +688,11 @@ __global__ __launch_bounds__(64 * NW, sizeof(T) == 2 ? 2 : 1) void ssm_scan_kern
         for (int b = 0; b < NB; ++b) sf[b] = frag_of(S[2 * k][b], S[2 * k + 1][b], T());
 #pragma unroll
         for (int tb = 0; tb < 4; ++tb) {
-          const Frag<T> cf = TK::row_frag(sC, k_row ^ (k * TK::slab_x), tb);
+          const Frag<T> cf = cnext;
+          if (4 * k + tb + 1 < 4 * KS) {
+            cnext = TK::row_frag(sC, k_row ^ ((k + (tb + 1) / 4) * TK::slab_x), (tb + 1) % 4);
+            ahead();
+          }
 #pragma unroll
           for (int b = 0; b < NB; ++b) Y[tb][b] = mma(sf[b], cf, Y[tb][b]);
         }
@@ -730,6 +746,8 @@ __global__ __launch_bounds__(64 * NW, sizeof(T) == 2 ? 2 : 1) void ssm_scan_kern
     }
     auto update = [&](auto terms_) {
       constexpr int terms = decltype(terms_)::value;
+      auto b_frag = [&](int j, int k) { return OUT ? TK::col_frag(sB, b_col, j, k >> 1, k & 1) : TK::col_blk(sB, b_col, j, k); };
+      Frag<T> next = b_frag(0, 0);
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         Frag<T> xs[terms][NB];
@@ -755,7 +773,11 @@ __global__ __launch_bounds__(64 * NW, sizeof(T) == 2 ? 2 : 1) void ssm_scan_kern
         }
 #pragma unroll
         for (int k = 0; k < KB; ++k) {
-          const Frag<T> bf = OUT ? TK::col_frag(sB, b_col, j, k >> 1, k & 1) : TK::col_blk(sB, b_col, j, k);
+          const Frag<T> bf = next;
+          if (k + 1 < KB || j == 0) {
+            next = b_frag(k + 1 < KB ? j : 1, k + 1 < KB ? k + 1 : 0);
+            ahead();
+          }
 #pragma unroll
           for (int m = 0; m < terms; ++m)
 #pragma unroll
