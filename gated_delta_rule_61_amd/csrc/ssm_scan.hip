@@ -33,17 +33,16 @@
 // That reads x and B twice but moves no per-chunk states.
 //
 // Measured (bf16, K = 128).  One prompt of 8192 tokens x 64 heads of 64, gated:
-// launches of 44 + 13 + 80 us, 128 us a call for 209 MB (41 us at a large copy's 5.1
-// TB/s).  Eight packed prompts of 5003 tokens, 32 heads of 128, initial and final
-// states: 34 + 12 + 52 us, 88 a call, 137 MB (27 us).  The same 8192 tokens as 16
-// prompts, one launch: 72 us.  fp32, 4096 tokens x 32 heads of 64: 121 us.  What
-// bounds it is no one unit: of the last launch's cycles the vector ALU issues in 37 %,
-// LDS in 17 % with 10 % more of bank conflicts (the transposing reads and the stores
-// of M take one half of every 16-byte unit at a time, so half of the banks), the
-// matrix cores work in 12 %, between three barriers a chunk.  Left out one at a time,
-// scores save 14 us of 72, the tile loads, the state update and the stores 10 each,
-// silu 6, the gates 3; twice the waves or prefetched tiles save nothing.  In the first
-// launch two of the three terms of the state update cost 10 us of 44.
+// launches of 42 + 13 + 73 us, 125 us a call from a loop for 209 MB (41 us at a large
+// copy's 5.1 TB/s).  Eight packed prompts of 5003 tokens, 32 heads of 128, initial and
+// final states: 31 + 12 + 50 us, 84 a call, 136 MB (27 us).  The same 8192 tokens as
+// 16 prompts, one launch: 88 us a call.  fp32, 4096 tokens x 32 heads of 64: 113 us.
+// What bounds it is no one unit: of the last launch's cycles the vector ALU issues in
+// 43 %, LDS in 21 % with 12 % more of bank conflicts (the transposing reads and the
+// stores of M take one half of every 16-byte unit at a time, so half of the banks), the
+// matrix cores work in 14 %, between three barriers a chunk.  Twice the waves gained
+// nothing, nor did a higher wave priority for the products.  The first launch takes 16
+// us without its state update, 33 with one bf16 term of three.
 //
 // Precision.  Gate sums are taken in 64 bits, over log2-decays held at -160 a
 // token or more (2^-160 is 0 in fp32 already), so that with bf16 io an fp32 G is
@@ -267,8 +266,8 @@ __device__ __forceinline__ void wait_vm() {
 }
 
 // Fragments are read from LDS one product ahead of their use: left alone, the compiler
-// has every product wait for its own (long prompt: output launch 75 -> 72 us).  LDS
-// accesses stay on their side of this, everything else may cross.
+// has every product wait for its own (the long prompt above 129 -> 125 us, the packed
+// ones 87 -> 84).  LDS accesses stay on their side of this, everything else may cross.
 __device__ __forceinline__ void ahead() { __builtin_amdgcn_sched_barrier(1); }
 
 __device__ __forceinline__ float ex2(float x) { return __builtin_amdgcn_exp2f(x); }
@@ -608,9 +607,6 @@ __global__ __launch_bounds__(64 * NW, sizeof(T) == 2 ? 2 : 1) void ssm_scan_kern
       if (more) stage(t0 - BT);
     }
     const Gates<HALF>& g = sG[buf][hw];
-    // the products go before the other work-group's loads and stores on the SIMD (packed
-    // prompts above 91 -> 88 us, the long one 135 -> 133)
-    __builtin_amdgcn_s_setprio(1);
     // The lane's addresses in the tiles, made anew for every chunk (the asm sees to
     // it): held over the loop they would spill.
     int lt = lane;
@@ -800,7 +796,6 @@ __global__ __launch_bounds__(64 * NW, sizeof(T) == 2 ? 2 : 1) void ssm_scan_kern
         if (t_row + tiles::blk_rows(tb) < nr) zr[tb] = gload<yvec>(zt + ((uint32_t)t_row * wz.stride + col_b));
       }
     }
-    __builtin_amdgcn_s_setprio(0);
     if constexpr (OUT) wait_vm<0>();   // z: behind the next tiles' loads the compiler would wait for those too
     tiles::lds_barrier();   // everyone is done with the tiles
     if constexpr (OUT) {
@@ -958,11 +953,11 @@ SsmPlan ssm_plan(int nb, int T, int Hk, int HV, int K, int V, int N, bool varlen
   const long long tokens = (long long)nb * T;
   const long long tiles = HV / p.nh;
   // One round of work-groups on 256 CUs: two a CU, one with fp32 tiles (bf16, one
-  // prompt of 8192 tokens x 64 heads: 256 work-groups 168 us, 512 135, 768 166, 1024
-  // 152).  But no segment shorter than 2 sqrt(T) tokens: halving the segments
+  // prompt of 8192 tokens x 64 heads: 256 work-groups 149 us, 512 124, 768 149, 1024
+  // 145).  But no segment shorter than 2 sqrt(T) tokens: halving the segments
   // saves two launches the half of their chunks and costs the join as many steps
-  // (2048 tokens x 32 heads: 64-token segments 44 us, 128 39, 256 51; 700 x 16
-  // heads: 64 27, 128 32, 256 44).
+  // (2048 tokens x 32 heads: 64-token segments 41 us, 128 36, 256 46; 700 x 16
+  // heads: 64 26, 128 29, 256 40).
   const long long want = bf16 ? 512 : 256;
   // packed sequences end in half a segment on average, up to half of the work-groups
   const long long tails = !varlen ? 0 : tiles * N < want ? tiles * N / 2 : want / 2;
@@ -970,7 +965,7 @@ SsmPlan ssm_plan(int nb, int T, int Hk, int HV, int K, int V, int N, bool varlen
   const long long least = ((long long)(2.0 * sqrt((double)T)) + 63) / 64 * 64;
   seg = seg < least ? least : seg;
   // nor two chunks alone: they cost less than two more launches (128 tokens x 8 heads
-  // 17.9 us in one launch, 20.8 in three; 192 tokens 24.1 and 21.4)
+  // 16.2 us in one launch, 20.6 in three; 192 tokens 21.3 and 20.9)
   // nor so many sequences that the join's launch would have 2^32 threads
   const bool join = (long long)N * HV * (K * V / 1024) < (1 << 24);
   if (seg >= T || T <= 128 || !join) seg = ((long long)T + 63) / 64 * 64;
