@@ -57,6 +57,7 @@
 #include "gdn_device.h"
 #include "mixer_launch.h"
 #include "scan_tiles.h"
+#include "ssm_rate.h"
 
 namespace gdn {
 
@@ -298,6 +299,8 @@ __device__ __forceinline__ double lane_of(double x, int l) {
   return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
 }
 
+constexpr double LOG2E = 1.4426950408889634;
+
 // Gates of a chunk and head, in LDS.  Scores are gated by 2^{G_t - G_s} D_s.
 template <bool HALF> struct alignas(16) Gates {
   float g[BT];            // G_t
@@ -533,14 +536,21 @@ __global__ __launch_bounds__(64 * NW, sizeof(T) == 2 ? 2 : 1) void ssm_scan_kern
     gdt = gload<T>(wd.at(0) + (uint64_t)(uint32_t)(t < count ? t : 0) * wd.stride + gh * (int)sizeof(T));
   };
   if (lane == 0) sSum[w] = 0.0;   // written and read by this wave only, up to the end
-  const double A2 = -(double)expf(a.A_log[hv0 + gh]) * 1.4426950408889634;
+  const float A_log = a.A_log[hv0 + gh];
+  const double A2 = -rate_of(A_log) * LOG2E;
+  const bool fast = a.softplus && A_log > FAST_RATE;
   const float dt_bias = a.dt_bias ? a.dt_bias[hv0 + gh] : 0.f;
   auto gates = [&](int t0) {
-    float d = to_f(gdt) + dt_bias;
-    if (a.softplus) d = d <= 20.f ? log1pf(expf(d)) : d;
-    if (t0 + BT * gc + lane >= count) d = 0.f;
+    const float u = to_f(gdt) + dt_bias;
+    float d = u;
+    if (a.softplus) d = u <= 20.f ? log1pf(expf(u)) : u;
     double lg = (double)d * A2;
+    if (fast) lg = -fast_decay(A_log, u) * LOG2E;
     lg = lg < -160.0 ? -160.0 : lg;
+    if (t0 + BT * gc + lane >= count) {   // rows past the end leave the state alone
+      d = 0.f;
+      lg = 0.0;
+    }
     const double G = wave_scan(lg);
     const double tot = lane_of(G, 63);
     Gates<HALF>& g = sG[gc][gh];

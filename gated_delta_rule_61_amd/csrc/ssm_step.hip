@@ -20,6 +20,7 @@
 
 #include "gdn_device.h"
 #include "mixer_launch.h"
+#include "ssm_rate.h"
 
 namespace gdn {
 
@@ -147,7 +148,9 @@ __global__ __launch_bounds__(TPB) void ssm_step_kernel(SsmArgs a, int parts) {
     dt[t] = to_f(dp[t * a.dt.token]);
     zz[t] = a.z.p ? to_f(zp[t * a.z.token + (cl & 7)]) : 0.f;
   }
-  const float A = -expf(a.A_log[hv]);
+  const float A_log = a.A_log[hv];
+  const float A = -expf(A_log);
+  const bool fast = A_log > FAST_RATE;
   const float bias = a.dt_bias ? a.dt_bias[hv] : 0.f;
   const float skip = a.D ? a.D[hv] : 0.f;
 
@@ -157,9 +160,12 @@ __global__ __launch_bounds__(TPB) void ssm_step_kernel(SsmArgs a, int parts) {
 
 #pragma unroll
   for (int t = 0; t < TT; ++t) {
-    float d = dt[t] + bias;
-    if (a.softplus) d = d <= 20.f ? log1pf(expf(d)) : d;
-    const float alpha = expf(A * d);
+    const float u = dt[t] + bias;
+    float d = u;
+    if (a.softplus) d = u <= 20.f ? log1pf(expf(u)) : u;
+    float Ad = A * d;
+    if (fast) Ad = -(float)(a.softplus ? fast_decay(A_log, u) : rate_of(A_log) * (double)d);
+    const float alpha = expf(Ad);
     float out[R];
 #pragma unroll
     for (int i = 0; i < R; ++i) {

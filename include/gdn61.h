@@ -492,7 +492,8 @@ int gdn_conv_step(const void* x, long long x_batch, long long x_token, const voi
  *                each of these five with the strides of its batch rows and
  *                tokens in elements (*_batch, *_token), so that slices of a
  *                projection are taken as they are; heads and channels contiguous
- *   A_log        [HV]           fp32
+ *   A_log        [HV]           fp32; exp(A_log) may pass fp32's largest number
+ *                               (D_t = 0 keeps the state then too)
  *   dt_bias, D   [HV]           fp32, or NULL (0)
  *   h0           [N, HV, V, K]  fp32 initial state, or NULL for zeros
  *   ht           [N, HV, V, K]  fp32 final state out, or NULL to skip
@@ -506,7 +507,8 @@ int gdn_conv_step(const void* x, long long x_batch, long long x_token, const voi
  * chunk_size = 64; x, Bm, Cm, z and their strides in multiples of 16 bytes.
  * Sums, gates and states are fp32 or wider; with bf16 io the products that make
  * y take the state and the decayed scores rounded to bf16, those that make ht
- * lose nothing to fp32.  Tokens are taken in chunks of 64 (from each sequence's
+ * lose nothing to fp32 (but for what is below 2^-126 of the weighted x or of its
+ * last 16 bits, which the matrix cores take as 0).  Tokens are taken in chunks of 64 (from each sequence's
  * start) as matrix products: an infinity or NaN in x makes its channel's outputs
  * NaN from the beginning of its chunk on, where the recurrence would from its
  * token on; one in dt, Bm or Cm reaches the tokens the recurrence says.

@@ -263,3 +263,57 @@ def test_scan_offsets_past_32_bits():
     assert not y[:, :-130].any() and not ht[0].any()
     del big, y
     torch.cuda.empty_cache()
+
+
+def _fast_rates(seed, B, T, HV, K, V, dtype, N=None):
+    """Heads whose rate exp(A_log) passes fp32's largest number, with steps that
+    underflow to 0 (dt = -200) or are 2e-35 (-80) among ordinary ones.  (No fp32
+    subnormal steps: their own rounding, times such a rate, is no small error.)"""
+    p = ssm_inputs(seed, B, T, 1, HV, K, V, dtype, N=N)
+    p["A_log"] = torch.tensor([90.0, 0.3, 200.0, 89.0, 64.5, 95.0])[:HV]
+    p["dt_bias"] = torch.zeros(HV)
+    p["dt"][:, 3::7] = -200.0
+    p["dt"][:, 5::11] = -80.0
+    p["dt"][:, 20:45] = -200.0     # the state of a long run of such tokens
+    return p
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("lens,HV,V", [([100, 1, 64, 70], 4, 64), ([100, 3], 3, 64), ([1000, 0, 40], 1, 64),
+                                       ([900], 2, 128), ([700, 33], 2, 64)])
+def test_scan_at_rates_past_fp32(dtype, lens, HV, V):
+    """A decay of 0, and 1 where the step is 0: also behind the end of a sequence,
+    within a chunk and in the chunks that fill up a group of gates."""
+    print(f"scan rates past fp32 {dtype} {lens} HV={HV} V={V}", flush=True)
+    T = sum(lens)
+    p = _fast_rates(1200, 1, T, HV, 64, V, dtype, N=len(lens))
+    y, ht = _run(p, cu_seqlens=torch.tensor(edges(lens), dtype=torch.int64, device=DEV))
+    torch.cuda.synchronize()
+    ry, mag, skip, rh, hm = ssm_ref(p, lens)
+    close("y", y[0], ry, ssm_bound(dtype, ry, mag, skip))
+    # bf16 io: a step of 2e-35 makes state elements of 1e-36.  Of the three bf16 terms
+    # whose products with B form them the second and third are then below 2^-126, where
+    # the matrix cores take a bf16 operand as 0: at most 2^-126 |B_s| a term is lost, and
+    # decays after it are at most 1.  2^-125 sum_s |B_s| is below 1e-34 here.
+    lost = np.zeros_like(hm)
+    if dtype == BF:
+        e, B = edges(lens), np.abs(f64(p["Bm"])[0, :, 0])
+        lost += 2.0 ** -125 * np.stack([B[lo:hi].sum(0) for lo, hi in zip(e, e[1:])])[:, None, None, :]
+    close("ht", ht, rh, 512 * U * hm + 2.0 ** -20 * hm + lost)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_step_at_rates_past_fp32(dtype):
+    print(f"step rates past fp32 {dtype}", flush=True)
+    for row, dt in enumerate((-200.0, -80.0, 0.5)):
+        p = _fast_rates(1300 + row, 1, 2, 6, 64, 64, dtype)
+        p["dt"][:] = dt
+        pool = d(p["h0"]).clone()
+        y = binding.ssm_step(*(d(p[k]) for k in ("x", "dt", "Bm", "Cm", "A_log")), pool, D=d(p["D"]), z=d(p["z"]),
+                             dt_bias=d(p["dt_bias"]))
+        torch.cuda.synchronize()
+        ry, mag, skip, rh, hm = ssm_ref(p, [2])
+        close(f"y {dt}", y[0], ry, 512 * U * mag + 2.0 ** -20 * (mag + skip) + store(dtype, ry))
+        # elements below 2^-126 are 2^-149 apart: three roundings a token (D x, its product
+        # with B, the sum), two tokens, half a step each
+        close(f"state {dt}", pool, rh, 2.0 ** -20 * hm + store(F32, rh) + 6 * 2.0 ** -150)
