@@ -60,9 +60,11 @@ struct SsmArgs {
   int bf16;
 };
 // How a prompt call is cut: every sequence into segments of `seg` tokens (a
-// multiple of 64), at most `slots` segments in all, `nh` heads a work-group.
+// multiple of 64), at most `slots` segments in all, `nh` heads a work-group.  At most
+// `joins` sequences have more than one segment, together at most `states`, whose
+// states the workspace holds.
 struct SsmPlan {
-  int nh, seg, slots;
+  int nh, seg, slots, joins, states;
   bool split;                   // whether a sequence can have more than one segment
   size_t decay_off, bytes;      // workspace: states first, then the log2-decays
 };

@@ -18,11 +18,10 @@ namespace gdn {
 
 constexpr float FAST_RATE = 64.f;
 
-// exp(A_log), at most e^144
+// exp(A_log), at most e^144 (the branch is uniform)
 __device__ __forceinline__ double rate_of(float A_log) {
-  const float lo = A_log > FAST_RATE ? FAST_RATE : A_log;
-  const float more = A_log > FAST_RATE ? (A_log > 144.f ? 80.f : A_log - FAST_RATE) : 0.f;
-  return (double)expf(lo) * (double)expf(more);
+  if (!(A_log > FAST_RATE)) return (double)expf(A_log);
+  return (double)expf(FAST_RATE) * (double)expf(A_log > 144.f ? 80.f : A_log - FAST_RATE);
 }
 
 // exp(A_log) softplus(u) for A_log > FAST_RATE

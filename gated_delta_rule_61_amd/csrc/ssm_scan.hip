@@ -354,15 +354,17 @@ __device__ __forceinline__ typename VecOf<4 * N>::type pack(const float (&y)[N],
 // ------------------------------------------------------------ segments
 struct Segment {
   int n, j;              // sequence (< 0: none), segment of it
+  int state;             // its state in the workspace, if the sequence is split
   long long start;       // its sequence's first token among the batch row's
   int len;               // tokens of the sequence
 };
 
-// Packed sequences are looked at 64 at a time, one a lane.
+// Packed sequences are looked at 64 at a time, one a lane.  Only sequences of two
+// segments or more have states in the workspace, one a segment.
 struct Packed {
   long long b0;    // first token
   int len, segs;   // tokens and segments, 0 behind the last sequence
-  int incl, all;   // segments up to and with this one, of all 64
+  int states;      // segments, if there are two or more
   __device__ __forceinline__ Packed(const SsmArgs& a, int seg, int n, int lane) {
     long long b1 = 0;
     b0 = 0;
@@ -374,7 +376,15 @@ struct Packed {
     }
     len = (int)(b1 - b0);
     segs = n < a.N ? (len > seg ? (len + seg - 1) / seg : 1) : 0;
-    incl = segs;
+    states = segs > 1 ? segs : 0;
+  }
+};
+
+// Inclusive sum over the lanes, and that of all.
+struct LaneSum {
+  int incl, all;
+  __device__ __forceinline__ LaneSum(int x, int lane) {
+    incl = x;
 #pragma unroll
     for (int off = 1; off < 64; off <<= 1) {
       const int y = __shfl_up(incl, off, 64);
@@ -387,44 +397,57 @@ struct Packed {
 // The segment and head tile of work-group `wg` of 8 XCDs: the tiles of a segment
 // (which share B and C) run next to each other on one XCD, and every XCD gets an
 // equal run of the segments that there are (packed sequences seldom fill the slots
-// the host counts).  Same result in every lane; n < 0: none.
+// the host counts).  OUT: of all segments; otherwise of those with a state.  Same
+// result in every lane; n < 0: none.
+template <bool OUT>
 __device__ __forceinline__ Segment find_segment(const SsmArgs& a, int seg, int slots, int tiles, int wg, int lane,
-                                                int& slot, int& tile) {
+                                                int& tile) {
   Segment g;
   g.n = -1;
-  g.j = 0;
+  g.j = g.state = 0;
   g.start = 0;
   g.len = 0;
-  Packed p(a, seg, a.cu ? lane : a.N, lane);
-  if (a.cu) {
-    int used = p.all;
-    for (int base = 64; base < a.N; base += 64) used += Packed(a, seg, base + lane, lane).all;
-    slots = used < slots ? used : slots;   // boundaries out of order may claim more
-  }
-  const int work = slots * tiles, per_xcd = (work + 7) / 8;
-  const int id = (wg & 7) * per_xcd + (wg >> 3);
-  slot = id / tiles;
-  tile = id - slot * tiles;
-  if ((wg >> 3) >= per_xcd || id >= work) return g;
+  int slot;
+  auto deal = [&](int slots) -> bool {
+    const int work = slots * tiles, per_xcd = (work + 7) / 8;
+    const int id = (wg & 7) * per_xcd + (wg >> 3);
+    slot = id / tiles;
+    tile = id - slot * tiles;
+    return (wg >> 3) < per_xcd && id < work;
+  };
   if (!a.cu) {
+    if (!deal(slots)) return g;
     const int per = a.T > seg ? (a.T + seg - 1) / seg : 1;
     g.n = slot / per;
     g.j = slot - g.n * per;
+    g.state = slot;
     g.len = a.T;
     return g;
   }
-  int run = 0;
+  auto dealt = [](const Packed& p) { return OUT ? p.segs : p.states; };
+  Packed p(a, seg, lane, lane);
+  LaneSum sum(dealt(p), lane);
+  int used = sum.all;
+  for (int base = 64; base < a.N; base += 64) used += LaneSum(dealt(Packed(a, seg, base + lane, lane)), lane).all;
+  if (!deal(used < slots ? used : slots)) return g;   // boundaries out of order may claim more
+  int run = 0, states = 0;   // of the sequences before these 64
   for (int base = 0; base < a.N; base += 64) {
-    if (base > 0) p = Packed(a, seg, base + lane, lane);
-    if (slot < run + p.all) {
-      const int l = __ffsll((unsigned long long)__ballot(p.incl > slot - run)) - 1;
+    if (base > 0) {
+      p = Packed(a, seg, base + lane, lane);
+      sum = LaneSum(dealt(p), lane);
+    }
+    const LaneSum st = OUT ? LaneSum(p.states, lane) : sum;
+    if (slot < run + sum.all) {
+      const int l = __ffsll((unsigned long long)__ballot(sum.incl > slot - run)) - 1;
       g.n = base + l;
-      g.j = slot - run - (__builtin_amdgcn_readlane(p.incl, l) - __builtin_amdgcn_readlane(p.segs, l));
+      g.j = slot - run - __builtin_amdgcn_readlane(sum.incl - dealt(p), l);
+      g.state = states + __builtin_amdgcn_readlane(st.incl - p.states, l) + g.j;
       g.start = __builtin_amdgcn_readlane((int)p.b0, l);
       g.len = __builtin_amdgcn_readlane(p.len, l);
       return g;
     }
-    run += p.all;
+    run += sum.all;
+    states += st.all;
   }
   return g;
 }
@@ -434,7 +457,8 @@ __device__ __forceinline__ Segment find_segment(const SsmArgs& a, int seg, int s
 // launch of a split call, which writes segment states and log-decays.
 template <typename T, int K, int V, int NH, bool OUT>
 __global__ __launch_bounds__(64 * NW, sizeof(T) == 2 ? 2 : 1) void ssm_scan_kernel(
-    SsmArgs a, int seg, int slots, bool split, float* __restrict__ seg_state, double* __restrict__ seg_decay) {
+    SsmArgs a, int seg, int slots, int states, bool split, float* __restrict__ seg_state,
+    double* __restrict__ seg_decay) {
   constexpr int CW = NH * V;            // columns of the work-group
   constexpr int NB = CW / 16 / NW;      // 16-column blocks of a wave
   constexpr int KB = K / 16, KS = K / 32;
@@ -454,8 +478,8 @@ __global__ __launch_bounds__(64 * NW, sizeof(T) == 2 ? 2 : 1) void ssm_scan_kern
   const int tid = threadIdx.x, lane = tid & 63;
   const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int r = lane & 15, q = lane >> 4;
-  int slot, tile;
-  const Segment sg = find_segment(a, seg, slots, a.HV / NH, blockIdx.x, lane, slot, tile);
+  int tile;
+  const Segment sg = find_segment<OUT>(a, seg, OUT ? slots : states, a.HV / NH, blockIdx.x, lane, tile);
   if (sg.n < 0) return;
   const int hv0 = tile * NH;
   const int hk = hv0 / (a.HV / a.Hk);
@@ -465,7 +489,7 @@ __global__ __launch_bounds__(64 * NW, sizeof(T) == 2 ? 2 : 1) void ssm_scan_kern
   // a sequence of one segment needs no join; elsewhere the last segment's state is
   // nobody's start and made only for ht
   const bool alone = !split || sg.len <= seg;
-  if (!OUT && (alone || (last && !a.ht))) return;
+  if (!OUT && last && !a.ht) return;
 
   // rows of this sequence, from the segment's first on
   const long long brow = a.cu ? 0 : sg.n;
@@ -508,8 +532,11 @@ __global__ __launch_bounds__(64 * NW, sizeof(T) == 2 ? 2 : 1) void ssm_scan_kern
     }
   };
   if (OUT) {
-    if (sg.j > 0) load_state(seg_state, slot - 1);   // the joined state behind the segment before
-    else if (a.h0) load_state(a.h0, sg.n);
+    if (sg.j > 0) {   // the joined state behind the segment before
+      if (sg.state <= states) load_state(seg_state, sg.state - 1);   // always, for boundaries in order
+    } else if (a.h0) {
+      load_state(a.h0, sg.n);
+    }
   }
 
   // ---- a chunk's tiles
@@ -844,7 +871,7 @@ __global__ __launch_bounds__(64 * NW, sizeof(T) == 2 ? 2 : 1) void ssm_scan_kern
   if (!OUT || out_ht) {
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
-      float* p = (OUT ? a.ht : seg_state) + state_at(OUT ? sg.n : slot, b);
+      float* p = (OUT ? a.ht : seg_state) + state_at(OUT ? sg.n : sg.state, b);
 #pragma unroll
       for (int k = 0; k < KB; ++k)
         *reinterpret_cast<f32x4*>(p + (OUT ? 32 * (k >> 1) + 4 * (k & 1) : 16 * k)) = S[k][b];
@@ -856,7 +883,7 @@ __global__ __launch_bounds__(64 * NW, sizeof(T) == 2 ? 2 : 1) void ssm_scan_kern
       double sum = 0.0;
 #pragma unroll
       for (int i = 0; i < GC; ++i) sum += sSum[i * NH + tid];
-      seg_decay[(size_t)slot * a.HV + hv0 + tid] = sum;
+      seg_decay[(size_t)sg.state * a.HV + hv0 + tid] = sum;
     }
   }
 }
@@ -869,34 +896,39 @@ __global__ __launch_bounds__(64 * NW, sizeof(T) == 2 ? 2 : 1) void ssm_scan_kern
 // (16 segments x 64 heads of 64 x 128: 67 MB in 13 us, 5.2 TB/s).  Each segment's
 // work-groups joining what lies before them instead, in the last launch, took 5 us
 // off 5 segments a prompt and added 37 to 16 (their reads are serial and repeated).
-__global__ __launch_bounds__(256) void ssm_join_kernel(SsmArgs a, int seg, int slots, int blocks_per_head,
+__global__ __launch_bounds__(256) void ssm_join_kernel(SsmArgs a, int seg, int states, int blocks_per_head,
                                                        float* __restrict__ seg_state,
                                                        const double* __restrict__ seg_decay) {
   const int lane = threadIdx.x & 63;
-  const int nh = blockIdx.x / blocks_per_head;
-  const int part = blockIdx.x - nh * blocks_per_head;
-  const int n = nh / a.HV, hv = nh - n * a.HV;
-  int slot0 = 0, segs = 1;
+  const int mh = blockIdx.x / blocks_per_head;
+  const int part = blockIdx.x - mh * blocks_per_head;
+  const int m = mh / a.HV, hv = mh - m * a.HV;   // the m-th sequence of those that are split
+  int n = m, slot0 = 0, segs = 1;
   if (!a.cu) {
     segs = a.T > seg ? (a.T + seg - 1) / seg : 1;
     slot0 = n * segs;
-  } else {   // slots of the sequences before n, summed over the wave
-    int before = 0;
-    for (int m = lane; m <= n; m += 64) {
-      long long b0 = a.cu[m], b1 = a.cu[m + 1];
-      b0 = b0 < 0 ? 0 : (b0 > a.T ? a.T : b0);
-      b1 = b1 < b0 ? b0 : (b1 > a.T ? a.T : b1);
-      const int len = (int)(b1 - b0), c = len > seg ? (len + seg - 1) / seg : 1;
-      if (m < n) before += c;
-      else segs = c;
+  } else {
+    int before = 0;   // split sequences before these 64
+    for (int base = 0;; base += 64) {
+      if (base >= a.N) return;
+      const Packed p(a, seg, base + lane, lane);
+      const LaneSum sum(p.states, lane);
+      const unsigned long long cut = __ballot(p.states > 0);
+      if (m < before + __popcll(cut)) {
+        const int rank = before + __popcll(cut & ((1ULL << lane) - 1));
+        const int l = __ffsll((unsigned long long)__ballot(p.states > 0 && rank == m)) - 1;
+        n = base + l;
+        segs = __builtin_amdgcn_readlane(p.states, l);
+        slot0 += __builtin_amdgcn_readlane(sum.incl, l) - segs;
+        break;
+      }
+      before += __popcll(cut);
+      slot0 += sum.all;
     }
-#pragma unroll
-    for (int off = 32; off > 0; off >>= 1) before += __shfl_xor(before, off, 64);
-    slot0 = before;
-    segs = __shfl(segs, n & 63, 64);
   }
-  // boundaries out of order may claim more slots than there are
-  if (segs > slots - slot0) segs = slots - slot0;
+  // boundaries out of order may claim more states than there are
+  if (slot0 < 0 || slot0 >= states) return;
+  if (segs > states - slot0) segs = states - slot0;
   if (segs < 2) return;
   const int own_states = segs - (a.ht ? 0 : 1);
   const size_t VK = (size_t)a.V * a.K, head = (size_t)a.HV * VK;
@@ -904,7 +936,10 @@ __global__ __launch_bounds__(256) void ssm_join_kernel(SsmArgs a, int seg, int s
   f32x4 st = zero4();
   if (a.h0) st = *reinterpret_cast<const f32x4*>(a.h0 + (size_t)n * head + hv * VK + e0);
   float* p = seg_state + (size_t)slot0 * head + hv * VK + e0;
-  const double* d = seg_decay + (size_t)slot0 * a.HV + hv;
+  // the decays by vector loads: as scalar ones they hold up the loop (13.6 us in place of 12.5 above)
+  int slot_v = slot0;
+  asm("" : "+v"(slot_v));
+  const double* d = seg_decay + (size_t)slot_v * a.HV + hv;
   constexpr int U = 4;
   for (int j = 0; j < own_states; j += U) {
     f32x4 own[U];
@@ -929,21 +964,23 @@ __global__ __launch_bounds__(256) void ssm_join_kernel(SsmArgs a, int seg, int s
 
 template <typename T, int K, int V, int NH>
 hipError_t launch_t(const SsmArgs& a, const SsmPlan& p, hipStream_t s) {
-  const int work = p.slots * (a.HV / NH);
-  const dim3 grid((unsigned)((work + 7) / 8 * 8)), block(64 * NW);
+  const int tiles = a.HV / NH;
+  auto grid = [&](int slots) { return dim3((unsigned)((slots * tiles + 7) / 8 * 8)); };
   float* st = reinterpret_cast<float*>(a.workspace);
   double* dec = p.split ? reinterpret_cast<double*>(reinterpret_cast<char*>(a.workspace) + p.decay_off) : nullptr;
   if (p.split) {
-    hipLaunchKernelGGL((ssm_scan_kernel<T, K, V, NH, false>), grid, block, 0, s, a, p.seg, p.slots, true, st, dec);
+    hipLaunchKernelGGL((ssm_scan_kernel<T, K, V, NH, false>), grid(p.states), dim3(64 * NW), 0, s, a, p.seg, p.slots,
+                       p.states, true, st, dec);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     constexpr int per_head = K * V / 1024;
-    hipLaunchKernelGGL(ssm_join_kernel, dim3((unsigned)((long long)a.N * a.HV * per_head)), dim3(256), 0, s, a, p.seg,
-                       p.slots, per_head, st, dec);
+    hipLaunchKernelGGL(ssm_join_kernel, dim3((unsigned)((long long)p.joins * a.HV * per_head)), dim3(256), 0, s, a,
+                       p.seg, p.states, per_head, st, dec);
     e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
-  hipLaunchKernelGGL((ssm_scan_kernel<T, K, V, NH, true>), grid, block, 0, s, a, p.seg, p.slots, p.split, st, dec);
+  hipLaunchKernelGGL((ssm_scan_kernel<T, K, V, NH, true>), grid(p.slots), dim3(64 * NW), 0, s, a, p.seg, p.slots,
+                     p.states, p.split, st, dec);
   return hipGetLastError();
 }
 
@@ -976,15 +1013,20 @@ SsmPlan ssm_plan(int nb, int T, int Hk, int HV, int K, int V, int N, bool varlen
   seg = seg < least ? least : seg;
   // nor two chunks alone: they cost less than two more launches (128 tokens x 8 heads
   // 16.2 us in one launch, 20.6 in three; 192 tokens 21.3 and 20.9)
-  // nor so many sequences that the join's launch would have 2^32 threads
+  // nor so many sequences that every work-group's look at their boundaries is what counts
   const bool join = (long long)N * HV * (K * V / 1024) < (1 << 24);
   if (seg >= T || T <= 128 || !join) seg = ((long long)T + 63) / 64 * 64;
   p.split = seg < T;
   p.seg = seg > 64 ? (int)seg : 64;
   p.slots = !p.split ? N : (varlen ? (int)(tokens / seg) + N : N * (int)((T + seg - 1) / seg));
-  const size_t state = (size_t)p.slots * HV * V * K * 4;
+  // Of packed sequences at most tokens / seg are longer than a segment, and each of
+  // them is cut into at most twice as many as it fills.
+  const long long full = p.split ? tokens / seg : 0;
+  p.joins = !varlen ? N : (int)(full < N ? full : N);
+  p.states = !varlen ? p.slots : (int)full + p.joins;
+  const size_t state = (size_t)p.states * HV * V * K * 4;
   p.decay_off = (state + 255) / 256 * 256;
-  p.bytes = p.split ? p.decay_off + ((size_t)p.slots * HV * 8 + 255) / 256 * 256 : 0;
+  p.bytes = p.split ? p.decay_off + ((size_t)p.states * HV * 8 + 255) / 256 * 256 : 0;
   return p;
 }
 

@@ -227,3 +227,23 @@ def test_sequences_past_the_joins_launch_are_not_split(L):
     few = L.ssm_chunk_fwd_workspace_bytes(1, 1 << 20, 8, 64, 128, 64, 1000, 1, 1)
     assert few > 0
     assert L.ssm_chunk_fwd_workspace_bytes(1, 1 << 20, 8, 64, 128, 64, 1 << 16, 1, 1) == 0
+
+
+@pytest.mark.parametrize("n,length,HV,V,K", [(200, 60, 64, 64, 128), (256, 100, 64, 64, 128), (1024, 64, 64, 64, 128),
+                                             (5000, 7, 32, 128, 128)])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_packed_workspace_does_not_grow_with_the_sequences(L, n, length, HV, V, K, dtype):
+    """Only sequences longer than a segment have states in the workspace: at most
+    twice the segments that the tokens fill, and no more than a segment has at
+    least (512 work-groups, half of them for the tails: 512 segment and head pairs
+    of the bound, 8 more bytes each for the log-decays)."""
+    got = binding.ssm_workspace_bytes(1, n * length, 1, HV, K, V, n, dtype, varlen=True)
+    assert 0 < got <= 2 * 512 * 2 * (V * K * 4 + 8) + 512
+    more = binding.ssm_workspace_bytes(1, n * length, 1, HV, K, V, 4 * n, dtype, varlen=True)
+    assert more <= got
+
+
+def test_workspace_of_one_packed_sequence_is_that_of_a_dense_one(L):
+    dense = binding.ssm_workspace_bytes(1, 8192, 1, 64, 128, 64, 1, torch.bfloat16)
+    packed = binding.ssm_workspace_bytes(1, 8192, 1, 64, 128, 64, 1, torch.bfloat16, varlen=True)
+    assert 0 < dense and 0 < packed <= 2 * dense

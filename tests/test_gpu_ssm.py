@@ -317,3 +317,25 @@ def test_step_at_rates_past_fp32(dtype):
         # elements below 2^-126 are 2^-149 apart: three roundings a token (D x, its product
         # with B, the sum), two tokens, half a step each
         close(f"state {dt}", pool, rh, 2.0 ** -20 * hm + store(F32, rh) + 6 * 2.0 ** -150)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_more_split_sequences_than_a_wave_has_lanes(dtype):
+    """70 sequences of two segments among short and empty ones: their states are
+    numbered over 64 sequences at a time; the workspace is as large as asked for."""
+    print(f"scan many split sequences {dtype}", flush=True)
+    seqs = [0, 5, 330] * 20 + [335, 1] * 30 + [3] * 70 + [322] * 20
+    T, Hk, HV, K, V = sum(seqs), 1, 1, 64, 64
+    p = ssm_inputs(1400, 1, T, Hk, HV, K, V, dtype, N=len(seqs))
+    p["dt_bias"] -= 3.0     # slow decays: the first segment's state matters in the second
+    nbytes = binding.ssm_workspace_bytes(1, T, Hk, HV, K, V, len(seqs), dtype, varlen=True)
+    seg = 320               # 2 sqrt(T) tokens, in chunks of 64
+    assert (seg - 64) ** 2 < 4 * T <= seg ** 2 and sum(n > seg for n in seqs) == 70
+    assert nbytes <= 2 * (T // seg) * (V * K * 4 + 8) + 512
+    ws = torch.full((nbytes + 4096,), 0xFF, dtype=torch.uint8, device=DEV)
+    y, ht = _run(p, cu_seqlens=torch.tensor(edges(seqs), dtype=torch.int64, device=DEV), workspace=ws[:nbytes])
+    torch.cuda.synchronize()
+    assert torch.all(ws[nbytes:] == 0xFF)
+    ry, mag, skip, rh, hm = ssm_ref(p, seqs)
+    close("y", y[0], ry, ssm_bound(dtype, ry, mag, skip))
+    close("ht", ht, rh, 512 * U * hm + 2.0 ** -20 * hm)
