@@ -140,8 +140,20 @@ __device__ __forceinline__ void emit(const Lane<T, W>& L, const float (&rows)[W]
     float q = 0.f;
 #pragma unroll
     for (int e = 0; e < 8; ++e) q = fmaf(y[e], y[e], q);
-    q = head_sum<NORM>(q);
-    const float f = L.norm ? __builtin_amdgcn_rsqf(q + eps) : 1.0f;
+    q = head_sum<NORM>(q) + eps;   // the same in all lanes of a head
+    // Squares that leave fp32's range (or its normal numbers, where the reciprocal
+    // root takes 0): once more from the head times a power of two, eps times its square.
+    if (L.norm && !(q >= 0x1p-100f && q <= 0x1p100f)) {
+      const float k = q < 1.0f ? 0x1p100f : 0x1p-70f;
+      q = 0.f;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        y[e] *= k;
+        q = fmaf(y[e], y[e], q);
+      }
+      q = head_sum<NORM>(q) + eps * k * k;
+    }
+    const float f = L.norm ? __builtin_amdgcn_rsqf(q) : 1.0f;
 #pragma unroll
     for (int e = 0; e < 8; ++e) y[e] *= f;
   }

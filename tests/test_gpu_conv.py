@@ -183,3 +183,32 @@ def test_conv_offsets_past_32_bits():
     assert not y[:, :-50].any()
     del x, y
     torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("norm_dim", [64, 128])
+@pytest.mark.parametrize("eps", [0.0, 1e-6])
+def test_norm_of_heads_whose_squares_leave_fp32(dtype, norm_dim, eps):
+    """Heads of 1e-30 to 1e37: the squares under- or overflow, the norms do not."""
+    print(f"conv norm of tiny and huge heads {dtype} {norm_dim} eps={eps}", flush=True)
+    size = [1e-30, 1e-21, 1e-19, 1.0, 1e18, 1e20, 1e30, 1e37]
+    B, T, sec = len(size), 3, (2 * norm_dim, norm_dim, 40)
+    x = (randn(1500, B, T, sum(sec)) * torch.tensor(size)[:, None, None]).to(dtype)
+    w = randn(1501, sum(sec), 2, dtype=dtype, scale=0.5)
+    outs = binding.causal_conv_fwd(d(x), d(w), activation=None, sections=sec, norm_dim=norm_dim, norm_sections=2,
+                                   norm_eps=eps)
+    torch.cuda.synchronize()
+    x64, w64 = f64(x), f64(w)
+    past = np.concatenate([np.zeros((B, 1, sum(sec))), x64[:, :-1]], 1)
+    y = w64[:, 0] * past + w64[:, 1] * x64
+    err = 3 * 2.0 ** -24 * (np.abs(w64[:, 0] * past) + np.abs(w64[:, 1] * x64))     # two products and their sum
+    at = 0
+    for i, (got, width) in enumerate(zip(outs, sec)):
+        r, e = y[..., at:at + width], err[..., at:at + width]
+        at += width
+        if i < 2:   # as conv_ref: the head's error over its norm, twice, and 2^-20
+            h, eh = (a.reshape(B, T, -1, norm_dim) for a in (r, e))
+            n = np.sqrt((h * h).sum(-1, keepdims=True) + eps)
+            e = (eh / n + np.abs(h) / n * (np.sqrt((eh * eh).sum(-1, keepdims=True)) / n + 2.0 ** -20)).reshape(r.shape)
+            r = (h / n).reshape(r.shape)
+        close(f"out{i}", got, r, e + store(dtype, r))
