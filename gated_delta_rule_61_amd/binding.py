@@ -722,7 +722,9 @@ def ssm_chunk_fwd(x: torch.Tensor, dt: torch.Tensor, Bm: torch.Tensor, Cm: torch
     into B = 1; rows behind the last boundary are left as they are.  ``h0``
     [N,HV,V,K] fp32 is the initial state.  Without softplus dt_t + dt_bias must
     not be negative.  ``out`` must not overlap an input.  A ``workspace`` (of
-    ``ssm_workspace_bytes``; else allocated) serves one call at a time."""
+    ``ssm_workspace_bytes``; else allocated) serves one call at a time.  With bf16
+    inputs y's last bits may differ with ``output_final_state``: a state that
+    nobody asks for is made from x rounded to bf16 after its weighting."""
     head, y, sizes, dev, code = _ssm_args(x, dt, Bm, Cm, A_log, D, z, dt_bias, dt_softplus, out)
     HV, K, V = sizes[3:]
     N, cu = _seqs(cu_seqlens, sizes[0], dev)

@@ -505,10 +505,14 @@ int gdn_conv_step(const void* x, long long x_batch, long long x_token, const voi
  *
  * Supported: bf16 or fp32 io, K and V in {64, 128}, HV a multiple of Hk,
  * chunk_size = 64; x, Bm, Cm, z and their strides in multiples of 16 bytes.
- * Sums, gates and states are fp32 or wider; with bf16 io the products that make
- * y take the state and the decayed scores rounded to bf16, those that make ht
- * lose nothing to fp32 (but for what is below 2^-126 of the weighted x or of its
- * last 16 bits, which the matrix cores take as 0).  Tokens are taken in chunks of 64 (from each sequence's
+ * Sums, gates and states are fp32 or wider.  With bf16 io the products that make
+ * y take the state and the decayed scores rounded to bf16.  Those that make ht, or
+ * the state behind a segment of a sequence that is split, take the weighted x as
+ * three bf16 terms and lose nothing to fp32 (but for what is below 2^-126 of the
+ * terms, which the matrix cores take as 0); those of a state that only y of the
+ * same segment reads take it rounded to bf16.  So y may differ within these
+ * roundings with ht asked for or not, and with what a sequence is packed among.
+ * Tokens are taken in chunks of 64 (from each sequence's
  * start) as matrix products: an infinity or NaN in x makes its channel's outputs
  * NaN from the beginning of its chunk on, where the recurrence would from its
  * token on; one in dt, Bm or Cm reaches the tokens the recurrence says.

@@ -339,3 +339,76 @@ def test_more_split_sequences_than_a_wave_has_lanes(dtype):
     ry, mag, skip, rh, hm = ssm_ref(p, seqs)
     close("y", y[0], ry, ssm_bound(dtype, ry, mag, skip))
     close("ht", ht, rh, 512 * U * hm + 2.0 ** -20 * hm)
+
+
+def _part(p, lens, seqs, heads):
+    """Sequences and heads of p (packed rows), each head with a group of its own; their lengths."""
+    e, per = edges(lens), p["x"].shape[2] // p["Bm"].shape[2]
+    rows = np.concatenate([np.arange(e[i], e[i + 1]) for i in seqs])
+    groups = [h // per for h in heads]
+    flat = lambda n: p[n].reshape(1, -1, *p[n].shape[2:])[:, rows]
+    q = {n: flat(n)[:, :, heads] for n in ("x", "dt", "z")} | {n: flat(n)[:, :, groups] for n in ("Bm", "Cm")}
+    q |= {n: p[n][heads] for n in ("A_log", "dt_bias", "D")} | {"h0": p["h0"][seqs][:, heads]}
+    return q, rows, [lens[i] for i in seqs]
+
+
+def _check_part(p, lens, dtype, y, ht, seqs, heads):
+    q, rows, ql = _part(p, lens, seqs, heads)
+    ry, mag, skip, rh, hm = ssm_ref(q, ql)
+    close("y", y.reshape(-1, *y.shape[2:])[rows][:, heads], ry, ssm_bound(dtype, ry, mag, skip))
+    if ht is not None:
+        close("ht", ht[seqs][:, heads], rh, 512 * U * hm + 2.0 ** -20 * hm)
+
+
+# (lengths or (B, T), Hk, HV, K, V, sequences and heads that are compared)
+LONG = [
+    ((8, 2100), 2, 8, 128, 64, [0, 7], [1, 6]),                      # two 64-wide heads a work-group
+    ((12, 2800), 2, 4, 128, 128, [0, 11], [0, 3]),                   # a 128-wide one
+    ((12, 3700), 1, 3, 64, 64, [3, 11], [0, 2]),                     # a 64-wide one (odd group)
+    ((12, 2800), 1, 4, 64, 128, [5], [1, 2]),
+    ((12, 3700), 3, 3, 128, 64, [11], [1]),
+    ([3900] * 7 + [3000, 0, 1, 64, 769, 384, 385, 0, 2000], 2, 4, 128, 128, [6, 7, 8, 9, 10, 11, 12, 13, 14, 15], [0, 2]),
+    ([3900] * 7 + [3000, 0, 1, 64, 769, 384, 385, 0, 2000], 2, 4, 64, 64, [6, 7, 8, 9, 10, 11, 12, 13, 14, 15], [1, 3]),
+]
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("case", LONG, ids=lambda c: f"{len(c[0])}seq-{c[1]}x{c[2]}-K{c[3]}V{c[4]}")
+def test_split_scan_of_long_segments(case, dtype):
+    """Segments of more chunks than a group of gates has (2 for two heads a
+    work-group, 4 for one), and slow decays: a token of the first chunk of a
+    segment still shows in the state behind it."""
+    lens, Hk, HV, K, V, seqs, heads = case
+    print(f"scan long segments {dtype} {Hk}x{HV} K={K} V={V}", flush=True)
+    dense = isinstance(lens, tuple)
+    B, T = lens if dense else (1, sum(lens))
+    lens = [T] * B if dense else lens
+    group = 2 if V == 64 and HV // Hk % 2 == 0 else 4
+    nbytes = binding.ssm_workspace_bytes(B, T, Hk, HV, K, V, len(lens), dtype, varlen=not dense)
+    states = nbytes // (HV * (V * K * 4 + 8))
+    if dense:   # B ceil(T / segment) states: no shorter segment makes so few
+        assert 2 <= states // B < T / (64 * group)
+    else:       # floor(T / segment) and that once more, or the number of sequences
+        full = states // 2 if states < 2 * len(lens) else states - len(lens)
+        assert 2 <= full and T / (full + 1) > 64 * group
+    p = ssm_inputs(1600, B, T, Hk, HV, K, V, dtype, N=len(lens))
+    p["dt_bias"] -= 3.0
+    y, ht = _run(p, cu_seqlens=None if dense else torch.tensor(edges(lens), dtype=torch.int64, device=DEV))
+    torch.cuda.synchronize()
+    _check_part(p, lens, dtype, y, ht, seqs, heads)
+
+
+@pytest.mark.parametrize("B,T,HV", [(64, 640, 16), (2, 1100, 4)])
+def test_bf16_y_with_and_without_the_final_state(B, T, HV):
+    """Not split (ten chunks) and split: within the bound both times, whatever the
+    number of terms that the state takes."""
+    print(f"scan bf16 without ht B={B} T={T}", flush=True)
+    p = ssm_inputs(1700, B, T, 1, HV, 128, 64, BF)
+    p["dt_bias"] -= 3.0
+    assert (binding.ssm_workspace_bytes(B, T, 1, HV, 128, 64, B, BF) == 0) == (B == 64)
+    y, ht = _run(p)
+    bare, none = _run(p, output_final_state=False)
+    torch.cuda.synchronize()
+    assert none is None
+    _check_part(p, [T] * B, BF, y, ht, [0, B - 1], [0, HV - 1])
+    _check_part(p, [T] * B, BF, bare, None, [0, B - 1], [0, HV - 1])
