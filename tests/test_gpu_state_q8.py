@@ -151,3 +151,32 @@ def test_cache_offsets_past_32_bits():
     assert not sc[~named].any()
     del q8
     torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("form", ["int8", "e4m3"])
+@pytest.mark.parametrize("dtype", [torch.float32, BF])
+@pytest.mark.parametrize("src,dst,pool,entries", [
+    ([2, 0, 2, 1], [5, 1, 0, 3], 3, 6),           # one slot into two entries, any order
+    ([0, -1, 3, 1, 2], [0, 1, 2, 6, -2], 3, 6),   # slots and entries outside their arrays, on either side
+    ([2, 0, -7], None, 3, 5),                     # targets 0, 1, 2 of 5
+    (None, [4, 2, 0], 3, 5),
+    (None, [1, 9], 3, 2),
+    (None, None, 4, 3),
+    ([0, 2147483647, -2147483648], [2, 0, 1], 3, 3),
+])
+def test_load_indices(form, dtype, src, dst, pool, entries):
+    """Slot src[i] into entry dst[i] where both exist, every other entry as it was."""
+    print(f"q8 load indices {form} {dtype} {src} {dst}", flush=True)
+    x = randn(6, pool, 2, 64, 128)
+    t = lambda v: None if v is None else torch.tensor(v, dtype=torch.int32, device=DEV)
+    q8, sc = _store(x, form, pool)
+    out = torch.full((entries, 2, 64, 128), 11.0, dtype=dtype, device=DEV)
+    want = out.clone()
+    value = (q8.float() * sc[..., None]).to(dtype)
+    n = len(src if src is not None else dst if dst is not None else range(entries))
+    for s, e in zip(src or range(n), dst or range(n)):
+        if 0 <= s < pool and 0 <= e < entries:
+            want[e] = value[s]
+    got = binding.state_load_q8(q8, sc, out, t(src), t(dst))
+    torch.cuda.synchronize()
+    assert got is out and torch.equal(bits(out), bits(want))
