@@ -7,7 +7,8 @@ import torch
 
 import oracle
 from gated_delta_rule_61_amd import binding, workloads
-from tests.mixer_cases import BF, DEV, EPS, bits, close, conv_ref, d, f64, randn, same, ssm_inputs, store
+from tests.mixer_cases import (BF, DEV, EPS, bits, close, conv_ref, d, f64, randn, same, ssm_bound, ssm_inputs, ssm_ref,
+                               store)
 from tests.test_gpu_graphs import _capture, _other_work
 from tests.tolerance import check
 
@@ -214,3 +215,43 @@ def test_profile_stages():
     prof = binding.profile_read()
     assert prof["conv"][1] == 2 and prof["ssm_scan"][1] == 1 and prof["ssm_step"][1] == 1 and prof["state_q8"][1] == 2
     assert all(prof[s][0] > 0 for s in ("conv", "ssm_scan", "ssm_step", "state_q8"))
+
+
+def test_a_prompt_that_goes_on_from_the_cache_element_by_element():
+    """The second part of a prompt and its single tokens, from a state that was read
+    back from the cache: every y and state against the oracle on the convolution's
+    own outputs and that state, with the element-wise bounds of the scan and step."""
+    print("prefix cache chain, element by element", flush=True)
+    N, Hk, HV, K, V = 3, 2, 4, 64, 64
+    p = _layer_inputs(60, N, 250, Hk, HV, K, V)
+    q = {n: d(p[n]) for n in ("w", "bias", "A_log", "D", "dt_bias")}
+    part = lambda lo, hi: {n: d(p[n][:, lo:hi].contiguous()) for n in ("xbc", "z", "dt")}
+    dims, sec = (Hk, HV, K, V), (HV * V, Hk * K, Hk * K)
+    conv = torch.zeros((N, 3, sum(sec)), dtype=BF, device=DEV)
+    _, h1 = _layer(part(0, 90), q, *dims, conv)
+    slots = torch.tensor([4, 0, 3], dtype=torch.int32, device=DEV)
+    for form in (torch.int8, torch.float8_e4m3fn):
+        q8, sc = torch.zeros((5, HV, V, K), device=DEV).to(form), torch.zeros((5, HV, V), device=DEV)
+        binding.state_store_q8(h1, q8, sc, dst_indices=slots)
+        back = binding.state_load_q8(q8, sc, torch.empty_like(h1), src_indices=slots)
+        c, one = conv.clone(), torch.ones(N, dtype=torch.int32, device=DEV)
+        mid = binding.causal_conv_fwd(part(90, 247)["xbc"], q["w"], q["bias"], sections=sec, state=c.clone(), has_state=one)
+        y2, h2 = _layer(part(90, 247), q, *dims, c, h0=back, has=one)
+        pool = h2.clone()
+        end = binding.causal_conv_step(part(247, 250)["xbc"], q["w"], q["bias"], c.clone(), sections=sec)
+        y3 = _layer(part(247, 250), q, *dims, c, pool=pool)
+        torch.cuda.synchronize()
+
+        def ref(xbc, lo, hi, h0):
+            x, B, C = (t.cpu() for t in xbc)
+            r = dict(x=x.unflatten(-1, (HV, V)), Bm=B.unflatten(-1, (Hk, K)), Cm=C.unflatten(-1, (Hk, K)),
+                     z=p["z"][:, lo:hi], dt=p["dt"][:, lo:hi], h0=h0.cpu(), **{n: p[n] for n in ("A_log", "D", "dt_bias")})
+            return ssm_ref(r, [hi - lo] * N)
+
+        ry, mag, skip, rh, hm = ref(mid, 90, 247, back)
+        close("y of the second part", y2.reshape(-1, HV, V), ry, ssm_bound(BF, ry, mag, skip))
+        close("its state", h2, rh, 512 * 2.0 ** -24 * hm + 2.0 ** -20 * hm)
+        ry, mag, skip, rh, hm = ref(end, 247, 250, h2)
+        close("y of the single tokens", y3.reshape(-1, HV, V), ry,
+              512 * 2.0 ** -24 * mag + 2.0 ** -20 * (mag + skip) + store(BF, ry))
+        close("the pool", pool, rh, 2.0 ** -20 * hm + store(torch.float32, rh))
