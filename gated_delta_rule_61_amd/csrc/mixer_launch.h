@@ -66,7 +66,7 @@ struct SsmArgs {
 struct SsmPlan {
   int nh, seg, slots, joins, states;
   bool split;                   // whether a sequence can have more than one segment
-  size_t decay_off, bytes;      // workspace: states first, then the log2-decays
+  size_t decay_off, table_off, bytes;   // workspace: states, log2-decays, the table of split sequences
 };
 SsmPlan ssm_plan(int nb, int T, int Hk, int HV, int K, int V, int N, bool varlen, bool bf16);
 hipError_t launch_ssm_fwd(const SsmArgs& a, hipStream_t s);

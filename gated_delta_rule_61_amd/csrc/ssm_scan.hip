@@ -359,26 +359,25 @@ struct Segment {
   int len;               // tokens of the sequence
 };
 
-// Packed sequences are looked at 64 at a time, one a lane.  Only sequences of two
-// segments or more have states in the workspace, one a segment.
-struct Packed {
-  long long b0;    // first token
-  int len, segs;   // tokens and segments, 0 behind the last sequence
-  int states;      // segments, if there are two or more
-  __device__ __forceinline__ Packed(const SsmArgs& a, int seg, int n, int lane) {
-    long long b1 = 0;
-    b0 = 0;
-    if (n < a.N) {
-      b0 = a.cu[n];
-      b1 = a.cu[n + 1];
-      b0 = b0 < 0 ? 0 : (b0 > a.T ? a.T : b0);
-      b1 = b1 < b0 ? b0 : (b1 > a.T ? a.T : b1);
-    }
+// Tokens [b0, b0 + len) of packed sequence n.
+struct Bounds {
+  long long b0;
+  int len;
+  __device__ __forceinline__ Bounds(const SsmArgs& a, int n) {
+    b0 = a.cu[n];
+    long long b1 = a.cu[n + 1];
+    b0 = b0 < 0 ? 0 : (b0 > a.T ? a.T : b0);
+    b1 = b1 < b0 ? b0 : (b1 > a.T ? a.T : b1);
     len = (int)(b1 - b0);
-    segs = n < a.N ? (len > seg ? (len + seg - 1) / seg : 1) : 0;
-    states = segs > 1 ? segs : 0;
   }
 };
+
+// States of packed sequence n in the workspace: one a segment, none for a single one.
+__device__ __forceinline__ int states_of(const SsmArgs& a, int seg, int n) {
+  if (n >= a.N) return 0;
+  const int len = Bounds(a, n).len;
+  return len > seg ? (len + seg - 1) / seg : 0;
+}
 
 // Inclusive sum over the lanes, and that of all.
 struct LaneSum {
@@ -394,13 +393,24 @@ struct LaneSum {
   }
 };
 
+// A packed sequence that is split, written by the join for the last launch: its
+// number, its first state and its states (0: there is no such sequence).
+struct alignas(16) SplitSeq {
+  int n, state, states, unused;
+};
+
 // The segment and head tile of work-group `wg` of 8 XCDs: the tiles of a segment
 // (which share B and C) run next to each other on one XCD, and every XCD gets an
 // equal run of the segments that there are (packed sequences seldom fill the slots
-// the host counts).  OUT: of all segments; otherwise of those with a state.  Same
-// result in every lane; n < 0: none.
+// the host counts).  Same result in every lane; n < 0: none.
+// First launch (few work-groups): the segments with a state, by the boundaries of all
+// sequences, 64 at a time.  Last launch (one work-group for every sequence and tile at
+// least): all segments, by the table of the split sequences, which are few; looking
+// through all boundaries here too took 4.2 ms for 4096 prompts of 64 tokens x 16
+// heads, this 0.64 ms.
 template <bool OUT>
-__device__ __forceinline__ Segment find_segment(const SsmArgs& a, int seg, int slots, int tiles, int wg, int lane,
+__device__ __forceinline__ Segment find_segment(const SsmArgs& a, int seg, int slots, bool split,
+                                                const SplitSeq* table, int joins, int tiles, int wg, int lane,
                                                 int& tile) {
   Segment g;
   g.n = -1;
@@ -424,31 +434,64 @@ __device__ __forceinline__ Segment find_segment(const SsmArgs& a, int seg, int s
     g.len = a.T;
     return g;
   }
-  auto dealt = [](const Packed& p) { return OUT ? p.segs : p.states; };
-  Packed p(a, seg, lane, lane);
-  LaneSum sum(dealt(p), lane);
-  int used = sum.all;
-  for (int base = 64; base < a.N; base += 64) used += LaneSum(dealt(Packed(a, seg, base + lane, lane)), lane).all;
-  if (!deal(used < slots ? used : slots)) return g;   // boundaries out of order may claim more
-  int run = 0, states = 0;   // of the sequences before these 64
-  for (int base = 0; base < a.N; base += 64) {
-    if (base > 0) {
-      p = Packed(a, seg, base + lane, lane);
-      sum = LaneSum(dealt(p), lane);
+  if constexpr (OUT) {
+    int used = a.N;
+    SplitSeq e{};
+    auto read = [&](int base) {
+      e.states = 0;
+      if (base + lane < joins) e = table[base + lane];
+    };
+    if (split) {
+      for (int base = 0; base < joins; base += 64) {
+        read(base);
+        used += LaneSum(e.states > 1 ? e.states - 1 : 0, lane).all;
+      }
     }
-    const LaneSum st = OUT ? LaneSum(p.states, lane) : sum;
-    if (slot < run + sum.all) {
-      const int l = __ffsll((unsigned long long)__ballot(sum.incl > slot - run)) - 1;
-      g.n = base + l;
-      g.j = slot - run - __builtin_amdgcn_readlane(sum.incl - dealt(p), l);
-      g.state = states + __builtin_amdgcn_readlane(st.incl - p.states, l) + g.j;
-      g.start = __builtin_amdgcn_readlane((int)p.b0, l);
-      g.len = __builtin_amdgcn_readlane(p.len, l);
-      return g;
+    if (!deal(used < slots ? used : slots)) return g;   // boundaries out of order may claim more
+    int n = slot;
+    if (split) {
+      for (int base = 0; base < joins; base += 64) {
+        if (joins > 64) read(base);
+        // segments of the sequences in front of a split one: one each, and the others
+        // (states less sequences) of the split ones among them
+        const int first = e.n + e.state - (base + lane);
+        const unsigned long long before = __ballot(e.states > 0 && first <= slot);
+        if (before == 0) break;
+        const int l = 63 - __clzll((long long)before);
+        const int at = slot - __builtin_amdgcn_readlane(first, l), of = __builtin_amdgcn_readlane(e.states, l);
+        n = __builtin_amdgcn_readlane(e.n, l) + (at < of ? 0 : at - of + 1);
+        g.j = at < of ? at : 0;
+        g.state = __builtin_amdgcn_readlane(e.state, l) + g.j;
+      }
     }
-    run += sum.all;
-    states += st.all;
+    if (n < 0 || n >= a.N) return g;
+    g.n = n;
+  } else {
+    int st = states_of(a, seg, lane);
+    LaneSum sum(st, lane);
+    int used = sum.all;
+    for (int base = 64; base < a.N; base += 64) used += LaneSum(states_of(a, seg, base + lane), lane).all;
+    if (!deal(used < slots ? used : slots)) return g;
+    int run = 0;   // of the sequences before these 64
+    for (int base = 0; base < a.N; base += 64) {
+      if (base > 0) {
+        st = states_of(a, seg, base + lane);
+        sum = LaneSum(st, lane);
+      }
+      if (slot < run + sum.all) {
+        const int l = __ffsll((unsigned long long)__ballot(sum.incl > slot - run)) - 1;
+        g.n = base + l;
+        g.j = slot - run - __builtin_amdgcn_readlane(sum.incl - st, l);
+        g.state = slot;
+        break;
+      }
+      run += sum.all;
+    }
+    if (g.n < 0) return g;
   }
+  const Bounds s(a, g.n);
+  g.start = s.b0;
+  g.len = s.len;
   return g;
 }
 
@@ -457,8 +500,8 @@ __device__ __forceinline__ Segment find_segment(const SsmArgs& a, int seg, int s
 // launch of a split call, which writes segment states and log-decays.
 template <typename T, int K, int V, int NH, bool OUT>
 __global__ __launch_bounds__(64 * NW, sizeof(T) == 2 ? 2 : 1) void ssm_scan_kernel(
-    SsmArgs a, int seg, int slots, int states, bool split, float* __restrict__ seg_state,
-    double* __restrict__ seg_decay) {
+    SsmArgs a, int seg, int slots, int states, bool split, const SplitSeq* __restrict__ table, int joins,
+    float* __restrict__ seg_state, double* __restrict__ seg_decay) {
   constexpr int CW = NH * V;            // columns of the work-group
   constexpr int NB = CW / 16 / NW;      // 16-column blocks of a wave
   constexpr int KB = K / 16, KS = K / 32;
@@ -479,7 +522,8 @@ __global__ __launch_bounds__(64 * NW, sizeof(T) == 2 ? 2 : 1) void ssm_scan_kern
   const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int r = lane & 15, q = lane >> 4;
   int tile;
-  const Segment sg = find_segment<OUT>(a, seg, OUT ? slots : states, a.HV / NH, blockIdx.x, lane, tile);
+  const Segment sg = find_segment<OUT>(a, seg, OUT ? slots : states, split, table, joins, a.HV / NH, blockIdx.x,
+                                       lane, tile);
   if (sg.n < 0) return;
   const int hv0 = tile * NH;
   const int hk = hv0 / (a.HV / a.Hk);
@@ -898,7 +942,8 @@ __global__ __launch_bounds__(64 * NW, sizeof(T) == 2 ? 2 : 1) void ssm_scan_kern
 // off 5 segments a prompt and added 37 to 16 (their reads are serial and repeated).
 __global__ __launch_bounds__(256) void ssm_join_kernel(SsmArgs a, int seg, int states, int blocks_per_head,
                                                        float* __restrict__ seg_state,
-                                                       const double* __restrict__ seg_decay) {
+                                                       const double* __restrict__ seg_decay,
+                                                       SplitSeq* __restrict__ table) {
   const int lane = threadIdx.x & 63;
   const int mh = blockIdx.x / blocks_per_head;
   const int part = blockIdx.x - mh * blocks_per_head;
@@ -909,26 +954,27 @@ __global__ __launch_bounds__(256) void ssm_join_kernel(SsmArgs a, int seg, int s
     slot0 = n * segs;
   } else {
     int before = 0;   // split sequences before these 64
-    for (int base = 0;; base += 64) {
-      if (base >= a.N) return;
-      const Packed p(a, seg, base + lane, lane);
-      const LaneSum sum(p.states, lane);
-      const unsigned long long cut = __ballot(p.states > 0);
+    n = -1;
+    for (int base = 0; base < a.N; base += 64) {
+      const int st = states_of(a, seg, base + lane);
+      const LaneSum sum(st, lane);
+      const unsigned long long cut = __ballot(st > 0);
       if (m < before + __popcll(cut)) {
         const int rank = before + __popcll(cut & ((1ULL << lane) - 1));
-        const int l = __ffsll((unsigned long long)__ballot(p.states > 0 && rank == m)) - 1;
+        const int l = __ffsll((unsigned long long)__ballot(st > 0 && rank == m)) - 1;
         n = base + l;
-        segs = __builtin_amdgcn_readlane(p.states, l);
+        segs = __builtin_amdgcn_readlane(st, l);
         slot0 += __builtin_amdgcn_readlane(sum.incl, l) - segs;
         break;
       }
       before += __popcll(cut);
       slot0 += sum.all;
     }
+    // boundaries out of order may claim more states than there are
+    if (n < 0 || slot0 < 0 || slot0 >= states) segs = 0;
+    else if (segs > states - slot0) segs = states - slot0;
+    if (hv == 0 && part == 0 && threadIdx.x == 0) table[m] = SplitSeq{n, slot0, segs, 0};
   }
-  // boundaries out of order may claim more states than there are
-  if (slot0 < 0 || slot0 >= states) return;
-  if (segs > states - slot0) segs = states - slot0;
   if (segs < 2) return;
   const int own_states = segs - (a.ht ? 0 : 1);
   const size_t VK = (size_t)a.V * a.K, head = (size_t)a.HV * VK;
@@ -967,20 +1013,22 @@ hipError_t launch_t(const SsmArgs& a, const SsmPlan& p, hipStream_t s) {
   const int tiles = a.HV / NH;
   auto grid = [&](int slots) { return dim3((unsigned)((slots * tiles + 7) / 8 * 8)); };
   float* st = reinterpret_cast<float*>(a.workspace);
-  double* dec = p.split ? reinterpret_cast<double*>(reinterpret_cast<char*>(a.workspace) + p.decay_off) : nullptr;
+  char* const ws = reinterpret_cast<char*>(a.workspace);
+  double* dec = p.split ? reinterpret_cast<double*>(ws + p.decay_off) : nullptr;
+  SplitSeq* table = p.split ? reinterpret_cast<SplitSeq*>(ws + p.table_off) : nullptr;
   if (p.split) {
     hipLaunchKernelGGL((ssm_scan_kernel<T, K, V, NH, false>), grid(p.states), dim3(64 * NW), 0, s, a, p.seg, p.slots,
-                       p.states, true, st, dec);
+                       p.states, true, table, 0, st, dec);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     constexpr int per_head = K * V / 1024;
     hipLaunchKernelGGL(ssm_join_kernel, dim3((unsigned)((long long)p.joins * a.HV * per_head)), dim3(256), 0, s, a,
-                       p.seg, p.states, per_head, st, dec);
+                       p.seg, p.states, per_head, st, dec, table);
     e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
   hipLaunchKernelGGL((ssm_scan_kernel<T, K, V, NH, true>), grid(p.slots), dim3(64 * NW), 0, s, a, p.seg, p.slots,
-                     p.states, p.split, st, dec);
+                     p.states, p.split, table, p.joins, st, dec);
   return hipGetLastError();
 }
 
@@ -1013,20 +1061,21 @@ SsmPlan ssm_plan(int nb, int T, int Hk, int HV, int K, int V, int N, bool varlen
   seg = seg < least ? least : seg;
   // nor two chunks alone: they cost less than two more launches (128 tokens x 8 heads
   // 16.2 us in one launch, 20.6 in three; 192 tokens 21.3 and 20.9)
-  // nor so many sequences that every work-group's look at their boundaries is what counts
+  // nor so many sequences that the first launch's look at their boundaries is what counts
   const bool join = (long long)N * HV * (K * V / 1024) < (1 << 24);
   if (seg >= T || T <= 128 || !join) seg = ((long long)T + 63) / 64 * 64;
   p.split = seg < T;
   p.seg = seg > 64 ? (int)seg : 64;
   p.slots = !p.split ? N : (varlen ? (int)(tokens / seg) + N : N * (int)((T + seg - 1) / seg));
-  // Of packed sequences at most tokens / seg are longer than a segment, and each of
-  // them is cut into at most twice as many as it fills.
-  const long long full = p.split ? tokens / seg : 0;
-  p.joins = !varlen ? N : (int)(full < N ? full : N);
-  p.states = !varlen ? p.slots : (int)full + p.joins;
+  // A packed sequence that is split has seg + 1 tokens or more, and of n such with L
+  // tokens in all the sum of ceil(length / seg) is at most (L - n) / seg + n.
+  const long long most = p.split && varlen ? tokens / (seg + 1) : N;
+  p.joins = (int)(most < N ? most : N);
+  p.states = !p.split || !varlen ? p.slots : (int)((tokens - p.joins) / seg) + p.joins;
   const size_t state = (size_t)p.states * HV * V * K * 4;
   p.decay_off = (state + 255) / 256 * 256;
-  p.bytes = p.split ? p.decay_off + ((size_t)p.states * HV * 8 + 255) / 256 * 256 : 0;
+  p.table_off = p.decay_off + ((size_t)p.states * HV * 8 + 255) / 256 * 256;
+  p.bytes = p.split ? p.table_off + (varlen ? ((size_t)p.joins * sizeof(SplitSeq) + 255) / 256 * 256 : 0) : 0;
   return p;
 }
 

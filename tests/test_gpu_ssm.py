@@ -412,3 +412,50 @@ def test_bf16_y_with_and_without_the_final_state(B, T, HV):
     assert none is None
     _check_part(p, [T] * B, BF, y, ht, [0, B - 1], [0, HV - 1])
     _check_part(p, [T] * B, BF, bare, None, [0, B - 1], [0, HV - 1])
+
+
+def test_time_does_not_grow_with_the_square_of_the_sequences():
+    """Eight times the packed sequences take about eight times as long (not 64)."""
+    print("scan of 2048 and 16384 sequences", flush=True)
+    best = []
+    for n in (2048, 16384):
+        p = {k: d(v) for k, v in ssm_inputs(1800, 1, 8 * n, 1, 4, 128, 64, BF, N=1, h0=False).items()}
+        cu = torch.arange(0, 8 * n + 1, 8, dtype=torch.int64, device=DEV)
+        run = lambda: _run(p, cu_seqlens=cu, output_final_state=False)
+        run()
+        a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        times = []
+        for _ in range(5):
+            a.record()
+            run()
+            b.record()
+            torch.cuda.synchronize()
+            times.append(a.elapsed_time(b))
+        best.append(min(times))
+    print(f"{best[0]:.3f} and {best[1]:.3f} ms", flush=True)
+    assert best[1] < 20 * best[0]
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_long_prompts_among_thousands_of_short_ones(dtype):
+    """Split sequences first, last and among 5000 of 8 tokens, whose bits are those
+    of a dense batch of them; the long ones against the oracle."""
+    print(f"scan of thousands of sequences {dtype}", flush=True)
+    long = {0: 1500, 1: 700, 2600: 2000, 5003: 1200}
+    lens = [long.get(i, 8) for i in range(5004)]
+    T, HV, K, V = sum(lens), 4, 64, 64
+    p = ssm_inputs(1900, 1, T, 1, HV, K, V, dtype, N=len(lens))
+    e = edges(lens)
+    assert binding.ssm_workspace_bytes(1, T, 1, HV, K, V, len(lens), dtype, varlen=True) > 0
+    y, ht = _run(p, cu_seqlens=torch.tensor(e, dtype=torch.int64, device=DEV))
+    short = [i for i in range(len(lens)) if i not in long]
+    rows = torch.tensor([list(range(e[i], e[i + 1])) for i in short])
+    q = {n: (p[n][0, rows] if n in ("x", "dt", "Bm", "Cm", "z") else p[n][short] if n == "h0" else p[n]) for n in p}
+    ys, hs = _run(q)
+    torch.cuda.synchronize()
+    same([y[0, d(rows)], ht[short]], [ys, hs], "short sequences")
+    for i in long:
+        if i == 2600:
+            _check_part(p, lens, dtype, y, ht, [i], [0, 1, 2, 3])
+        else:
+            _check_part(p, lens, dtype, y, ht, [i], [2])
