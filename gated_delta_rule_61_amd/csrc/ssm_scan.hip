@@ -32,17 +32,20 @@
 // order, and the third starts each segment from the state behind the one before.
 // That reads x and B twice but moves no per-chunk states.
 //
-// Measured (bf16, K = 128).  One prompt of 8192 tokens x 64 heads of 64, gated:
-// launches of 42 + 13 + 73 us, 125 us a call from a loop for 209 MB (41 us at a large
-// copy's 5.1 TB/s).  Eight packed prompts of 5003 tokens, 32 heads of 128, initial and
-// final states: 31 + 12 + 50 us, 84 a call, 136 MB (27 us).  The same 8192 tokens as
-// 16 prompts, one launch: 88 us a call.  fp32, 4096 tokens x 32 heads of 64: 113 us.
+// Measured (bf16, K = 128; a call's time from captured calls over three inputs in turn,
+// the launches' from a kernel trace of warm calls, which adds up to 4 %).  One prompt
+// of 8192 tokens x 64 heads of 64, gated: launches of 38 + 13 + 70 us, 118 a call for
+// 209 MB (41 us at a large copy's 5.1 TB/s).  Eight packed prompts of 5003 tokens, 32
+// heads of 128, initial and final states: 31 + 12 + 49 us, 92 a call, 136 MB (27 us).
+// The same 8192 tokens as 16 prompts, one launch: 82 us a call.  fp32, 4096 tokens x 32
+// heads of 64: 31 + 8 + 80 us, 114 a call, 106 MB (21 us; its products take about 56).
 // What bounds it is no one unit: of the last launch's cycles the vector ALU issues in
-// 43 %, LDS in 21 % with 12 % more of bank conflicts (the transposing reads and the
+// 41 %, LDS in 19 % with 11 % more of bank conflicts (the transposing reads and the
 // stores of M take one half of every 16-byte unit at a time, so half of the banks), the
-// matrix cores work in 14 %, between three barriers a chunk.  Twice the waves gained
-// nothing, nor did a higher wave priority for the products.  The first launch takes 16
-// us without its state update, 33 with one bf16 term of three.
+// matrix cores work in 13 %, between three barriers a chunk: with two waves a SIMD the
+// latencies of the tiles and of z are only partly hidden.  Twice the waves gained
+// nothing, nor did a higher wave priority for the products.  The first launch takes 13
+// us without its state update, 29 with one bf16 term of three.
 //
 // Precision.  Gate sums are taken in 64 bits, over log2-decays held at -160 a
 // token or more (2^-160 is 0 in fp32 already), so that with bf16 io an fp32 G is
@@ -51,6 +54,10 @@
 // segment's state handed on) is formed from the exact products of B with the
 // scaled x as three bf16 terms (24 bits); the state that only feeds this
 // segment's bf16 y takes one term, and S and M are rounded to bf16 as operands.
+// (x, B and C may be of any size, so fp16 with its 11 bits does not do; a second term
+// of S and M would cost half again of the products and 16 KiB more for M, with which
+// two work-groups no longer fit a CU.)  y of the workloads above is off by 0.0018 and
+// 0.0019 of its norm against 64 bits, of which storing y as bf16 makes 0.0017.
 
 #include <math.h>
 
@@ -267,8 +274,9 @@ __device__ __forceinline__ void wait_vm() {
 }
 
 // Fragments are read from LDS one product ahead of their use: left alone, the compiler
-// has every product wait for its own (the long prompt above 129 -> 125 us, the packed
-// ones 87 -> 84).  LDS accesses stay on their side of this, everything else may cross.
+// has every product wait for its own (200 packed prompts of 60 tokens x 64 heads 282 ->
+// 278 us, 100 tokens x 8 heads 16.3 -> 16.0, the long prompt above the same, the packed
+// ones 91 -> 92).  LDS accesses stay on their side of this, everything else may cross.
 __device__ __forceinline__ void ahead() { __builtin_amdgcn_sched_barrier(1); }
 
 __device__ __forceinline__ float ex2(float x) { return __builtin_amdgcn_exp2f(x); }
@@ -937,7 +945,7 @@ __global__ __launch_bounds__(64 * NW, sizeof(T) == 2 ? 2 : 1) void ssm_scan_kern
 // nothing where ht is not asked for).
 // A thread owns four elements of a (sequence, head) and walks down its segments,
 // the loads of four in flight together.  Memory-bound: every state once in and out
-// (16 segments x 64 heads of 64 x 128: 67 MB in 13 us, 5.2 TB/s).  Each segment's
+// (16 segments x 64 heads of 64 x 128: 67 MB in 12.5 us, 5.4 TB/s).  Each segment's
 // work-groups joining what lies before them instead, in the last launch, took 5 us
 // off 5 segments a prompt and added 37 to 16 (their reads are serial and repeated).
 __global__ __launch_bounds__(256) void ssm_join_kernel(SsmArgs a, int seg, int states, int blocks_per_head,
@@ -1048,11 +1056,11 @@ SsmPlan ssm_plan(int nb, int T, int Hk, int HV, int K, int V, int N, bool varlen
   const long long tokens = (long long)nb * T;
   const long long tiles = HV / p.nh;
   // One round of work-groups on 256 CUs: two a CU, one with fp32 tiles (bf16, one
-  // prompt of 8192 tokens x 64 heads: 256 work-groups 149 us, 512 124, 768 149, 1024
-  // 145).  But no segment shorter than 2 sqrt(T) tokens: halving the segments
+  // prompt of 8192 tokens x 64 heads: 256 work-groups 148 us, 512 117, 768 144, 1024
+  // 140; fp32, 4096 tokens x 32 heads: 128 195, 256 116, 512 123).  But no segment shorter than 2 sqrt(T) tokens: halving the segments
   // saves two launches the half of their chunks and costs the join as many steps
-  // (2048 tokens x 32 heads: 64-token segments 41 us, 128 36, 256 46; 700 x 16
-  // heads: 64 26, 128 29, 256 40).
+  // (2048 tokens x 32 heads: 64-token segments 41 us, 128 37, 256 47; 700 x 16
+  // heads: 64 25, 128 28, 256 40).
   const long long want = bf16 ? 512 : 256;
   // packed sequences end in half a segment on average, up to half of the work-groups
   const long long tails = !varlen ? 0 : tiles * N < want ? tiles * N / 2 : want / 2;
@@ -1060,7 +1068,7 @@ SsmPlan ssm_plan(int nb, int T, int Hk, int HV, int K, int V, int N, bool varlen
   const long long least = ((long long)(2.0 * sqrt((double)T)) + 63) / 64 * 64;
   seg = seg < least ? least : seg;
   // nor two chunks alone: they cost less than two more launches (128 tokens x 8 heads
-  // 16.2 us in one launch, 20.6 in three; 192 tokens 21.3 and 20.9)
+  // 16.1 us in one launch, 18.7 in three; 192 tokens 21.7 and 19.2)
   // nor so many sequences that the first launch's look at their boundaries is what counts
   const bool join = (long long)N * HV * (K * V / 1024) < (1 << 24);
   if (seg >= T || T <= 128 || !join) seg = ((long long)T + 63) / 64 * 64;

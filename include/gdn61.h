@@ -512,10 +512,10 @@ int gdn_conv_step(const void* x, long long x_batch, long long x_token, const voi
  * terms, which the matrix cores take as 0); those of a state that only y of the
  * same segment reads take it rounded to bf16.  So y may differ within these
  * roundings with ht asked for or not, and with what a sequence is packed among.
- * Tokens are taken in chunks of 64 (from each sequence's
- * start) as matrix products: an infinity or NaN in x makes its channel's outputs
- * NaN from the beginning of its chunk on, where the recurrence would from its
- * token on; one in dt, Bm or Cm reaches the tokens the recurrence says.
+ * Tokens are taken in chunks of 64 (from each sequence's start) as matrix
+ * products: an infinity or NaN in x makes its channel's outputs NaN from the
+ * beginning of its chunk on, where the recurrence would from its token on; one in
+ * dt, Bm or Cm reaches the tokens the recurrence says.
  * Fewer than 2^24 (64-token chunk or sequence, head) pairs.  Calls that share a
  * workspace (captured graphs too) must not run at the same time.  Allocates
  * nothing; asynchronous on `stream`.
