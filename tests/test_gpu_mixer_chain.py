@@ -255,3 +255,81 @@ def test_a_prompt_that_goes_on_from_the_cache_element_by_element():
         close("y of the single tokens", y3.reshape(-1, HV, V), ry,
               512 * 2.0 ** -24 * mag + 2.0 ** -20 * (mag + skip) + store(BF, ry))
         close("the pool", pool, rh, 2.0 ** -20 * hm + store(torch.float32, rh))
+
+
+def test_graph_replays_with_other_boundaries():
+    """A captured packed call (the host never reads the boundaries): replayed with
+    other sequences, more, fewer or none of them split, and with none at all."""
+    print("mixer graph, other boundaries", flush=True)
+    T, N, Hk, HV, K, V = 1700, 7, 1, 2, 64, 64
+    p = _layer_inputs(110, 1, T, Hk, HV, K, V)
+    s, q = {n: d(p[n]) for n in ("xbc", "z", "dt")}, {n: d(p[n]) for n in ("w", "bias", "A_log", "D", "dt_bias")}
+    sec = (HV * V, Hk * K, Hk * K)
+    h0, conv0 = d(randn(111, N, HV, V, K)), d(randn(112, N, 3, sum(sec), dtype=BF))
+    has = torch.tensor([1, 0, 1, 1, 0, 1, 0], dtype=torch.int32, device=DEV)
+    cu, conv = torch.zeros(N + 1, dtype=torch.int64, device=DEV), conv0.clone()
+    outs = tuple(torch.zeros((1, T, w), dtype=BF, device=DEV) for w in sec)
+    y = torch.zeros((1, T, HV, V), dtype=BF, device=DEV)
+
+    def call():
+        x, B, C = binding.causal_conv_fwd(s["xbc"], q["w"], q["bias"], sections=sec, state=conv, has_state=has,
+                                          cu_seqlens=cu, out=outs)
+        return binding.ssm_chunk_fwd(x.unflatten(-1, (HV, V)), s["dt"], B.unflatten(-1, (Hk, K)),
+                                     C.unflatten(-1, (Hk, K)), q["A_log"], D=q["D"], z=s["z"], dt_bias=q["dt_bias"],
+                                     h0=h0, cu_seqlens=cu, out=y)[1]
+
+    edges = [[0, 200, 200, 900, 901, 1500, 1600, 1700], [0, 100, 220, 340, 400, 500, 600, 700], [0, 0, 0, 0, 0, 0, 0, 1700],
+             [0] * 8, [0, 1700] + [1700] * 6, [0, 200, 200, 900, 901, 1500, 1600, 1700]]
+    assert binding.ssm_workspace_bytes(1, T, Hk, HV, K, V, N, BF, varlen=True) > 0
+    fresh = lambda: (conv.copy_(conv0), y.fill_(7.0), [o.fill_(7.0) for o in outs])
+
+    def set_cu(e):
+        cu.copy_(torch.tensor(e))
+        fresh()
+
+    want = []
+    for e in edges:
+        set_cu(e)
+        ht = call()
+        torch.cuda.synchronize()
+        want.append([t.clone() for t in (ht, y, conv, *outs)])
+    set_cu(edges[0])
+    g, ht = _capture(call)
+    for e, ref in zip(edges, want):
+        set_cu(e)
+        ht.fill_(7.0)
+        torch.cuda.synchronize()
+        g.replay()
+        torch.cuda.synchronize()
+        same([ht, y, conv, *outs], ref, f"replay with {e}")
+        _other_work()
+
+
+def test_steps_over_pools_past_4_gib():
+    print("steps over pools of 4.6 GB", flush=True)
+    N, HV, K, V = 3, 32, 128, 128
+    p = _layer_inputs(120, N, 2, 1, HV, K, V)
+    s, q = {n: d(p[n]) for n in ("xbc", "z", "dt")}, {n: d(p[n]) for n in ("w", "bias", "A_log", "D", "dt_bias")}
+    D, sec = p["xbc"].shape[-1], (HV * V, K, K)
+    st, cv = d(randn(121, N, HV, V, K)), d(randn(122, N, 3, D, dtype=BF))
+    small, conv = st.clone(), cv.clone()
+    ref = _layer(s, q, 1, HV, K, V, conv, pool=small)
+    for state, slots in ((st, 2200), (cv, 4600 * 1000 * 1000 // (6 * D))):
+        pool = torch.zeros((slots, *state.shape[1:]), dtype=state.dtype, device=DEV)
+        idx = torch.tensor([slots - 1, 5, slots - 2], dtype=torch.int32, device=DEV)
+        assert pool.numel() * pool.element_size() > 1 << 32
+        pool[idx.long()] = state
+        if state is st:
+            x, B, C = binding.causal_conv_step(s["xbc"], q["w"], q["bias"], cv.clone(), sections=sec)
+            y = binding.ssm_step(x.unflatten(-1, (HV, V)), s["dt"], B.unflatten(-1, (1, K)), C.unflatten(-1, (1, K)),
+                                 q["A_log"], pool, state_indices=idx, D=q["D"], z=s["z"], dt_bias=q["dt_bias"])
+            got = [y, pool[idx.long()]]
+            want = [ref, small]
+        else:
+            out = binding.causal_conv_step(s["xbc"], q["w"], q["bias"], pool, idx, sections=sec)
+            got = [*out, pool[idx.long()]]
+            want = [*binding.causal_conv_step(s["xbc"], q["w"], q["bias"], cv.clone(), sections=sec), conv]
+        torch.cuda.synchronize()
+        same(got, want, "large pool")
+        del pool
+        torch.cuda.empty_cache()

@@ -459,3 +459,32 @@ def test_long_prompts_among_thousands_of_short_ones(dtype):
             _check_part(p, lens, dtype, y, ht, [i], [0, 1, 2, 3])
         else:
             _check_part(p, lens, dtype, y, ht, [i], [2])
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_scan_and_step_of_rows_far_apart(dtype):
+    """Token strides just below the largest: 32-bit offsets within a chunk."""
+    print(f"scan of rows far apart {dtype}", flush=True)
+    T, Hk, HV, K, V = 66, 1, 2, 64, 64
+    p = ssm_inputs(2000, 1, T, Hk, HV, K, V, dtype)
+    names, at = ("x", "Bm", "Cm", "z", "dt"), 0
+    wide = torch.empty((1, T, (1 << 23) - 8), dtype=dtype, device=DEV)
+    far = {}
+    for n in names:
+        t = d(p[n]).flatten(2)
+        wide[..., at:at + t.shape[-1]] = t
+        far[n] = wide[..., at:at + t.shape[-1]].view(1, T, *p[n].shape[2:])
+        assert far[n].stride(1) == (1 << 23) - 8
+        at += t.shape[-1]
+    kw = dict(D=d(p["D"]), dt_bias=d(p["dt_bias"]))
+    got = binding.ssm_chunk_fwd(*(far[n] for n in ("x", "dt", "Bm", "Cm")), d(p["A_log"]), z=far["z"], h0=d(p["h0"]), **kw)
+    want = _run(p)
+    pools = [d(p["h0"]).clone() for _ in range(2)]
+    got += (binding.ssm_step(*(far[n][:, :4] for n in ("x", "dt", "Bm", "Cm")), d(p["A_log"]), pools[0],
+                             z=far["z"][:, :4], **kw), pools[0])
+    want += (binding.ssm_step(*(d(p[n])[:, :4] for n in ("x", "dt", "Bm", "Cm")), d(p["A_log"]), pools[1],
+                              z=d(p["z"])[:, :4], **kw), pools[1])
+    torch.cuda.synchronize()
+    same(got, want, "rows far apart")
+    del wide, far, got
+    torch.cuda.empty_cache()
