@@ -488,3 +488,29 @@ def test_scan_and_step_of_rows_far_apart(dtype):
     same(got, want, "rows far apart")
     del wide, far, got
     torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_rates_past_fp32_without_softplus(dtype):
+    """Steps of 0, 2^-100 and ordinary ones, as they are given."""
+    print(f"scan and step, rates past fp32, plain dt {dtype}", flush=True)
+    B, T, HV = 2, 150, 5
+    p = ssm_inputs(2100, B, T, 1, HV, 64, 64, dtype)
+    p["A_log"], p["dt_bias"] = torch.tensor([90.0, 200.0, 0.3, 63.0, 70.0]), torch.zeros(HV)
+    p["dt"] = (p["dt"].float().abs() * 0.1).to(dtype)
+    p["dt"][:, 2::5], p["dt"][:, 4::9], p["dt"][:, 30:60] = 0.0, 2.0 ** -100, 0.0
+    y, ht = _run(p, dt_softplus=False)
+    pool = ht.clone()
+    q = {n: (p[n][:, 100:104] if n in ("x", "dt", "Bm", "Cm", "z") else p[n]) for n in p}
+    ys = binding.ssm_step(*(d(q[n]) for n in ("x", "dt", "Bm", "Cm", "A_log")), pool, D=d(q["D"]), z=d(q["z"]),
+                          dt_bias=d(q["dt_bias"]), dt_softplus=False)
+    torch.cuda.synchronize()
+    ry, mag, skip, rh, hm = ssm_ref(p, [T] * B, softplus=False)
+    close("y", y.reshape(-1, HV, 64), ry, ssm_bound(dtype, ry, mag, skip))
+    # the bf16 terms of steps of 2^-100 that the matrix cores take as 0, as above
+    lost = 2.0 ** -125 * np.abs(f64(p["Bm"])[:, :, 0]).sum(1)[:, None, None] if dtype == BF else 0.0
+    close("ht", ht, rh, 512 * U * hm + 2.0 ** -20 * hm + lost)
+    q["h0"] = ht.cpu()
+    ry, mag, skip, rh, hm = ssm_ref(q, [4] * B, softplus=False)
+    close("step y", ys.reshape(-1, HV, 64), ry, 512 * U * mag + 2.0 ** -20 * (mag + skip) + store(dtype, ry))
+    close("step state", pool, rh, 2.0 ** -20 * hm + store(F32, rh) + 12 * 2.0 ** -150)   # four tokens, as above
