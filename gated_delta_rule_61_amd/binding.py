@@ -74,6 +74,17 @@ _SIGNATURES = {
                      + [_c_float] + [_c_void_p] * 3 + [_c_int, _c_void_p] + [_c_int] * 6 + [_c_void_p]),
     "gdn_conv_step": (_c_int, [_c_void_p, _c_ll, _c_ll, _c_void_p, _c_void_p, _c_int] + [_c_void_p] * 3
                       + [_c_int] * 3 + [_c_void_p] * 2 + [_c_int] * 6 + [_c_void_p]),
+    "gdn_conv_bwd_workspace_bytes": (_c_size_t, [_c_int] * 4),
+    "gdn_conv_bwd": (_c_int, [_c_void_p] * 3 + [_c_int] * 3 + [_c_void_p, _c_ll, _c_ll, _c_void_p, _c_void_p]
+                     + [_c_int] * 3 + [_c_float, _c_void_p] + [_c_int] * 6 + [_c_void_p] * 4 + [_c_size_t, _c_void_p]),
+    "gdn_group_norm_fwd": (_c_int, [_c_void_p, _c_ll, _c_ll, _c_void_p, _c_void_p, _c_int, _c_int, _c_void_p, _c_ll,
+                                    _c_ll, _c_int, _c_int, _c_float] + [_c_int] * 5 + [_c_void_p] * 2),
+    "gdn_group_norm_bwd_workspace_bytes": (_c_size_t, [_c_int] * 5),
+    "gdn_group_norm_bwd": (_c_int, [_c_void_p, _c_ll, _c_ll] * 2 + [_c_void_p, _c_void_p, _c_int, _c_int, _c_void_p,
+                                    _c_ll, _c_ll, _c_int, _c_int, _c_float] + [_c_int] * 5 + [_c_void_p] * 5
+                           + [_c_size_t, _c_void_p]),
+    "kda_decode": (_c_int, [_c_void_p] * 8 + [_c_int, _c_void_p, _c_void_p] + [_c_int] * 7 + [_c_float] * 3
+                   + [_c_int, _c_float, _c_int, _c_void_p]),
     "ssm_chunk_fwd_workspace_bytes": (_c_size_t, [_c_int] * 9),
     "ssm_chunk_fwd": (_c_int, [_c_void_p, _c_ll, _c_ll] * 5 + [_c_void_p] * 3 + [_c_int] + [_c_void_p] * 3
                       + [_c_int] * 9 + [_c_void_p, _c_void_p, _c_size_t, _c_void_p]),
@@ -147,7 +158,7 @@ def _need(t: Optional[torch.Tensor], name: str, dtype: Optional[torch.dtype], sh
 
 
 STAGES = ("varlen_tables", "intra", "scan", "decode", "handoff", "bwd_dh", "fwd_h", "conv", "ssm_scan", "ssm_step",
-          "state_q8")
+          "state_q8", "conv_bwd", "norm")
 
 
 def profile_enable(on: bool = True) -> None:
@@ -594,8 +605,8 @@ def _cuda(t: torch.Tensor, name: str) -> torch.device:
     return t.device
 
 
-def _conv_args(x, weight, bias, activation, sections, state, out):
-    """Checked arguments shared by the two convolutions: the call's leading and
+def _conv_args(x, weight, bias, activation, sections, state, out, out_name="out"):
+    """Checked arguments shared by the convolutions: the call's leading and
     trailing arguments, the outputs, and what the callers go on with."""
     if x.dim() != 3 or weight.dim() != 2:
         raise ValueError("x must be [B, T, D] and weight [D, W]")
@@ -624,8 +635,8 @@ def _conv_args(x, weight, bias, activation, sections, state, out):
     else:
         outs = (out,) if isinstance(out, torch.Tensor) else tuple(out)
         if len(outs) != n:
-            raise ValueError(f"out must hold {n} tensors, got {len(outs)}")
-        ptrs = [_want(o, f"out[{i}]", io, (B, T, wd), dev) for i, (o, wd) in enumerate(zip(outs, widths))]
+            raise ValueError(f"{out_name} must hold {n} tensors, got {len(outs)}")
+        ptrs = [_want(o, f"{out_name}[{i}]", io, (B, T, wd), dev) for i, (o, wd) in enumerate(zip(outs, widths))]
     if n < 3:
         ptrs += [None] * (3 - n)
         widths += (0,) * (3 - n)
@@ -675,6 +686,158 @@ def causal_conv_step(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch
     state_indices = _index(state_indices, "state_indices", B, dev)
     _call(dev, lib().gdn_conv_step, *head, sp, _ptr(state_indices), state.shape[0], *tail)
     return outs[0] if sections is None else outs
+
+
+def _scratch(workspace: Optional[torch.Tensor], nbytes: int, dev: torch.device):
+    """(workspace, its pointer): the caller's where it is large enough, else a new one (none for 0 bytes)."""
+    if not nbytes:
+        return None, None
+    if workspace is None or workspace.numel() * workspace.element_size() < nbytes:
+        workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+    else:
+        _need(workspace, "workspace", None, None, dev)
+    return workspace, workspace.data_ptr()
+
+
+def causal_conv_bwd(dout, x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tensor] = None, *,
+                    activation: Optional[str] = "silu", sections=None, norm_dim: int = 0, norm_sections: int = 0,
+                    norm_eps: float = 1e-6, cu_seqlens: Optional[torch.Tensor] = None,
+                    workspace: Optional[torch.Tensor] = None):
+    """Gradients of ``causal_conv_fwd`` (without a state: sequences start from
+    zeros).  ``dout``: the gradient of its result, one tensor or with
+    ``sections`` a tuple, packed; the other arguments as they were given there.
+    Returns (dx [B,T,D], dweight [D,W], dbias [D] or None without a bias) in the
+    io dtype; dx's rows behind the last boundary of ``cu_seqlens`` are left as
+    they are.  A ``workspace`` (else allocated) serves one call at a time."""
+    douts = (dout,) if isinstance(dout, torch.Tensor) else tuple(dout)
+    head, (B, T, D, W, code), _, _, _, dev = _conv_args(x, weight, bias, activation, sections, None, douts, "dout")
+    N, cu = _seqs(cu_seqlens, B, dev)
+    dx, dw = x.new_empty((B, T, D)), torch.empty_like(weight)
+    db = None if bias is None else torch.empty_like(bias)
+    L = lib()
+    nbytes = int(L.gdn_conv_bwd_workspace_bytes(B, T, D, W))
+    workspace, wp = _scratch(workspace, nbytes, dev)
+    xp, xb, xt, wptr, bptr, silu = head[:6]
+    _call(dev, L.gdn_conv_bwd, *head[6:], xp, xb, xt, wptr, bptr, silu, norm_dim, norm_sections, norm_eps, cu, N, B, T,
+          D, W, code, dx.data_ptr(), dw.data_ptr(), _ptr(db), wp, nbytes)
+    return dx, dw, db
+
+
+_ACTS = {None: 0, "silu": 1, "sigmoid": 2}
+
+
+def _norm_args(x, num_groups, weight, bias, z, activation):
+    """Checked arguments shared by the norm and its gradients: the call's rows
+    of x, its weights and gate, its sizes, device and io code."""
+    if x.dim() != 3:
+        raise ValueError("x must be [B, T, C]")
+    if activation not in _ACTS:
+        raise ValueError(f"activation must be None, 'silu' or 'sigmoid', got {activation!r}")
+    shape = x.shape
+    B, T, C = shape
+    if num_groups <= 0 or C % num_groups or C == 0:
+        raise ValueError(f"num_groups ({num_groups}) must divide the {C} channels")
+    d = C // num_groups
+    dev, io = _cuda(x, "x"), x.dtype
+    code = _IO_CODES.get(io)
+    if code is None:
+        _io_code(io)
+    wdt, shared = torch.float32, 1
+    for t, name in ((weight, "weight"), (bias, "bias")):
+        if t is not None and (t.dtype not in _IO_CODES or t.dim() != 1 or t.shape[0] not in (d, C)):
+            raise ValueError(f"{name} must be [{d}] (one for all groups) or [{C}], fp32 or bf16")
+    first = weight if weight is not None else bias
+    if first is not None:
+        wdt, shared = first.dtype, int(first.shape[0] == d)
+    wn = (d,) if shared else (C,)
+    wp, bp = _want(weight, "weight", wdt, wn, dev), _want(bias, "bias", wdt, wn, dev)
+    tail = (wp, bp, _IO_CODES[wdt], shared, *((None, 0, 0) if z is None else _rows(z, "z", io, shape, dev)),
+            _ACTS[activation])
+    return _rows(x, "x", io, shape, dev), tail, (B, T, num_groups, d, code), dev
+
+
+def group_norm_fwd(x: torch.Tensor, num_groups: int, weight: Optional[torch.Tensor] = None,
+                   bias: Optional[torch.Tensor] = None, *, z: Optional[torch.Tensor] = None,
+                   activation: Optional[str] = "silu", rms: bool = False, eps: float = 1e-5,
+                   out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Norm of every group of C / num_groups consecutive channels of a token (the
+    heads of a mixer): n = (x - mean) / sqrt(var + eps), or x / sqrt(mean(x^2) +
+    eps) with ``rms``; a = n weight + bias; y = a act(z) with an output gate
+    ``z``, else act(a).  ``x``, ``z`` [B,T,C] (bf16 or fp32, possibly slices of
+    wider tensors); ``weight``, ``bias`` [C], or [C / num_groups] for one that
+    all groups share, fp32 or bf16; ``activation``: None, "silu" or "sigmoid".
+    Returns y [B,T,C]; ``out`` must not overlap an input."""
+    xr, tail, dims, dev = _norm_args(x, num_groups, weight, bias, z, activation)
+    if out is None:
+        out = x.new_empty(x.shape)
+    else:
+        _want(out, "out", x.dtype, x.shape, dev)
+    _call(dev, lib().gdn_group_norm_fwd, *xr, *tail, 1 if rms else 0, eps, *dims, out.data_ptr())
+    return out
+
+
+def group_norm_bwd(dout: torch.Tensor, x: torch.Tensor, num_groups: int, weight: Optional[torch.Tensor] = None,
+                   bias: Optional[torch.Tensor] = None, *, z: Optional[torch.Tensor] = None,
+                   activation: Optional[str] = "silu", rms: bool = False, eps: float = 1e-5,
+                   workspace: Optional[torch.Tensor] = None):
+    """Gradients of ``group_norm_fwd`` from the gradient ``dout`` [B,T,C] of its
+    result (possibly a slice of a wider tensor); the other arguments as they were
+    given there.  Returns (dx [B,T,C], dz [B,T,C], dweight, dbias), the last
+    three None where z, weight or bias is; those of weight and bias in their
+    dtype.  A ``workspace`` (else allocated) serves one call at a time."""
+    xr, tail, dims, dev = _norm_args(x, num_groups, weight, bias, z, activation)
+    B, T, G, d, _ = dims
+    dx = x.new_empty(x.shape)
+    dz = None if z is None else x.new_empty(x.shape)
+    dw = None if weight is None else torch.empty_like(weight)
+    db = None if bias is None else torch.empty_like(bias)
+    L = lib()
+    nbytes = int(L.gdn_group_norm_bwd_workspace_bytes(B, T, G, d, tail[3])) if dw is not None or db is not None else 0
+    workspace, wp = _scratch(workspace, nbytes, dev)
+    _call(dev, L.gdn_group_norm_bwd, *_rows(dout, "dout", x.dtype, x.shape, dev), *xr, *tail, 1 if rms else 0, eps,
+          *dims, dx.data_ptr(), _ptr(dz), _ptr(dw), _ptr(db), wp, nbytes)
+    return dx, dz, dw, db
+
+
+def kda_decode(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, a: torch.Tensor, b: torch.Tensor,
+               A_log: torch.Tensor, dt_bias: torch.Tensor, state: torch.Tensor,
+               state_indices: Optional[torch.Tensor] = None, scale: Optional[float] = None,
+               softplus_beta: float = 1.0, softplus_threshold: float = 20.0,
+               use_qk_l2norm: bool = True, eps: float = 1e-6,
+               out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """``gdn_decode`` with one gate per key channel (the recurrence of
+    ``kda_chunk_fwd``): T = 1..4 tokens; ``q``, ``k`` [B,T,H,K], ``v`` [B,T,HV,V],
+    gate inputs ``a`` [B,T,HV,K] and ``b`` [B,T,HV] (bf16 or fp32), ``A_log``
+    [HV], ``dt_bias`` [HV,K] fp32; ``state`` [pool,HV,V,K] (bf16 or fp32) is
+    updated in place at the slots ``state_indices`` [B] (None = row b).  A slot
+    outside the pool gives o = 0 and leaves the pool alone.  Returns o
+    [B,T,HV,V]."""
+    if q.dim() != 4 or v.dim() != 4:
+        raise ValueError("q, k must be [B, T, H, K] and v [B, T, HV, V]")
+    shape = q.shape
+    B, T, H, K = shape
+    HV, V = v.shape[2:]
+    dev, io = _cuda(q, "q"), q.dtype
+    code = _IO_CODES.get(io)
+    if code is None:
+        _io_code(io)
+    rows, f32 = (B, T, HV, V), torch.float32
+    head = (_want(q, "q", io, shape, dev), _want(k, "k", io, shape, dev), _want(v, "v", io, rows, dev),
+            _want(a, "a", io, (B, T, HV, K), dev), _want(b, "b", io, (B, T, HV), dev),
+            _want(A_log, "A_log", f32, (HV,), dev), _want(dt_bias, "dt_bias", f32, (HV, K), dev))
+    scode = _IO_CODES.get(state.dtype)
+    if state.dim() != 4 or scode is None:
+        raise ValueError("state must be [pool, HV, V, K] fp32 or bf16")
+    pool = state.shape[0]
+    sp = _want(state, "state", state.dtype, (pool, HV, V, K), dev)
+    state_indices = _index(state_indices, "state_indices", B, dev)
+    if out is None:
+        out = q.new_empty(rows)
+    else:
+        _want(out, "out", io, rows, dev)
+    _call(dev, lib().kda_decode, *head, sp, scode, _ptr(state_indices), out.data_ptr(), B, T, H, HV, K, V, pool,
+          K ** -0.5 if scale is None else scale, softplus_beta, softplus_threshold, 1 if use_qk_l2norm else 0, eps, code)
+    return out
 
 
 def _ssm_args(x, dt, Bm, Cm, A_log, D, z, dt_bias, softplus, out):

@@ -1,5 +1,6 @@
-// C ABI of the operators around the scans (causal convolution, selective
-// state-space scan and step, 8-bit state cache): argument validation (host
+// C ABI of the operators around the scans (causal convolution and its
+// gradients, norm of the heads and its gradients, selective state-space scan and
+// step, the delta rule's step with one gate per key channel, 8-bit state cache): argument validation (host
 // only, before any HIP call) and the launch of each.
 
 #include <stdint.h>
@@ -127,6 +128,40 @@ int check_ssm_rows(const SsmArgs& a) {
   return GDN_OK;
 }
 
+int check_norm(GroupNormArgs& a, int weight_dtype, int dtype) {
+  if (int st = known_dtype(dtype)) return st;
+  a.bf16 = dtype == GDN_DTYPE_BF16;
+  if (a.B < 0 || a.T < 0 || a.G <= 0 || a.d <= 0)
+    return fail(GDN_ERR_INVALID_ARGUMENT, "sizes must be positive (B, T >= 0): B=%d T=%d G=%d d=%d", a.B, a.T, a.G,
+                a.d);
+  if ((long long)a.B * a.T >= (1LL << 25))
+    return fail(GDN_ERR_UNSUPPORTED, "B*T too large (got %lld tokens)", (long long)a.B * a.T);
+  if (a.d % 8 || a.d > 8192)
+    return fail(GDN_ERR_UNSUPPORTED, "groups take a multiple of 8 channels up to 8192 (got %d)", a.d);
+  if ((long long)a.G * a.d >= (1 << 23)) return fail(GDN_ERR_UNSUPPORTED, "G * d must stay below 2^23");
+  if (a.act < 0 || a.act > 2) return fail(GDN_ERR_INVALID_ARGUMENT, "unknown activation code %d", a.act);
+  if (a.rms != 0 && a.rms != 1) return fail(GDN_ERR_INVALID_ARGUMENT, "rms must be 0 or 1 (got %d)", a.rms);
+  if (a.shared != 0 && a.shared != 1)
+    return fail(GDN_ERR_INVALID_ARGUMENT, "weight_shared must be 0 or 1 (got %d)", a.shared);
+  if (!(a.eps >= 0.f)) return fail(GDN_ERR_INVALID_ARGUMENT, "eps must be >= 0");
+  if (weight_dtype != GDN_DTYPE_F32 && weight_dtype != GDN_DTYPE_BF16)
+    return fail(GDN_ERR_INVALID_ARGUMENT, "unknown weight dtype code %d", weight_dtype);
+  a.w_bf16 = weight_dtype == GDN_DTYPE_BF16;
+  const void* ptrs[] = {a.weight, a.bias, a.y, a.dx, a.dz, a.dweight, a.dbias};
+  for (const void* p : ptrs)
+    if (!aligned16(p)) return fail(GDN_ERR_INVALID_ARGUMENT, "tensor pointers must be 16-byte aligned");
+  return GDN_OK;
+}
+
+int check_workspace(const void* workspace, size_t have, size_t need) {
+  if (need == 0) return GDN_OK;
+  if (!workspace || have < need)
+    return fail(GDN_ERR_WORKSPACE, "workspace of %zu bytes needed (got %zu)", need, workspace ? have : (size_t)0);
+  if (((uintptr_t)workspace & 255u) != 0)
+    return fail(GDN_ERR_INVALID_ARGUMENT, "workspace must be 256-byte aligned");
+  return GDN_OK;
+}
+
 // A launch has fewer than 2^32 threads.
 bool too_many(long long groups, int threads) { return groups >= (1LL << 32) / threads; }
 
@@ -199,6 +234,140 @@ int gdn_conv_step(const void* x, long long x_batch, long long x_token, const voi
   if (too_many((long long)B * (D / 512 + 1), 64))
     return fail(GDN_ERR_UNSUPPORTED, "too many rows x channels for one launch");
   return timed(GDN_STAGE_CONV, stream, [&](hipStream_t s) { return launch_conv_step(a, s); });
+}
+
+size_t gdn_conv_bwd_workspace_bytes(int B, int T, int D, int W) {
+  if (B < 0 || T < 0 || D <= 0 || D % 8 || W < 2 || W > 4) return 0;
+  ConvBwdArgs a{};
+  a.B = B; a.T = T; a.D = D; a.W = W;
+  a.dweight = &a;   // any: the size does not depend on which sums are wanted
+  return conv_bwd_bytes(a);
+}
+
+int gdn_conv_bwd(const void* dout0, const void* dout1, const void* dout2, int width0, int width1, int width2,
+                 const void* x, long long x_batch, long long x_token, const void* weight, const void* bias, int silu,
+                 int norm_dim, int norm_sections, float norm_eps, const int64_t* cu_seqlens, int num_seqs, int B,
+                 int T, int D, int W, int dtype, void* dx, void* dweight, void* dbias, void* workspace,
+                 size_t workspace_bytes, void* stream) {
+  // the checks of the forward convolution, dout in the place of its outputs
+  ConvArgs f{};
+  f.x = {x, x_batch, x_token};
+  f.weight = weight; f.bias = bias; f.silu = silu;
+  f.out[0] = const_cast<void*>(dout0); f.out[1] = const_cast<void*>(dout1); f.out[2] = const_cast<void*>(dout2);
+  f.norm_dim = norm_dim; f.norm_sections = norm_sections; f.eps = norm_eps;
+  f.B = B; f.T = T; f.D = D; f.W = W;
+  if (int st = check_seqs(cu_seqlens, num_seqs, B, T, f.N)) return st;
+  if (int st = check_conv(f, width0, width1, width2, dtype)) return st;
+  const bool tokens = (long long)B * T > 0;
+  if (!tokens && !dweight && !dbias) return ok();
+  if (int st = check_conv_ptrs(f, tokens)) return st;
+  if (tokens && !dx) return fail(GDN_ERR_INVALID_ARGUMENT, "dx is required");
+  if (!aligned16(dx) || !aligned16(dweight) || !aligned16(dbias))
+    return fail(GDN_ERR_INVALID_ARGUMENT, "tensor pointers must be 16-byte aligned");
+  if (int st = check_rows("x", f.x, B, T, 8)) return st;
+  if (too_many(((long long)B * T / 8 + 1) * (D / 512 + 1), 64))
+    return fail(GDN_ERR_UNSUPPORTED, "too many tokens x channels for one launch");
+  ConvBwdArgs a{};
+  a.x = f.x; a.weight = weight; a.bias = bias;
+  a.dout[0] = dout0; a.dout[1] = dout1; a.dout[2] = dout2;
+  a.end[0] = f.end[0]; a.end[1] = f.end[1]; a.end[2] = f.end[2];
+  a.norm_dim = norm_dim; a.norm_sections = norm_sections; a.eps = norm_eps; a.silu = silu;
+  a.dx = dx; a.dweight = dweight; a.dbias = dbias;
+  a.cu = cu_seqlens; a.N = f.N; a.B = B; a.T = T; a.D = D; a.W = W; a.bf16 = f.bf16;
+  if (int st = check_workspace(workspace, workspace_bytes, conv_bwd_bytes(a))) return st;
+  a.partial = (float*)workspace;
+  return timed(GDN_STAGE_CONV_BWD, stream, [&](hipStream_t s) { return launch_conv_bwd(a, s); });
+}
+
+int gdn_group_norm_fwd(const void* x, long long x_batch, long long x_token, const void* weight, const void* bias,
+                       int weight_dtype, int weight_shared, const void* z, long long z_batch, long long z_token,
+                       int activation, int rms, float eps, int B, int T, int G, int d, int dtype, void* y,
+                       void* stream) {
+  GroupNormArgs a{};
+  a.x = {x, x_batch, x_token}; a.z = {z, z_batch, z_token};
+  a.weight = weight; a.bias = bias; a.shared = weight_shared; a.y = y;
+  a.act = activation; a.rms = rms; a.eps = eps; a.B = B; a.T = T; a.G = G; a.d = d;
+  if (int st = check_norm(a, weight_dtype, dtype)) return st;
+  if ((long long)B * T == 0) return ok();
+  if (!x || !y) return fail(GDN_ERR_INVALID_ARGUMENT, "x and y are required");
+  const int unit = a.bf16 ? 8 : 4;
+  if (int st = check_rows("x", a.x, B, T, unit)) return st;
+  if (z)
+    if (int st = check_rows("z", a.z, B, T, unit)) return st;
+  return timed(GDN_STAGE_NORM, stream, [&](hipStream_t s) { return launch_group_norm_fwd(a, s); });
+}
+
+size_t gdn_group_norm_bwd_workspace_bytes(int B, int T, int G, int d, int weight_shared) {
+  if (B < 0 || T < 0 || G <= 0 || d <= 0 || d % 8 || d > 8192 || (long long)G * d >= (1 << 23) ||
+      (long long)B * T >= (1LL << 25))
+    return 0;
+  GroupNormArgs a{};
+  a.B = B; a.T = T; a.G = G; a.d = d; a.shared = weight_shared;
+  a.dweight = &a;   // any: the size does not depend on which sums are wanted
+  return group_norm_bwd_bytes(a);
+}
+
+int gdn_group_norm_bwd(const void* dout, long long dout_batch, long long dout_token, const void* x, long long x_batch,
+                       long long x_token, const void* weight, const void* bias, int weight_dtype, int weight_shared,
+                       const void* z, long long z_batch, long long z_token, int activation, int rms, float eps, int B,
+                       int T, int G, int d, int dtype, void* dx, void* dz, void* dweight, void* dbias, void* workspace,
+                       size_t workspace_bytes, void* stream) {
+  GroupNormArgs a{};
+  a.dout = {dout, dout_batch, dout_token}; a.x = {x, x_batch, x_token}; a.z = {z, z_batch, z_token};
+  a.weight = weight; a.bias = bias; a.shared = weight_shared;
+  a.dx = dx; a.dz = dz; a.dweight = dweight; a.dbias = dbias;
+  a.act = activation; a.rms = rms; a.eps = eps; a.B = B; a.T = T; a.G = G; a.d = d;
+  if (int st = check_norm(a, weight_dtype, dtype)) return st;
+  const bool tokens = (long long)B * T > 0;
+  if (!tokens && !dweight && !dbias) return ok();
+  if (tokens) {
+    if (!dout || !x || !dx || (z && !dz))
+      return fail(GDN_ERR_INVALID_ARGUMENT, "dout, x and dx are required, and dz with z");
+    const int unit = a.bf16 ? 8 : 4;
+    if (int st = check_rows("dout", a.dout, B, T, unit)) return st;
+    if (int st = check_rows("x", a.x, B, T, unit)) return st;
+    if (z)
+      if (int st = check_rows("z", a.z, B, T, unit)) return st;
+  }
+  if (int st = check_workspace(workspace, workspace_bytes, group_norm_bwd_bytes(a))) return st;
+  a.partial = (float*)workspace;
+  return timed(GDN_STAGE_NORM, stream, [&](hipStream_t s) { return launch_group_norm_bwd(a, s); });
+}
+
+int kda_decode(const void* q, const void* k, const void* v, const void* a, const void* b, const float* A_log,
+               const float* dt_bias, void* state, int state_dtype, const int32_t* state_indices, void* o, int B, int T,
+               int H, int HV, int K, int V, int pool, float scale, float softplus_beta, float softplus_threshold,
+               int use_qk_l2norm, float eps, int dtype, void* stream) {
+  if (int st = known_dtype(dtype)) return st;
+  if (state_dtype != GDN_DTYPE_F32 && state_dtype != GDN_DTYPE_BF16)
+    return fail(GDN_ERR_INVALID_ARGUMENT, "unknown state dtype code %d", state_dtype);
+  if (B < 0 || H <= 0 || HV <= 0 || K <= 0 || V <= 0 || pool < 0)
+    return fail(GDN_ERR_INVALID_ARGUMENT, "sizes must be positive: B=%d H=%d HV=%d K=%d V=%d pool=%d", B, H, HV, K, V,
+                pool);
+  if (T < 1 || T > 4) return fail(GDN_ERR_INVALID_ARGUMENT, "a step takes T = 1..4 tokens (got T=%d)", T);
+  if (HV % H != 0) return fail(GDN_ERR_INVALID_ARGUMENT, "HV (%d) must be a multiple of H (%d)", HV, H);
+  if ((K != 64 && K != 128) || (V != 64 && V != 128))
+    return fail(GDN_ERR_UNSUPPORTED, "supported head dims are K, V in {64, 128} (got K=%d V=%d)", K, V);
+  if (!state_indices && pool < B)
+    return fail(GDN_ERR_INVALID_ARGUMENT, "identity slots need pool >= B (pool=%d B=%d)", pool, B);
+  if (!(softplus_beta > 0.f)) return fail(GDN_ERR_INVALID_ARGUMENT, "softplus_beta must be > 0");
+  if (!(eps >= 0.f)) return fail(GDN_ERR_INVALID_ARGUMENT, "eps must be >= 0");
+  if (B == 0) return ok();
+  if (!q || !k || !v || !a || !b || !A_log || !dt_bias || !state || !o)
+    return fail(GDN_ERR_INVALID_ARGUMENT, "q, k, v, a, b, A_log, dt_bias, state and o are required");
+  const void* ptrs[] = {q, k, v, state, o};
+  for (const void* p : ptrs)
+    if (!aligned16(p)) return fail(GDN_ERR_INVALID_ARGUMENT, "q, k, v, state and o must be 16-byte aligned");
+  if ((long long)pool * HV * V * K >= (1LL << 40)) return fail(GDN_ERR_UNSUPPORTED, "state pool too large");
+  if (too_many((long long)B * HV, 256))
+    return fail(GDN_ERR_UNSUPPORTED, "too many batch rows x heads for one launch (B=%d HV=%d)", B, HV);
+  KdaStepArgs s{};
+  s.q = q; s.k = k; s.v = v; s.a = a; s.b = b; s.A_log = A_log; s.dt_bias = dt_bias;
+  s.state = state; s.state_bf16 = state_dtype == GDN_DTYPE_BF16; s.idx = state_indices; s.pool = pool; s.o = o;
+  s.B = B; s.T = T; s.H = H; s.HV = HV; s.K = K; s.V = V;
+  s.scale = scale; s.sp_beta = softplus_beta; s.sp_thr = softplus_threshold; s.eps = eps;
+  s.use_norm = use_qk_l2norm != 0; s.bf16 = dtype == GDN_DTYPE_BF16;
+  return timed(GDN_STAGE_DECODE, stream, [&](hipStream_t st) { return launch_kda_decode(s, st); });
 }
 
 size_t ssm_chunk_fwd_workspace_bytes(int B, int T, int Hk, int HV, int K, int V, int num_seqs, int varlen,

@@ -72,6 +72,60 @@ SsmPlan ssm_plan(int nb, int T, int Hk, int HV, int K, int V, int N, bool varlen
 hipError_t launch_ssm_fwd(const SsmArgs& a, hipStream_t s);
 hipError_t launch_ssm_step(const SsmArgs& a, hipStream_t s);
 
+// The delta-rule step with one gate per key channel.
+struct KdaStepArgs {
+  const void *q, *k;            // [B, T, H, K]
+  const void *v, *a, *b;        // [B, T, HV, V], [B, T, HV, K], [B, T, HV]
+  const float *A_log, *dt_bias; // [HV], [HV, K]
+  void* state;                  // [pool, HV, V, K]
+  int state_bf16;
+  const int32_t* idx;           // [B] or nullptr (the identity)
+  int pool;
+  void* o;                      // [B, T, HV, V]
+  int B, T, H, HV, K, V;
+  float scale, sp_beta, sp_thr, eps;
+  int use_norm;
+  int bf16;
+};
+hipError_t launch_kda_decode(const KdaStepArgs& a, hipStream_t s);
+
+// Norm of every group of d consecutive channels of a token, with an activation or a gate.
+struct GroupNormArgs {
+  Rows x, z, dout;              // [B, T, C]; z.p may be nullptr (no gate); dout: the gradient only
+  const void *weight, *bias;    // [d] (shared by the groups) or [C]; nullptr: 1 and 0
+  int w_bf16, shared;
+  void *y, *dx, *dz;            // packed [B, T, C]
+  void *dweight, *dbias;        // as weight and bias; nullptr: not wanted
+  int act;                      // 0 none, 1 silu, 2 sigmoid; of z where there is one, else of the result
+  int rms;
+  float eps;
+  float* partial;               // workspace: sums of the waves' rows
+  int B, T, G, d;               // G groups of d channels, C = G d
+  int bf16;
+};
+hipError_t launch_group_norm_fwd(const GroupNormArgs& a, hipStream_t s);
+hipError_t launch_group_norm_bwd(const GroupNormArgs& a, hipStream_t s);
+size_t group_norm_bwd_bytes(const GroupNormArgs& a);
+
+// Gradients of the causal convolution.
+struct ConvBwdArgs {
+  Rows x;                       // [B, T, D]
+  const void *weight, *bias;    // [D, W], [D] or nullptr
+  const void* dout[3];          // packed [B, T, width] each; unused sections nullptr
+  int end[3];                   // channel ends of the sections
+  int norm_dim, norm_sections;  // 0 = no norm
+  float eps;
+  int silu;
+  void* dx;                     // packed [B, T, D]
+  void *dweight, *dbias;        // [D, W], [D] (nullptr: not wanted)
+  float* partial;               // workspace: sums of the runs
+  const int64_t* cu;            // [N + 1] or nullptr (dense)
+  int N, B, T, D, W;
+  int bf16;
+};
+hipError_t launch_conv_bwd(const ConvBwdArgs& a, hipStream_t s);
+size_t conv_bwd_bytes(const ConvBwdArgs& a);
+
 struct StateQ8Args {
   void* wide;                   // [wide_n, HV, V, K] fp32 or bf16: the source of a store, the target of a load
   int wide_bf16;

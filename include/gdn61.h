@@ -475,6 +475,116 @@ int gdn_conv_step(const void* x, long long x_batch, long long x_token, const voi
                   int B, int T, int D, int W, int dtype, void* stream);
 
 /*
+ * Gradients of gdn_conv_fwd's convolution, with its activation and norms, for
+ * sequences that start from zeros (training): with dy the gradient of the
+ * outputs, u the activated convolution and c what the activation took,
+ *
+ *   du = dy, in a normalised head r (dy - n (n . dy)), n = r u,
+ *        r = 1 / sqrt(sum of u^2 + norm_eps)
+ *   dc = du silu'(c),   dx_t = sum_j w_j dc_{t+W-1-j}  (rows of the sequence)
+ *   dweight_j = sum_t dc_t x_{t-W+1+j},   dbias = sum_t dc_t
+ *
+ *   dout0..2     [B, T, width]  io dtype, packed: the outputs' gradients
+ *   x, weight, bias, silu, norm_*, cu_seqlens, ...   as in gdn_conv_fwd; c is
+ *                               computed again from them
+ *   dx           [B, T, D]      io dtype out, packed; rows behind the last
+ *                               boundary are left as they are
+ *   dweight      [D, W]         io dtype out, or NULL
+ *   dbias        [D]            io dtype out, or NULL (also without a bias)
+ *   workspace    device buffer of gdn_conv_bwd_workspace_bytes() bytes, 256-byte
+ *                aligned (NULL allowed where neither sum is wanted)
+ *
+ * Sums are fp32, in an order that does not change from run to run.  Limits as in
+ * gdn_conv_fwd.  Calls that share a workspace (captured graphs too) must not run
+ * at the same time.  Allocates nothing; asynchronous on `stream`.
+ */
+size_t gdn_conv_bwd_workspace_bytes(int B, int T, int D, int W);
+int gdn_conv_bwd(const void* dout0, const void* dout1, const void* dout2, int width0, int width1, int width2,
+                 const void* x, long long x_batch, long long x_token, const void* weight, const void* bias, int silu,
+                 int norm_dim, int norm_sections, float norm_eps, const int64_t* cu_seqlens, int num_seqs,
+                 int B, int T, int D, int W, int dtype, void* dx, void* dweight, void* dbias,
+                 void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Norm of the groups of a token's channels, channels last (the heads of a
+ * mixer, behind its scan), with an activation or an output gate: per token and
+ * group of d channels
+ *
+ *   n = (x - mean) / sqrt(var + eps)      (rms: x / sqrt(mean of x^2 + eps))
+ *   a = n weight + bias
+ *   y = a act(z) with a gate z, else act(a)
+ *
+ *   x            [B, T, G * d]  io dtype; row t of batch b starts x_batch * b +
+ *                               x_token * t elements behind x; channels contiguous
+ *   weight, bias [d] (weight_shared = 1: the same for every group) or [G * d]
+ *                               (0), fp32 or bf16 (weight_dtype), or NULL (1, 0)
+ *   z            [B, T, G * d]  io dtype with strides of its own, or NULL
+ *   activation   GDN_ACT_NONE, GDN_ACT_SILU or GDN_ACT_SIGMOID
+ *   y            [B, T, G * d]  io dtype out, packed
+ *
+ * Statistics are those of one token's group; the variance is the mean square of
+ * x - mean.  fp32 throughout, one rounding.
+ *
+ * gdn_group_norm_bwd takes the gradient of y (dout, with strides of its own) and
+ * gives those of x and z (packed, io dtype; dz with z only), and of weight and
+ * bias in their dtype (NULL: not wanted; also without a weight or a bias), as
+ * sums over the tokens, and over the groups with weight_shared, in fp32 and in an
+ * order that does not change from run to run.  It computes the statistics again
+ * from x.  workspace: gdn_group_norm_bwd_workspace_bytes() bytes, 256-byte
+ * aligned (NULL allowed where neither sum is wanted); calls that share one
+ * (captured graphs too) must not run at the same time.
+ *
+ * Supported: bf16 or fp32 io, d a multiple of 8 up to 8192, G * d below 2^23;
+ * x, z, dout and their strides in multiples of 16 bytes, 16-byte aligned tensors.
+ * Allocates nothing; asynchronous on `stream`.
+ */
+enum { GDN_ACT_NONE = 0, GDN_ACT_SILU = 1, GDN_ACT_SIGMOID = 2 };
+int gdn_group_norm_fwd(const void* x, long long x_batch, long long x_token, const void* weight, const void* bias,
+                       int weight_dtype, int weight_shared, const void* z, long long z_batch, long long z_token,
+                       int activation, int rms, float eps, int B, int T, int G, int d, int dtype,
+                       void* y, void* stream);
+size_t gdn_group_norm_bwd_workspace_bytes(int B, int T, int G, int d, int weight_shared);
+int gdn_group_norm_bwd(const void* dout, long long dout_batch, long long dout_token,
+                       const void* x, long long x_batch, long long x_token, const void* weight, const void* bias,
+                       int weight_dtype, int weight_shared, const void* z, long long z_batch, long long z_token,
+                       int activation, int rms, float eps, int B, int T, int G, int d, int dtype,
+                       void* dx, void* dz, void* dweight, void* dbias,
+                       void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * The delta rule's step with one gate per key channel, T = 1..4 tokens a call,
+ * over a pool of states: the recurrence of kda_chunk_fwd for single tokens, its
+ * gates made from a layer's inputs as in gdn_decode.  Per token
+ *
+ *   gk_c = -exp(A_log) softplus(a_c + dt_bias_c)   (softplus as in gdn_decode)
+ *   S <- S diag(e^{gk}),  S <- S + beta (v - S k) k^T,  o = S q,
+ *   beta = sigmoid(b); k over its L2 norm and q over its norm, times scale
+ *   (use_qk_l2norm = 0: q times scale only)
+ *
+ *   q, k         [B, T, H, K]   io dtype (head of v-head j: j / (HV / H))
+ *   v            [B, T, HV, V]  io dtype
+ *   a            [B, T, HV, K]  io dtype gate inputs
+ *   b            [B, T, HV]     io dtype
+ *   A_log        [HV]           fp32; exp(A_log) may pass fp32's largest number
+ *   dt_bias      [HV, K]        fp32
+ *   state        [pool, HV, V, K] fp32 or bf16 (state_dtype), read and written
+ *                IN PLACE at slot state_indices[b] (or b when NULL, then pool >=
+ *                B).  Carried in fp32 across the T tokens; a bf16 pool gets it
+ *                rounded to nearest, ties to even, once.  A slot outside [0, pool)
+ *                leaves the pool untouched and writes o = 0 for that row.  Two
+ *                rows naming the same slot race (undefined result).
+ *   o            [B, T, HV, V]  io dtype out
+ *
+ * Supported: bf16 or fp32 io, K and V in {64, 128}; 16-byte aligned tensors.
+ * Allocates nothing; asynchronous on `stream`.
+ */
+int kda_decode(const void* q, const void* k, const void* v, const void* a, const void* b,
+               const float* A_log, const float* dt_bias, void* state, int state_dtype, const int32_t* state_indices,
+               void* o, int B, int T, int H, int HV, int K, int V, int pool,
+               float scale, float softplus_beta, float softplus_threshold, int use_qk_l2norm, float eps,
+               int dtype, void* stream);
+
+/*
  * Selective state-space scan of prompts: per sequence and head,
  *
  *   D_t = softplus(dt_t + dt_bias)    (dt_softplus = 0: dt_t + dt_bias, which
@@ -599,7 +709,7 @@ enum {
   GDN_STAGE_VARLEN_TABLES = 0, /* varlen chunk tables                         */
   GDN_STAGE_INTRA = 1,         /* per-chunk (I + A)^-1 and Aqk                 */
   GDN_STAGE_SCAN = 2,          /* chunk-state scan fused with the output       */
-  GDN_STAGE_DECODE = 3,        /* decode step                                  */
+  GDN_STAGE_DECODE = 3,        /* decode steps                                 */
   GDN_STAGE_HANDOFF = 4,       /* prefill state -> decode pool (bf16)          */
   GDN_STAGE_BWD_DH = 5,        /* backward state-gradient scan                 */
   GDN_STAGE_FWD_H = 6,         /* forward decay-only state scan                */
@@ -607,7 +717,9 @@ enum {
   GDN_STAGE_SSM_SCAN = 8,      /* selective state-space scan (all launches)    */
   GDN_STAGE_SSM_STEP = 9,      /* selective state-space step                   */
   GDN_STAGE_STATE_Q8 = 10,     /* 8-bit state cache, store and load            */
-  GDN_STAGE_COUNT = 11
+  GDN_STAGE_CONV_BWD = 11,     /* gradients of the causal convolution          */
+  GDN_STAGE_NORM = 12,         /* group norm and its gradients                 */
+  GDN_STAGE_COUNT = 13
 };
 int gdn_profile_enable(int on);
 int gdn_profile_read(double* ms, int* counts);

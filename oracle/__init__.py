@@ -22,7 +22,7 @@ Sources (cited by page and function in each module):
   state (gate, q/k normalisation, per-token state update) and its state pool,
   into which a prefill's final state is handed over.
 
-The operators around the scans (``mixer``) follow their definitions in
+The operators around the scans (``mixer``, ``layer``) follow their definitions in
 ``include/gdn61.h``.
 
 Pins: every function here is checked in ``tests/test_oracle_*.py`` against
@@ -39,6 +39,7 @@ from .bf16 import round_to_bf16
 from .handoff import state_to_pool
 from .backward import state_grad_scan
 from .state_scan import state_scan
+from .layer import causal_conv_bwd, gdn_recurrent_bwd, group_norm, kda_step
 from .mixer import causal_conv, head_norm, quantise_state, silu, ssm_scan
 
 __all__ = [
@@ -46,5 +47,6 @@ __all__ = [
     "chunk_intra_matrices", "chunk_intra_wu",
     "decode_gate", "decode_normalize", "gdn_decode",
     "round_to_bf16", "state_to_pool", "state_grad_scan", "state_scan",
+    "causal_conv_bwd", "gdn_recurrent_bwd", "group_norm", "kda_step",
     "causal_conv", "head_norm", "quantise_state", "silu", "ssm_scan",
 ]
