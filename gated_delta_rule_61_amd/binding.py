@@ -74,6 +74,9 @@ _SIGNATURES = {
                      + [_c_float] + [_c_void_p] * 3 + [_c_int, _c_void_p] + [_c_int] * 6 + [_c_void_p]),
     "gdn_conv_step": (_c_int, [_c_void_p, _c_ll, _c_ll, _c_void_p, _c_void_p, _c_int] + [_c_void_p] * 3
                       + [_c_int] * 3 + [_c_void_p] * 2 + [_c_int] * 6 + [_c_void_p]),
+    "gdn_chunk_bwd_workspace_bytes": (_c_size_t, [_c_int] * 9),
+    "gdn_chunk_bwd": (_c_int, [_c_void_p] * 6 + [_c_float] + [_c_void_p] * 4 + [_c_int] * 9 + [_c_void_p] * 7
+                      + [_c_size_t, _c_void_p]),
     "gdn_conv_bwd_workspace_bytes": (_c_size_t, [_c_int] * 4),
     "gdn_conv_bwd": (_c_int, [_c_void_p] * 3 + [_c_int] * 3 + [_c_void_p, _c_ll, _c_ll, _c_void_p, _c_void_p]
                      + [_c_int] * 3 + [_c_float, _c_void_p] + [_c_int] * 6 + [_c_void_p] * 4 + [_c_size_t, _c_void_p]),
@@ -158,7 +161,7 @@ def _need(t: Optional[torch.Tensor], name: str, dtype: Optional[torch.dtype], sh
 
 
 STAGES = ("varlen_tables", "intra", "scan", "decode", "handoff", "bwd_dh", "fwd_h", "conv", "ssm_scan", "ssm_step",
-          "state_q8", "conv_bwd", "norm")
+          "state_q8", "conv_bwd", "norm", "bwd_scan", "bwd_grad")
 
 
 def profile_enable(on: bool = True) -> None:
@@ -697,6 +700,45 @@ def _scratch(workspace: Optional[torch.Tensor], nbytes: int, dev: torch.device):
     else:
         _need(workspace, "workspace", None, None, dev)
     return workspace, workspace.data_ptr()
+
+
+def chunk_bwd_workspace_bytes(B: int, T: int, Hk: int, HV: int, K: int, V: int, num_seqs: int, dtype: torch.dtype,
+                              varlen: bool = False) -> int:
+    """Workspace of ``gdn_chunk_bwd``, in bytes."""
+    return int(lib().gdn_chunk_bwd_workspace_bytes(B, T, Hk, HV, K, V, num_seqs, int(varlen), _io_code(dtype)))
+
+
+def gdn_chunk_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: Optional[torch.Tensor], beta: torch.Tensor,
+                  dout: torch.Tensor, dht: Optional[torch.Tensor] = None, scale: Optional[float] = None,
+                  h0: Optional[torch.Tensor] = None, cu_seqlens: Optional[torch.Tensor] = None, chunk_size: int = 64,
+                  g_gamma: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None):
+    """Gradients of ``gdn_chunk_fwd`` from ``dout`` [B,T,HV,V], that of its output
+    (io dtype), and ``dht`` [N,HV,V,K] fp32, that of its final states (None:
+    zeros); the other arguments as they were given there.  Returns (dq, dk, dv,
+    dg, dbeta, dh0) in the io dtype, of the shapes of q, k, v, g, beta and h0;
+    dg is None without ``g``, dh0 without ``h0``.  A ``workspace`` (of
+    ``chunk_bwd_workspace_bytes``; else allocated) serves one call at a time."""
+    if q.dim() != 4 or v.dim() != 4:
+        raise ValueError("q, k must be [B, T, Hk, K] and v [B, T, HV, V]")
+    dev = _cuda(q, "q")
+    B, T, Hk, HV, K, V, N, dev, io = _chunk_common(q, k, v, beta, h0, cu_seqlens, chunk_size, g, (), "g")
+    if g_gamma is not None:
+        if g is not None:
+            raise ValueError("pass g or g_gamma, not both")
+        _need(g_gamma, "g_gamma", torch.float32, (HV,), dev)
+    _want(dout, "dout", io, v.shape, dev)
+    _want(dht, "dht", torch.float32, (N, HV, V, K), dev)
+    dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
+    dg = None if g is None else torch.empty((B, T, HV), dtype=io, device=dev)
+    dbeta = torch.empty((B, T, HV), dtype=io, device=dev)
+    dh0 = None if h0 is None else torch.empty((N, HV, V, K), dtype=io, device=dev)
+    L, code = lib(), _io_code(io)
+    nbytes = int(L.gdn_chunk_bwd_workspace_bytes(B, T, Hk, HV, K, V, N, 0 if cu_seqlens is None else 1, code))
+    workspace, wp = _scratch(workspace, nbytes, dev)
+    _call(dev, L.gdn_chunk_bwd, _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(g_gamma), _ptr(beta),
+          K ** -0.5 if scale is None else scale, _ptr(h0), _ptr(dout), _ptr(dht), _ptr(cu_seqlens), N, B, T, Hk, HV, K, V,
+          chunk_size, code, _ptr(dq), _ptr(dk), _ptr(dv), _ptr(dg), _ptr(dbeta), _ptr(dh0), wp, nbytes)
+    return dq, dk, dv, dg, dbeta, dh0
 
 
 def causal_conv_bwd(dout, x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tensor] = None, *,

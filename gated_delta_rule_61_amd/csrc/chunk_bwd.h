@@ -1,0 +1,167 @@
+// Gradients of the chunked gated delta rule (scalar gate): the arrays that pass
+// between its launches, and what the kernels share.  Per chunk of 64 tokens, with
+// G the chunk-local cumulative gate, h = S^T [K, V] at the chunk's start, dh' the
+// gradient of the state at its end, A = (I + L)^-1 and P = scale tril(Q K^T o Gamma)
+// of the prefill's intra step:
+//
+//   states      R = beta (V - e^G K h),  Vn = A R,
+//               h <- e^{G_last} h + (e^{G_last - G} K)^T Vn
+//   gradients   Y = P^T dO + e^{G_last - G} K dh',  dR = A^T Y,
+//               dh <- e^{G_last} dh' + scale (e^G Q)^T dO - (beta e^G K)^T dR
+//   then        dq = scale (e^G dO h^T + tril(dO Vn^T o Gamma) K)
+//               E  = -(e^G dR h^T + stril(dR Vn^T o Gamma) K)
+//               W  = e^{G_last - G} Vn dh'^T + scale tril(dO Vn^T o Gamma)^T Q
+//                    - stril(dR Vn^T o Gamma)^T (beta K)
+//               dk = beta E + W,  dv = beta dR,  dbeta = v . dR + k . E
+//               dG = q . dq + beta k . E - k . W;  at the chunk's last row also
+//               <h', dh'> = e^{G_last} <h, dh'> + sum_t k_t . (e^{G_last - G_t} dh' Vn_t);
+//               dg = the sums of dG from each row to the chunk's end
+//
+// Every array that holds a gradient is kept times a power of two, one for each
+// (sequence, v-head), that brings the largest of its dO and dht to 2 .. 4: with
+// bf16 io the operands of the products are fp16 (2^-11 where bf16 has 2^-8), and
+// the gradients of a mean over many tokens lie far below fp16's normal numbers.
+#pragma once
+
+#include "gdn_device.h"
+#include "gdn_launch.h"
+#include "scan_tiles.h"
+
+namespace gdn {
+namespace bwd {
+
+constexpr int BT = 64;
+using tiles::perm_row;
+
+// The power of two that brings `amax` to 2 .. 4 (and its inverse); NaN where it is
+// not finite, which then every gradient of the (sequence, head) becomes.
+__device__ __forceinline__ float grad_scale(uint32_t amax_bits, float& inverse) {
+  const int e = (int)(amax_bits >> 23);   // biased exponent; the sign is clear
+  int up = amax_bits == 0 ? 0 : 128 - e;  // 2^up amax in [2, 4)
+  up = up > 126 ? 126 : up < -126 ? -126 : up;
+  float s = __builtin_bit_cast(float, (uint32_t)(127 + up) << 23);
+  inverse = __builtin_bit_cast(float, (uint32_t)(127 - up) << 23);
+  if (e == 255) s = inverse = __builtin_bit_cast(float, 0x7FC00000u);
+  return s;
+}
+
+// Eight values in a row from the two accumulators that hold them.
+__device__ __forceinline__ f32x8 both(const f32x4& a, const f32x4& b) {
+  return f32x8{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
+}
+
+// Two accumulators as one operand fragment.  fp16 without saturation: a value past
+// 65504 becomes an infinity, which shows in the result.
+__device__ __forceinline__ void join(Frag<f16_t>& f, const f32x4& a, const f32x4& b) {
+  f.v = __builtin_convertvector(both(a, b), f16x8);
+}
+__device__ __forceinline__ void join(Frag<float>& f, const f32x4& a, const f32x4& b) {
+  f.v = both(a, b);
+}
+
+// Eight consecutive values of the io type as the compute type.
+__device__ __forceinline__ Frag<f16_t> widen(const Frag<bf16_t>& a, float s) {
+  Frag<f16_t> r;
+  r.v = __builtin_convertvector(__builtin_convertvector(a.v, f32x8) * s, f16x8);
+  return r;
+}
+__device__ __forceinline__ Frag<f16_t> widen(const Frag<bf16_t>& a) {
+  Frag<f16_t> r;
+  r.v = __builtin_convertvector(__builtin_convertvector(a.v, f32x8), f16x8);
+  return r;
+}
+__device__ __forceinline__ Frag<float> widen(const Frag<float>& a, float s) {
+  Frag<float> r;
+  r.v = a.v * s;
+  return r;
+}
+__device__ __forceinline__ Frag<float> widen(const Frag<float>& a) { return a; }
+
+__device__ __forceinline__ f32x8 values(const Frag<f16_t>& a) { return __builtin_convertvector(a.v, f32x8); }
+__device__ __forceinline__ f32x8 values(const Frag<float>& a) { return a.v; }
+__device__ __forceinline__ f32x8 values(const Frag<bf16_t>& a) { return __builtin_convertvector(a.v, f32x8); }
+
+__device__ __forceinline__ void store8(f16_t* p, const Frag<f16_t>& f) {
+  store_nt16(p, __builtin_bit_cast(tiles::u32x4, f.v));
+}
+__device__ __forceinline__ void store8(float* p, const Frag<float>& f) {
+  store_nt16(p, f32x4{f.v[0], f.v[1], f.v[2], f.v[3]});
+  store_nt16(p + 4, f32x4{f.v[4], f.v[5], f.v[6], f.v[7]});
+}
+// ... eight fp32 values in the io type
+__device__ __forceinline__ void store_io8(bf16_t* p, const f32x8& x) {
+  store_nt16(p, tiles::u32x4{pack_bf2(x[0], x[1]), pack_bf2(x[2], x[3]), pack_bf2(x[4], x[5]), pack_bf2(x[6], x[7])});
+}
+__device__ __forceinline__ void store_io8(float* p, const f32x8& x) {
+  store_nt16(p, f32x4{x[0], x[1], x[2], x[3]});
+  store_nt16(p + 4, f32x4{x[4], x[5], x[6], x[7]});
+}
+
+// An LDS tile of rows of COLS elements.  16-bit: 16-byte units swizzled by row as
+// in the prefill's scan (row fragments and transposing reads without bank
+// conflicts).  fp32: rows padded by 16 bytes.
+template <typename C, int COLS> struct Tile;
+template <int COLS> struct Tile<f16_t, COLS> {
+  static constexpr int pitch = 2 * COLS;
+  static constexpr int bytes(int rows) { return rows * pitch; }
+  static __device__ __forceinline__ int off(int row, int col) {   // byte of an element; col a multiple of 4
+    int u;
+    if constexpr (COLS == 128) u = tiles::qk_off<128>(row, col >> 3);
+    else u = tiles::a_off(row, col >> 3);
+    return u + 2 * (col & 4);
+  }
+  static __device__ __forceinline__ void put(char* t, int row, int col, const Frag<f16_t>& f) {
+    *reinterpret_cast<f16x8*>(t + off(row, col)) = f.v;
+  }
+  // four consecutive values of a row
+  static __device__ __forceinline__ void put4(char* t, int row, int col, const f32x4& x) {
+    typedef _Float16 f16x4 __attribute__((ext_vector_type(4)));
+    *reinterpret_cast<f16x4*>(t + off(row, col)) = __builtin_convertvector(x, f16x4);
+  }
+  // row `row`, columns col .. col + 7
+  static __device__ __forceinline__ Frag<f16_t> row8(const char* t, int row, int col) {
+    Frag<f16_t> f;
+    f.v = *reinterpret_cast<const f16x8*>(t + off(row, col));
+    return f;
+  }
+  // rows r0 .. r0 + 7 of the lane's column: column n of the block's 16 (NATURAL:
+  // col0 + n; else the permuted order of block col0 / 16 of a pair)
+  template <bool NATURAL>
+  static __device__ __forceinline__ Frag<f16_t> col8(const char* t, int r0, int blk, int n) {
+    const int c = NATURAL ? 16 * blk + 4 * (n & 3) : perm_row(blk, 4 * (n & 3));
+    const int r = r0 + (n >> 2);
+    const uint2 lo = tiles::ld_tr(t + off(r, c)), hi = tiles::ld_tr(t + off(r + 4, c));
+    Frag<f16_t> f;
+    f.v = __builtin_bit_cast(f16x8, tiles::u32x4{lo.x, lo.y, hi.x, hi.y});
+    return f;
+  }
+};
+template <int COLS> struct Tile<float, COLS> {
+  static constexpr int pitch = 4 * COLS + 16;
+  static constexpr int bytes(int rows) { return rows * pitch; }
+  static __device__ __forceinline__ int off(int row, int col) { return row * pitch + 4 * col; }
+  static __device__ __forceinline__ void put(char* t, int row, int col, const Frag<float>& f) {
+    float* p = reinterpret_cast<float*>(t + off(row, col));
+    *reinterpret_cast<f32x4*>(p) = f32x4{f.v[0], f.v[1], f.v[2], f.v[3]};
+    *reinterpret_cast<f32x4*>(p + 4) = f32x4{f.v[4], f.v[5], f.v[6], f.v[7]};
+  }
+  static __device__ __forceinline__ void put4(char* t, int row, int col, const f32x4& x) {
+    *reinterpret_cast<f32x4*>(t + off(row, col)) = x;
+  }
+  static __device__ __forceinline__ Frag<float> row8(const char* t, int row, int col) {
+    Frag<float> f;
+    load8(f, reinterpret_cast<const float*>(t + off(row, col)));
+    return f;
+  }
+  template <bool NATURAL>
+  static __device__ __forceinline__ Frag<float> col8(const char* t, int r0, int blk, int n) {
+    const int c = NATURAL ? 16 * blk + n : perm_row(blk, n);
+    Frag<float> f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) f.v[e] = *reinterpret_cast<const float*>(t + off(r0 + e, c));
+    return f;
+  }
+};
+
+}  // namespace bwd
+}  // namespace gdn

@@ -281,6 +281,55 @@ hipError_t launch_chunk_fwd(const ChunkArgs& a, hipStream_t s) {
   return e;
 }
 
+hipError_t launch_chunk_bwd(const ChunkBwdArgs& b, hipStream_t s) {
+  const ChunkArgs& a = b.f;
+  if (a.cu_seqlens) {
+    prof_begin(GDN_STAGE_VARLEN_TABLES, s);
+    hipLaunchKernelGGL(varlen_tables_kernel, dim3(1), dim3(1024), 0, s, a.cu_seqlens, a.N, a.T,
+                       a.chunk_off, a.seq_order);
+    hipError_t e = hipGetLastError();
+    prof_end(GDN_STAGE_VARLEN_TABLES, s);
+    if (e != hipSuccess) return e;
+  }
+  const bool work = b.nslots > 0 && (long long)a.B * a.T > 0;
+  if (work) {
+    prof_begin(GDN_STAGE_INTRA, s);
+    hipError_t e = launch_intra_gdn(a, s, (a.T + 63) / 64, b.nslots);
+    prof_end(GDN_STAGE_INTRA, s);
+    if (e != hipSuccess) return e;
+  }
+  prof_begin(GDN_STAGE_BWD_SCAN, s);
+  hipError_t e = b.amax ? launch_chunk_bwd_amax(b, s) : hipSuccess;
+  if (e == hipSuccess) e = launch_chunk_bwd_scan(b, s);
+  prof_end(GDN_STAGE_BWD_SCAN, s);
+  if (e != hipSuccess || !work) return e;
+  prof_begin(GDN_STAGE_BWD_GRAD, s);
+  e = launch_chunk_bwd_grad(b, s);
+  prof_end(GDN_STAGE_BWD_GRAD, s);
+  return e;
+}
+
+// Workspace of the gradients: the prefill's, then what passes between the launches.
+struct BwdWorkspace {
+  ChunkWorkspace f;
+  size_t amax, hs, ds, vn, dr, total;
+  int nslots;
+};
+static BwdWorkspace bwd_workspace_layout(int B, int T, int HV, int K, int V, int N, bool varlen, bool bf16) {
+  BwdWorkspace w;
+  const int NT = (T + 63) / 64, eb = bf16 ? 2 : 4;
+  w.nslots = varlen ? NT + N : B * NT;
+  w.f = chunk_workspace_layout((long long)B * T, HV, K, N, NT * B + N, eb, false);
+  const size_t cells = (size_t)w.nslots * HV;
+  w.amax = w.f.total;
+  w.hs = w.amax + up((size_t)N * HV * 4);
+  w.ds = w.hs + up(cells * K * V * eb);
+  w.vn = w.ds + up(cells * K * V * eb);
+  w.dr = w.vn + up(cells * V * 64 * eb);
+  w.total = w.dr + up(cells * V * 64 * eb);
+  return w;
+}
+
 }  // namespace gdn
 
 using namespace gdn;
@@ -359,6 +408,56 @@ int gdn_chunk_fwd(const void* q, const void* k, const void* v, const float* g,
   a.seq_order = cu_seqlens ? (int32_t*)(ws + L.order_off) : nullptr;
   a.max_chunks = (T + 63) / 64 * B + (cu_seqlens ? P.N : 0);
   const hipError_t e = launch_chunk_fwd(a, (hipStream_t)stream);
+  if (e != hipSuccess) return fail(GDN_ERR_LAUNCH, "HIP launch failed: %s", hipGetErrorString(e));
+  return ok();
+}
+
+size_t gdn_chunk_bwd_workspace_bytes(int B, int T, int Hk, int HV, int K, int V, int num_seqs, int varlen,
+                                     int dtype) {
+  if (B < 0 || T < 0 || Hk <= 0 || HV <= 0 || K <= 0 || V <= 0 || num_seqs < 0) return 0;
+  if (dtype != GDN_DTYPE_F32 && dtype != GDN_DTYPE_BF16) return 0;
+  if ((long long)B * T >= (1LL << 31) / 64) return 0;
+  return bwd_workspace_layout(B, T, HV, K, V, varlen ? num_seqs : B, varlen != 0, dtype == GDN_DTYPE_BF16).total;
+}
+
+int gdn_chunk_bwd(const void* q, const void* k, const void* v, const float* g, const float* g_gamma,
+                  const float* beta, float scale, const float* h0, const void* dout, const float* dht,
+                  const int64_t* cu_seqlens, int num_seqs, int B, int T, int Hk, int HV, int K, int V,
+                  int chunk_size, int dtype, void* dq, void* dk, void* dv, void* dg, void* dbeta, void* dh0,
+                  void* workspace, size_t workspace_bytes, void* stream) {
+  Problem P;
+  int st = check_chunk(q, k, v, g, false, beta, h0, nullptr, nullptr, 64, 0, GDN_DTYPE_F32, cu_seqlens, num_seqs, B,
+                       T, Hk, HV, K, V, chunk_size, dtype, dout, P);
+  if (st != GDN_OK) return st;
+  if (g && g_gamma) return fail(GDN_ERR_INVALID_ARGUMENT, "pass g or g_gamma, not both");
+  if ((long long)B * T > 0 && (!dq || !dk || !dv || !dbeta))
+    return fail(GDN_ERR_INVALID_ARGUMENT, "dout, dq, dk, dv and dbeta are required");
+  const void* ptrs[] = {dht, dq, dk, dv, dg, dbeta, dh0};
+  for (const void* p : ptrs)
+    if (p && !aligned16(p)) return fail(GDN_ERR_INVALID_ARGUMENT, "tensor pointers must be 16-byte aligned");
+  const bool bf16 = dtype == GDN_DTYPE_BF16;
+  const BwdWorkspace L = bwd_workspace_layout(B, T, HV, K, V, P.N, cu_seqlens != nullptr, bf16);
+  if (!workspace || workspace_bytes < L.total)
+    return fail(GDN_ERR_WORKSPACE, "workspace of %zu bytes needed (got %zu)", L.total,
+                workspace ? workspace_bytes : (size_t)0);
+  if (((uintptr_t)workspace & 255u) != 0)
+    return fail(GDN_ERR_INVALID_ARGUMENT, "workspace must be 256-byte aligned");
+  if (P.N == 0) return ok();
+  char* ws = (char*)workspace;
+  ChunkBwdArgs a{};
+  ChunkArgs& f = a.f;
+  f.q = q; f.k = k; f.v = v; f.g = g; f.g_gamma = g_gamma; f.beta = beta; f.scale = scale; f.h0 = h0;
+  f.cu_seqlens = cu_seqlens; f.N = P.N; f.B = B; f.T = T; f.Hk = Hk; f.HV = HV; f.K = K; f.V = V; f.bf16 = bf16;
+  f.Ainv = ws + L.f.ainv_off;
+  f.Aqk = ws + L.f.aqk_off;
+  f.GF = ws + L.f.gf_off;
+  f.chunk_off = cu_seqlens ? (int32_t*)(ws + L.f.coff_off) : nullptr;
+  f.seq_order = cu_seqlens ? (int32_t*)(ws + L.f.order_off) : nullptr;
+  a.dout = dout; a.dht = dht; a.dq = dq; a.dk = dk; a.dv = dv; a.dg = dg; a.dbeta = dbeta; a.dh0 = dh0;
+  a.amax = bf16 ? (uint32_t*)(ws + L.amax) : nullptr;
+  a.hs = ws + L.hs; a.ds = ws + L.ds; a.vn = ws + L.vn; a.dr = ws + L.dr;
+  a.nslots = L.nslots;
+  const hipError_t e = launch_chunk_bwd(a, (hipStream_t)stream);
   if (e != hipSuccess) return fail(GDN_ERR_LAUNCH, "HIP launch failed: %s", hipGetErrorString(e));
   return ok();
 }

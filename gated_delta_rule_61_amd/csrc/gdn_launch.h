@@ -113,6 +113,24 @@ struct KdaBuffers {
 };
 hipError_t launch_kda_fwd(const ChunkArgs& a, const KdaBuffers& kb, hipStream_t s);
 
+// Gradients of the chunked rule (scalar gate).
+struct ChunkBwdArgs {
+  ChunkArgs f;           // the forward problem; of its outputs the workspace arrays only
+  const void* dout;      // [B, T, HV, V]
+  const float* dht;      // [N, HV, V, K] or nullptr
+  void *dq, *dk, *dv;    // [B, T, Hk, K] x 2, [B, T, HV, V]
+  void *dg, *dbeta;      // [B, T, HV]; dg may be nullptr
+  void* dh0;             // [N, HV, V, K] or nullptr
+  // workspace
+  uint32_t* amax;        // [N, HV] bits of the largest |dout|, |dht| (bf16 io)
+  void *hs, *ds;         // [chunks, HV, V, K] states at the chunks' starts, gradients at their ends
+  void *vn, *dr;         // [chunks, HV, V, 64] new values, their gradients, a column a row
+  int nslots;            // chunks that these hold
+};
+hipError_t launch_chunk_bwd_amax(const ChunkBwdArgs& a, hipStream_t s);
+hipError_t launch_chunk_bwd_scan(const ChunkBwdArgs& a, hipStream_t s);
+hipError_t launch_chunk_bwd_grad(const ChunkBwdArgs& a, hipStream_t s);
+
 // The scalar-gate intra-chunk step on its own: A = (I + L)^-1, w, u.
 struct IntraArgs {
   const void *k, *v;               // [B*T, Hk, K], [B*T, HV, V] io dtype

@@ -187,6 +187,49 @@ int gdn_chunk_fwd_noalloc(const void* q, const void* k, const void* v,
                           int chunk_size, int dtype, void* o, void* stream);
 
 /*
+ * Gradients of gdn_chunk_fwd: from those of its outputs o (dout) and final states
+ * (dht) to those of q, k, v, the gates, beta and the initial states, for
+ *
+ *   S_t = e^{g_t} S_{t-1} (I - beta_t k_t k_t^T) + beta_t v_t k_t^T,  o_t = scale S_t q_t.
+ *
+ *   q, k, v, g, g_gamma, beta, scale, h0, cu_seqlens, ...   as they were given there
+ *                (nothing is kept from the forward call: the states are computed
+ *                again)
+ *   dout         [B, T, HV, V]  io dtype
+ *   dht          [N, HV, V, K]  fp32, or NULL (zeros)
+ *   dq, dk       [B, T, Hk, K]  io dtype out, sums over the v-heads of a key head
+ *   dv           [B, T, HV, V]  io dtype out
+ *   dg           [B, T, HV]     io dtype out, or NULL: the gradient of each token's
+ *                               log-gate (with g_gamma too: its tokens' sum is that
+ *                               of the head's fixed decay)
+ *   dbeta        [B, T, HV]     io dtype out
+ *   dh0          [N, HV, V, K]  io dtype out, or NULL (also without h0)
+ *   workspace    device buffer of gdn_chunk_bwd_workspace_bytes() bytes, 256-byte
+ *                aligned (varlen: whether cu_seqlens is given).  Calls that share
+ *                one (captured graphs too) must not run at the same time.
+ *
+ * Every gradient is of the io dtype.  With bf16 io the operands of the products
+ * (states, gradients of states and of the new values, scores) are fp16 with fp32
+ * sums, which limits all of them alike; the gradients among them are kept times a
+ * power of two, one for each (sequence, v-head), that brings the largest |dout|
+ * and |dht| of it to 2 .. 4, so gradients of any size keep their precision, and
+ * one 2^-16 of its head's largest still has a bf16's.  A value past 65504 times
+ * that scale becomes an infinity; where dout or dht hold an infinity or NaN, all
+ * gradients of that sequence and head (of the key head, for dq and dk, in the
+ * chunks of the sequence) are NaN.  fp32 io: fp32 throughout.  The same bits in
+ * every run.  Supported sizes and errors as in gdn_chunk_fwd.  T = 0 (or all
+ * sequences empty) is valid: dh0 = dht (or zeros) is written.
+ */
+size_t gdn_chunk_bwd_workspace_bytes(int B, int T, int Hk, int HV, int K, int V, int num_seqs, int varlen,
+                                     int dtype);
+int gdn_chunk_bwd(const void* q, const void* k, const void* v, const float* g, const float* g_gamma,
+                  const float* beta, float scale, const float* h0, const void* dout, const float* dht,
+                  const int64_t* cu_seqlens, int num_seqs,
+                  int B, int T, int Hk, int HV, int K, int V, int chunk_size, int dtype,
+                  void* dq, void* dk, void* dv, void* dg, void* dbeta, void* dh0,
+                  void* workspace, size_t workspace_bytes, void* stream);
+
+/*
  * KDA chunked prefill forward (one log-gate per key channel).
  *
  * As gdn_chunk_fwd, with
@@ -719,7 +762,9 @@ enum {
   GDN_STAGE_STATE_Q8 = 10,     /* 8-bit state cache, store and load            */
   GDN_STAGE_CONV_BWD = 11,     /* gradients of the causal convolution          */
   GDN_STAGE_NORM = 12,         /* group norm and its gradients                 */
-  GDN_STAGE_COUNT = 13
+  GDN_STAGE_BWD_SCAN = 13,     /* the chunked rule's gradients: both state scans */
+  GDN_STAGE_BWD_GRAD = 14,     /* ... and the chunks' gradients                */
+  GDN_STAGE_COUNT = 15
 };
 int gdn_profile_enable(int on);
 int gdn_profile_read(double* ms, int* counts);

@@ -177,3 +177,57 @@ def test_binding_refuses():
         binding.kda_decode(q, q, q, q, q[..., 0], w[0], w, q)
     with pytest.raises(ValueError, match=r"\[B, T, H, K\]"):
         binding.kda_decode(q[0], q, q, q, q[..., 0], w[0], w, q)
+
+
+def _chunk_bwd(L, **kw):
+    a = dict(q=FAKE, k=FAKE, v=FAKE, g=FAKE, gamma=None, beta=FAKE, scale=1.0, h0=None, do=FAKE, dht=None, cu=None, n=0,
+             B=2, T=64, Hk=2, HV=4, K=128, V=128, cs=64, dt=1, dq=FAKE, dk=FAKE, dv=FAKE, dg=FAKE, db=FAKE, dh0=None,
+             ws=FAKE, wsb=1 << 40)
+    a.update(kw)
+    return L.gdn_chunk_bwd(*a.values(), None)
+
+
+@pytest.mark.parametrize("kw,status,msg", [
+    (dict(K=96, V=96), 2, b"head dims"),
+    (dict(K=64), 2, b"head dims"),
+    (dict(Hk=3), 1, b"multiple"),
+    (dict(HV=0), 1, b"sizes"),
+    (dict(cs=32), 2, b"chunk_size"),
+    (dict(dt=3), 1, b"dtype"),
+    (dict(gamma=FAKE), 1, b"not both"),
+    (dict(q=None), 1, b"required"),
+    (dict(do=None), 1, b"required"),
+    (dict(dq=None), 1, b"required"),
+    (dict(db=None), 1, b"required"),
+    (dict(do=FAKE + 8), 1, b"aligned"),
+    (dict(dk=FAKE + 8), 1, b"aligned"),
+    (dict(dht=FAKE + 4), 1, b"aligned"),
+    (dict(cu=FAKE, n=2), 1, b"B == 1"),
+    (dict(cu=FAKE, n=-2, B=1), 1, b"num_seqs"),
+    (dict(B=1 << 13, T=1 << 13), 2, b"too large"),
+    (dict(ws=None), 4, b"workspace"),
+    (dict(wsb=1024), 4, b"workspace"),
+    (dict(ws=FAKE + 128), 1, b"256-byte"),
+])
+def test_chunk_bwd_refuses(L, kw, status, msg):
+    assert _chunk_bwd(L, **kw) == status
+    assert msg in L.gdn_last_error()
+
+
+def test_chunk_bwd_workspace(L):
+    size = L.gdn_chunk_bwd_workspace_bytes
+    assert size(1, 64, 2, 4, 128, 128, 1, 0, 9) == 0
+    assert size(1, -1, 2, 4, 128, 128, 1, 0, 1) == 0
+    # a chunk: two states and two [64, V] arrays of the compute type, and the prefill's arrays
+    assert size(1, 64, 1, 1, 128, 128, 1, 0, 1) >= 2 * (2 * 128 * 128 + 2 * 64 * 128)
+    assert size(1, 64, 1, 1, 128, 128, 1, 0, 0) >= 2 * size(1, 64, 1, 1, 128, 128, 1, 0, 1) - 4096
+    assert size(1, 64, 1, 1, 128, 128, 5, 1, 1) > 4 * size(1, 64, 1, 1, 128, 128, 1, 0, 1)
+    assert _chunk_bwd(L, cu=FAKE, n=0, B=1) == 0
+
+
+def test_chunk_bwd_binding_refuses():
+    q = torch.zeros(1, 4, 2, 64)
+    with pytest.raises(ValueError, match="on a GPU"):
+        binding.gdn_chunk_bwd(q, q, q, q[..., 0], q[..., 0], q)
+    with pytest.raises(ValueError, match=r"\[B, T, Hk, K\]"):
+        binding.gdn_chunk_bwd(q[0], q, q, q[..., 0], q[..., 0], q)
