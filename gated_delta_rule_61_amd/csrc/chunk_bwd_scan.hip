@@ -4,20 +4,23 @@
 // the other, and every V column of either stands for itself: one launch runs both
 // at once, with twice the work-groups of one.
 //
-// A work-group is one (sequence, v-head, 64 columns, direction): four waves of 16
-// columns, whose state (K x 16, fp32) stays in MFMA accumulators.  As in the
-// prefill's scan, rows of the A operands are placed so that two accumulators are
-// the next product's B operand, without a trip through LDS: K h -> R -> A R ->
-// state, and K dh' -> Y -> A^T Y -> state.  The chunk's K (and Q), A (and P), v or
-// dO tiles are shared through LDS, in the compute type, rows behind the
-// sequence's end as zeros; those of the next chunk are in flight in registers
-// meanwhile.  Row fragments are 16-byte reads; K^T, Q^T, A^T, P^T and dO^T come
-// from the same tiles by transposing reads.
+// A work-group is one (sequence, v-head, 64 columns, direction): four state waves
+// of 16 columns, one per SIMD, whose state (K x 16, fp32) stays in MFMA
+// accumulators, and four movers.  As in the prefill's scan, rows of the A operands
+// are placed so that two accumulators are the next product's B operand, without a
+// trip through LDS: K h -> R -> A R -> state, and K dh' -> Y -> A^T Y -> state.
+// The movers bring the next chunk's K (and Q), A (and P), v or dO tiles into the
+// other half of a double buffer in LDS, in the compute type, rows behind the
+// sequence's end as zeros, with the chunk after that in flight in their registers;
+// one barrier a chunk.  Row fragments are 16-byte reads; K^T, Q^T, A^T, P^T and
+// dO^T come from the same tiles by transposing reads.  (fp32 tiles fit once: the
+// movers then write between two barriers.)
 //
 // h and dh' leave as [V][K] rows, Vn and dR transposed ([V][64]): what a lane's
 // accumulators hold in order.
 
 #include "chunk_bwd.h"
+#include "chunk_common.h"
 
 namespace gdn {
 
@@ -48,6 +51,7 @@ struct ScanLds {
   static constexpr int Q = G + 4 * BT * 4;                     // backward only
   static constexpr int P = Q + Tile<C, D>::bytes(BT);
   static constexpr int bytes = P + Tile<C, 64>::bytes(BT);
+  static constexpr int stages = 2 * bytes <= 160 * 1024 ? 2 : 1;
 };
 
 // A [64][COLS] tile on its way from global memory to LDS: 256 threads, 8
@@ -98,22 +102,18 @@ template <> struct VTile<float> {
 };
 
 template <typename T, int D>
-__global__ __launch_bounds__(256) void gdn_bwd_scan_kernel(ChunkBwdArgs a) {
+__global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))) void gdn_bwd_scan_kernel(ChunkBwdArgs a) {
   typedef typename ComputeOf<T>::type C;
   typedef ScanLds<T, C, D> L;
   typedef Tile<C, D> TK;
   typedef Tile<C, 64> TA;
   constexpr int KS = D / 32, KB = D / 16, NVT = D / 64;
+  constexpr bool TWO = L::stages == 2;
   extern __shared__ __attribute__((aligned(16))) char lds[];
-  char* const sK = lds + L::K;
-  char* const sA = lds + L::A;
-  char* const sV = lds + L::V;
-  float* const sG = reinterpret_cast<float*>(lds + L::G);
-  char* const sQ = lds + L::Q;
-  char* const sP = lds + L::P;
 
-  const int tid = threadIdx.x, lane = tid & 63, n = lane & 15, g = lane >> 4;
+  const int tid = threadIdx.x & 255, lane = tid & 63, n = lane & 15, g = lane >> 4;
   const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const bool mover = __builtin_amdgcn_readfirstlane(threadIdx.x >> 8) != 0;
   const int Hk = a.f.Hk, HV = a.f.HV;
 
   // Work-group -> (sequence, head, columns, direction).  Ids are dealt round-robin to
@@ -138,7 +138,82 @@ __global__ __launch_bounds__(256) void gdn_bwd_scan_kernel(ChunkBwdArgs a) {
   const size_t sbase = (((size_t)ns * HV + j) * D + vrow) * D;
 
   float inv = 1.f, gs = 1.f;
-  if (back && a.amax) gs = grad_scale(a.amax[(size_t)ns * HV + j], inv);
+  if (back && a.amax) {
+    // the largest gradient of the (sequence, head): of dht, and of the chunks' quarters
+    uint32_t* const sm = reinterpret_cast<uint32_t*>(lds);
+    uint32_t m = a.dht ? a.amax_dht[(size_t)ns * HV + j] : 0;
+    for (int i = threadIdx.x; i < 4 * NC; i += 512) m = max(m, a.part[((size_t)slot0 * 4 + i) * HV + j]);
+#pragma unroll
+    for (int off = 32; off > 0; off >>= 1) m = max(m, (uint32_t)__shfl_xor((int)m, off, 64));
+    if (lane == 0) sm[threadIdx.x >> 6] = m;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m = max(m, sm[i]);
+    __syncthreads();
+    gs = grad_scale(m, inv);
+    if (v0 == 0 && threadIdx.x == 0) a.amax[(size_t)ns * HV + j] = m;   // for the chunks' gradients
+  }
+  auto chunk_of = [&](int i) { return back ? NC - 1 - i : i; };
+
+  if (mover) {
+    const size_t krow = (size_t)Hk * D, vstride = (size_t)HV * D, arow = (size_t)HV * BT;
+    const size_t plane = (size_t)gf_stride((long long)a.f.B * a.f.T);
+    const T* const vsrc = reinterpret_cast<const T*>(back ? a.dout : a.f.v) + (size_t)j * D + v0;
+    const C* const Ain = reinterpret_cast<const C*>(a.f.Ainv) + (size_t)j * BT;
+    const C* const Pin = reinterpret_cast<const C*>(a.f.Aqk) + (size_t)j * BT;
+    const float* const GF = reinterpret_cast<const float*>(a.f.GF) + (size_t)j * 4 * plane;
+    Stage<T, D> k_in, q_in;
+    Stage<C, 64> a_in, p_in;
+    Stage<T, 64> v_in;
+    float gate_in = 0.f;
+    auto fetch = [&](int i) {
+      const int c0 = bos + BT * chunk_of(i), nrow = eos - c0 < BT ? eos - c0 : BT;
+      const size_t t0 = (size_t)c0;
+      k_in.load(reinterpret_cast<const T*>(a.f.k) + (size_t)jk * D + t0 * krow, krow, nrow, tid);
+      a_in.load(Ain + t0 * arow, arow, nrow, tid);
+      v_in.load(vsrc + t0 * vstride, vstride, nrow, tid);
+      if (back) {
+        q_in.load(reinterpret_cast<const T*>(a.f.q) + (size_t)jk * D + t0 * krow, krow, nrow, tid);
+        p_in.load(Pin + t0 * arow, arow, nrow, tid);
+      }
+      gate_in = lane < nrow ? GF[(size_t)w * plane + t0 + lane] : 0.f;
+    };
+    auto place = [&](char* st) {
+      k_in.each([&](int r, int col, const Frag<T>& f) { TK::put(st + L::K, r, col, widen(f)); }, tid);
+      a_in.each([&](int r, int col, const Frag<C>& f) { TA::put(st + L::A, r, col, f); }, tid);
+      reinterpret_cast<float*>(st + L::G)[tid] = gate_in;
+      if (back) {
+        v_in.each([&](int r, int col, const Frag<T>& f) { TA::put(st + L::V, r, col, widen(f, gs)); }, tid);
+        q_in.each([&](int r, int col, const Frag<T>& f) { TK::put(st + L::Q, r, col, widen(f)); }, tid);
+        p_in.each([&](int r, int col, const Frag<C>& f) { TA::put(st + L::P, r, col, f); }, tid);
+      } else {
+        v_in.each([&](int r, int col, const Frag<T>& f) { VTile<T>::put(st + L::V, r, col, f); }, tid);
+      }
+    };
+    if (NC > 0) fetch(0);
+    if constexpr (TWO) {
+      if (NC > 0) {
+        place(lds);
+        if (NC > 1) fetch(1);
+      }
+      tiles::lds_barrier();
+      for (int i = 0; i < NC; ++i) {
+        if (i + 1 < NC) {
+          place(lds + ((i + 1) & 1) * L::bytes);
+          if (i + 2 < NC) fetch(i + 2);
+        }
+        tiles::lds_barrier();
+      }
+    } else {
+      for (int i = 0; i < NC; ++i) {
+        place(lds);
+        if (i + 1 < NC) fetch(i + 1);
+        tiles::lds_barrier();
+        tiles::lds_barrier();
+      }
+    }
+    return;
+  }
 
   f32x4 S[KB];
   const float* init = back ? a.dht : a.f.h0;
@@ -147,71 +222,26 @@ __global__ __launch_bounds__(256) void gdn_bwd_scan_kernel(ChunkBwdArgs a) {
     S[kb] = zero4();
     if (init) S[kb] = *reinterpret_cast<const f32x4*>(init + sbase + perm_row(kb, 4 * g)) * gs;
   }
-
-  const size_t krow = (size_t)Hk * D, vstride = (size_t)HV * D, arow = (size_t)HV * BT;
-  const size_t plane = (size_t)gf_stride((long long)a.f.B * a.f.T);
-  const T* const vsrc = reinterpret_cast<const T*>(back ? a.dout : a.f.v) + (size_t)j * D + v0;
-  const C* const Ain = reinterpret_cast<const C*>(a.f.Ainv) + (size_t)j * BT;
-  const C* const Pin = reinterpret_cast<const C*>(a.f.Aqk) + (size_t)j * BT;
-  const float* const GF = reinterpret_cast<const float*>(a.f.GF) + (size_t)j * 4 * plane;
-
-  Stage<T, D> k_in, q_in;
-  Stage<C, 64> a_in, p_in;
-  Stage<T, 64> v_in;
-  float gate_in = 0.f;
-  auto fetch = [&](int c) {
-    const int c0 = bos + BT * c, nrow = eos - c0 < BT ? eos - c0 : BT;
-    const size_t t0 = (size_t)c0;
-    k_in.load(reinterpret_cast<const T*>(a.f.k) + (size_t)jk * D + t0 * krow, krow, nrow, tid);
-    a_in.load(Ain + t0 * arow, arow, nrow, tid);
-    v_in.load(vsrc + t0 * vstride, vstride, nrow, tid);
-    if (back) {
-      q_in.load(reinterpret_cast<const T*>(a.f.q) + (size_t)jk * D + t0 * krow, krow, nrow, tid);
-      p_in.load(Pin + t0 * arow, arow, nrow, tid);
-    }
-    gate_in = lane < nrow ? GF[(size_t)w * plane + t0 + lane] : 0.f;
-  };
-  auto place = [&]() {
-    k_in.each([&](int r, int col, const Frag<T>& f) { TK::put(sK, r, col, widen(f)); }, tid);
-    a_in.each([&](int r, int col, const Frag<C>& f) { TA::put(sA, r, col, f); }, tid);
-    sG[tid] = gate_in;
-    if (back) {
-      v_in.each([&](int r, int col, const Frag<T>& f) { TA::put(sV, r, col, widen(f, gs)); }, tid);
-      q_in.each([&](int r, int col, const Frag<T>& f) { TK::put(sQ, r, col, widen(f)); }, tid);
-      p_in.each([&](int r, int col, const Frag<C>& f) { TA::put(sP, r, col, f); }, tid);
-    } else {
-      v_in.each([&](int r, int col, const Frag<T>& f) { VTile<T>::put(sV, r, col, f); }, tid);
-    }
-  };
-  // state and column stores of chunk c
+  // state and column stores of a chunk
   const size_t chunk_state = (size_t)HV * D * D, chunk_cols = (size_t)HV * D * BT;
   C* const st_out = reinterpret_cast<C*>(back ? a.ds : a.hs) + ((size_t)j * D + vrow) * D;
   C* const col_out = reinterpret_cast<C*>(back ? a.dr : a.vn) + ((size_t)j * D + vrow) * BT;
 
-  if (NC > 0) fetch(back ? NC - 1 : 0);
+  if constexpr (TWO) tiles::lds_barrier();
   for (int i = 0; i < NC; ++i) {
-    const int c = back ? NC - 1 - i : i;
-    const size_t slot = (size_t)(slot0 + c);
-    __syncthreads();
-    place();
-    if (i + 1 < NC) fetch(back ? c - 1 : c + 1);
-    __syncthreads();
+    const size_t slot = (size_t)(slot0 + chunk_of(i));
+    const char* const st = lds + (TWO ? (i & 1) * L::bytes : 0);
+    const char* const sK = st + L::K;
+    const char* const sA = st + L::A;
+    const char* const sV = st + L::V;
+    const float* const sG = reinterpret_cast<const float*>(st + L::G);
+    const char* const sQ = st + L::Q;
+    const char* const sP = st + L::P;
+    if constexpr (!TWO) tiles::lds_barrier();
 
-    Frag<C> Sh[KS];
-#pragma unroll
-    for (int s = 0; s < KS; ++s) {
-      join(Sh[s], S[2 * s], S[2 * s + 1]);
-      store8(st_out + slot * chunk_state + 32 * s + 8 * g, Sh[s]);
-    }
-    // X = K S, lane: tokens perm_row(tb, 4 g + i), column n
-    f32x4 X[4];
-#pragma unroll
-    for (int tb = 0; tb < 4; ++tb) X[tb] = zero4();
-#pragma unroll
-    for (int s = 0; s < KS; ++s)
-#pragma unroll
-      for (int tb = 0; tb < 4; ++tb) X[tb] = mma(TK::row8(sK, perm_row(tb, n), 32 * s + 8 * g), Sh[s], X[tb]);
-    f32x4 ex[4], ey[4], bz[4];
+    // lane: tokens perm_row(tb, 4 g + i), column n
+    f32x4 X[4], Z[4], ex[4], ey[4], bz[4];
+    Frag<C> Sh[KS], Zf[2], dO[2];
 #pragma unroll
     for (int tb = 0; tb < 4; ++tb) {
       ex[tb] = *reinterpret_cast<const f32x4*>(sG + perm_row(tb, 4 * g));
@@ -219,8 +249,29 @@ __global__ __launch_bounds__(256) void gdn_bwd_scan_kernel(ChunkBwdArgs a) {
       bz[tb] = *reinterpret_cast<const f32x4*>(sG + 2 * BT + perm_row(tb, 4 * g));
     }
     const float eGl = sG[3 * BT];
-    f32x4 Z[4];
-    Frag<C> Zf[2];
+#pragma unroll
+    for (int s = 0; s < KS; ++s) join(Sh[s], S[2 * s], S[2 * s + 1]);
+    if (back) {
+      // P^T dO first: it waits for nothing
+#pragma unroll
+      for (int p = 0; p < 2; ++p) dO[p] = TA::template col8<true>(sV, 32 * p + 8 * g, w, n);
+#pragma unroll
+      for (int tb = 0; tb < 4; ++tb) {
+        Z[tb] = mma(TA::template col8<false>(sP, 32 + 8 * g, tb, n), dO[1], zero4());
+        if (tb < 2) Z[tb] = mma(TA::template col8<false>(sP, 8 * g, tb, n), dO[0], Z[tb]);
+      }
+    }
+    // X = K S
+#pragma unroll
+    for (int tb = 0; tb < 4; ++tb) X[tb] = zero4();
+#pragma unroll
+    for (int s = 0; s < KS; ++s)
+#pragma unroll
+      for (int tb = 0; tb < 4; ++tb) X[tb] = mma(TK::row8(sK, perm_row(tb, n), 32 * s + 8 * g), Sh[s], X[tb]);
+#pragma unroll
+    for (int s = 0; s < KS; ++s) store8(st_out + slot * chunk_state + 32 * s + 8 * g, Sh[s]);
+#pragma unroll
+    for (int kb = 0; kb < KB; ++kb) S[kb] = S[kb] * eGl;
     if (!back) {
       // R = beta (v - e^G X), Vn = A R (block lower triangular in 32-token slabs)
 #pragma unroll
@@ -238,78 +289,58 @@ __global__ __launch_bounds__(256) void gdn_bwd_scan_kernel(ChunkBwdArgs a) {
         store8(col_out + slot * chunk_cols + 32 * p + 8 * g, Zf[p]);
         join(Zf[p], Z[2 * p] * ey[2 * p], Z[2 * p + 1] * ey[2 * p + 1]);
       }
-#pragma unroll
-      for (int kb = 0; kb < KB; ++kb) S[kb] = S[kb] * eGl;
     } else {
-      // Y = e^{G_last - G} X + P^T dO, dR = A^T Y
-      Frag<C> dO[2];
+      // dh' <- e^{G_last} dh' + Q^T (scale e^G dO), which waits for nothing either
 #pragma unroll
-      for (int p = 0; p < 2; ++p) dO[p] = TA::template col8<true>(sV, 32 * p + 8 * g, w, n);
-#pragma unroll
-      for (int tb = 0; tb < 4; ++tb) {
-        X[tb] = X[tb] * ey[tb];
-        if (tb < 2) X[tb] = mma(TA::template col8<false>(sP, 8 * g, tb, n), dO[0], X[tb]);
-        X[tb] = mma(TA::template col8<false>(sP, 32 + 8 * g, tb, n), dO[1], X[tb]);
+      for (int p = 0; p < 2; ++p) {   // slots 8 g + e are the tokens of blocks 2 p and 2 p + 1
+        const f32x8 x = values(dO[p]);
+        join(dO[p], f32x4{x[0], x[1], x[2], x[3]} * (ex[2 * p] * a.f.scale),
+             f32x4{x[4], x[5], x[6], x[7]} * (ex[2 * p + 1] * a.f.scale));
       }
+#pragma unroll
+      for (int kb = 0; kb < KB; ++kb) S[kb] = mma(TK::template col8<false>(sQ, 8 * g, kb, n), dO[0], S[kb]);
+      // Y = e^{G_last - G} X + P^T dO, dR = A^T Y
       Frag<C> Y0, Y1;
-      join(Y0, X[0], X[1]);
-      join(Y1, X[2], X[3]);
+      join(Y0, X[0] * ey[0] + Z[0], X[1] * ey[1] + Z[1]);
+      join(Y1, X[2] * ey[2] + Z[2], X[3] * ey[3] + Z[3]);
 #pragma unroll
       for (int tb = 0; tb < 4; ++tb) {
         Z[tb] = mma(TA::template col8<false>(sA, 32 + 8 * g, tb, n), Y1, zero4());
         if (tb < 2) Z[tb] = mma(TA::template col8<false>(sA, 8 * g, tb, n), Y0, Z[tb]);
       }
 #pragma unroll
+      for (int kb = 0; kb < KB; ++kb) S[kb] = mma(TK::template col8<false>(sQ, 32 + 8 * g, kb, n), dO[1], S[kb]);
+#pragma unroll
       for (int p = 0; p < 2; ++p) {
         join(Zf[p], Z[2 * p], Z[2 * p + 1]);
         store8(col_out + slot * chunk_cols + 32 * p + 8 * g, Zf[p]);
         join(Zf[p], Z[2 * p] * (-bz[2 * p] * ex[2 * p]), Z[2 * p + 1] * (-bz[2 * p + 1] * ex[2 * p + 1]));
       }
-      // dh' <- e^{G_last} dh' + Q^T (scale e^G dO)
-#pragma unroll
-      for (int p = 0; p < 2; ++p) {
-        f32x8 x = values(dO[p]);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {   // slots 8 g + e are the tokens of blocks 2 p and 2 p + 1
-          x[e] *= a.f.scale * ex[2 * p][e];
-          x[4 + e] *= a.f.scale * ex[2 * p + 1][e];
-        }
-        join(dO[p], f32x4{x[0], x[1], x[2], x[3]}, f32x4{x[4], x[5], x[6], x[7]});
-      }
-#pragma unroll
-      for (int kb = 0; kb < KB; ++kb) {
-        S[kb] = S[kb] * eGl;
-#pragma unroll
-        for (int p = 0; p < 2; ++p) S[kb] = mma(TK::template col8<false>(sQ, 32 * p + 8 * g, kb, n), dO[p], S[kb]);
-      }
     }
     // ... + K^T Z
 #pragma unroll
-    for (int kb = 0; kb < KB; ++kb)
+    for (int p = 0; p < 2; ++p)
 #pragma unroll
-      for (int p = 0; p < 2; ++p) S[kb] = mma(TK::template col8<false>(sK, 32 * p + 8 * g, kb, n), Zf[p], S[kb]);
+      for (int kb = 0; kb < KB; ++kb) S[kb] = mma(TK::template col8<false>(sK, 32 * p + 8 * g, kb, n), Zf[p], S[kb]);
+    tiles::lds_barrier();
   }
   if (back && a.dh0) {
     T* out = reinterpret_cast<T*>(a.dh0) + sbase;
 #pragma unroll
-    for (int s = 0; s < KS; ++s) {
-      store_io8(out + 32 * s + 8 * g, both(S[2 * s], S[2 * s + 1]) * inv);
-    }
+    for (int s = 0; s < KS; ++s) store_io8(out + 32 * s + 8 * g, both(S[2 * s], S[2 * s + 1]) * inv);
   }
 }
 
 // ---------------------------------------------------------- largest gradients
-// amax[n, j] = bits of max |dht| (0 without one): one work-group a (sequence, head).
-__global__ __launch_bounds__(256) void bwd_amax_init_kernel(const float* __restrict__ dht, int per,
-                                                            uint32_t* __restrict__ amax) {
+// amax_dht[n, j] = bits of max |dht|: one work-group a (sequence, head).
+__global__ __launch_bounds__(256) void bwd_amax_dht_kernel(const float* __restrict__ dht, int per,
+                                                           uint32_t* __restrict__ amax) {
   __shared__ uint32_t sm[4];
   uint32_t m = 0;
-  if (dht) {
-    const uint4* p = reinterpret_cast<const uint4*>(dht + (size_t)blockIdx.x * per);
-    for (int i = threadIdx.x; i < per / 4; i += 256) {
-      const uint4 x = p[i];
-      m = max(m, max(max(x.x & 0x7FFFFFFFu, x.y & 0x7FFFFFFFu), max(x.z & 0x7FFFFFFFu, x.w & 0x7FFFFFFFu)));
-    }
+  const uint4* p = reinterpret_cast<const uint4*>(dht + (size_t)blockIdx.x * per);
+  for (int i = threadIdx.x; i < per / 4; i += 256) {
+    const uint4 x = p[i];
+    m = max(m, max(max(x.x & 0x7FFFFFFFu, x.y & 0x7FFFFFFFu), max(x.z & 0x7FFFFFFFu, x.w & 0x7FFFFFFFu)));
   }
 #pragma unroll
   for (int off = 32; off > 0; off >>= 1) m = max(m, (uint32_t)__shfl_xor((int)m, off, 64));
@@ -318,50 +349,33 @@ __global__ __launch_bounds__(256) void bwd_amax_init_kernel(const float* __restr
   if (threadIdx.x == 0) amax[blockIdx.x] = max(max(sm[0], sm[1]), max(sm[2], sm[3]));
 }
 
-// max |dout| of 16 rows of a chunk into amax (the order does not change a maximum).
-// LPH lanes hold a head's channels of a row.
+// part[slot][quarter][head] = bits of max |dout| of 16 rows of a chunk.  LPH lanes hold a
+// head's channels of a row.
 template <int LPH>
-__global__ __launch_bounds__(256) void bwd_amax_kernel(const bf16_t* __restrict__ dout, uint32_t* __restrict__ amax,
-                                                       const int64_t* __restrict__ cu, const int32_t* __restrict__ coff,
-                                                       int T, int N, int NT, int HV, int cblocks) {
+__global__ __launch_bounds__(256) void bwd_amax_kernel(ChunkBwdArgs a, int cblocks) {
   const int cb = blockIdx.x % cblocks, part = blockIdx.x / cblocks % 4, slot = blockIdx.x / cblocks / 4;
-  // the chunk and its sequence
-  int ns, c0, nrow;
-  if (cu) {
-    if (slot >= coff[N]) return;
-    int lo = 0, hi = N;
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (coff[mid] <= slot) lo = mid; else hi = mid;
-    }
-    ns = lo;
-    long long b0 = cu[lo], b1 = cu[lo + 1];
-    b0 = b0 < 0 ? 0 : (b0 > T ? T : b0);
-    b1 = b1 < b0 ? b0 : (b1 > T ? T : b1);
-    c0 = (int)b0 + 64 * (slot - coff[lo]);
-    nrow = (int)b1 - c0 < 64 ? (int)b1 - c0 : 64;
-  } else {
-    ns = slot / NT;
-    const int it = slot - ns * NT;
-    c0 = ns * T + 64 * it;
-    nrow = T - 64 * it < 64 ? T - 64 * it : 64;
-  }
+  int c0, nrow;
+  if (!intra::locate_chunk(slot, a.f.cu_seqlens, a.f.chunk_off, a.f.N, a.f.T, (a.f.T + BT - 1) / BT, c0, nrow)) return;
   const int ch = (cb * 256 + threadIdx.x) * 8;
-  const int C = HV * LPH * 8;
+  const int HV = a.f.HV, C = HV * LPH * 8;
   if (ch >= C) return;   // whole heads
-  const int r1 = nrow < 16 * part + 16 ? nrow : 16 * part + 16;
   uint32_t m = 0;
-  const bf16_t* p = dout + (size_t)c0 * C + ch;
-#pragma unroll 4
-  for (int r = 16 * part; r < r1; ++r) {
-    const uint4 x = *reinterpret_cast<const uint4*>(p + (size_t)r * C);
-    const uint32_t ws[4] = {x.x, x.y, x.z, x.w};
+  const bf16_t* p = reinterpret_cast<const bf16_t*>(a.dout) + (size_t)c0 * C + ch;
+  uint4 x[16];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) m = max(m, max((ws[i] << 16) & 0x7FFFFFFFu, ws[i] & 0x7FFF0000u));
+  for (int i = 0; i < 16; ++i) {   // rows behind the end: the last one again
+    const int r = 16 * part + i < nrow ? 16 * part + i : nrow - 1;
+    x[i] = *reinterpret_cast<const uint4*>(p + (size_t)r * C);
+  }
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    const uint32_t ws[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) m = max(m, max((ws[e] << 16) & 0x7FFFFFFFu, ws[e] & 0x7FFF0000u));
   }
 #pragma unroll
   for (int off = 1; off < LPH; off <<= 1) m = max(m, (uint32_t)__shfl_xor((int)m, off, 64));
-  if (threadIdx.x % LPH == 0 && m) atomicMax(amax + (size_t)ns * HV + ch / (8 * LPH), m);
+  if (threadIdx.x % LPH == 0) a.part[((size_t)slot * 4 + part) * HV + ch / (8 * LPH)] = m;
 }
 
 template <typename T, int D>
@@ -370,9 +384,10 @@ hipError_t launch_scan(const ChunkBwdArgs& a, hipStream_t s) {
   const long long units = ((long long)a.f.N * a.f.Hk + 7) / 8 * 8;
   const unsigned grid = (unsigned)(units * (a.f.HV / a.f.Hk) * (D / 64) * 2);
   const void* kern = reinterpret_cast<const void*>(gdn_bwd_scan_kernel<T, D>);
-  if (L::bytes > 65536)
-    if (hipError_t e = hipFuncSetAttribute(kern, hipFuncAttributeMaxDynamicSharedMemorySize, L::bytes)) return e;
-  hipLaunchKernelGGL((gdn_bwd_scan_kernel<T, D>), dim3(grid), dim3(256), L::bytes, s, a);
+  const int bytes = L::stages * L::bytes;
+  if (bytes > 65536)
+    if (hipError_t e = hipFuncSetAttribute(kern, hipFuncAttributeMaxDynamicSharedMemorySize, bytes)) return e;
+  hipLaunchKernelGGL((gdn_bwd_scan_kernel<T, D>), dim3(grid), dim3(512), bytes, s, a);
   return hipGetLastError();
 }
 
@@ -380,14 +395,15 @@ hipError_t launch_scan(const ChunkBwdArgs& a, hipStream_t s) {
 
 hipError_t launch_chunk_bwd_amax(const ChunkBwdArgs& a, hipStream_t s) {
   const ChunkArgs& f = a.f;
-  hipLaunchKernelGGL(bwd_amax_init_kernel, dim3((unsigned)(f.N * f.HV)), dim3(256), 0, s, a.dht, f.V * f.K, a.amax);
-  if (hipError_t e = hipGetLastError()) return e;
+  if (a.dht) {
+    hipLaunchKernelGGL(bwd_amax_dht_kernel, dim3((unsigned)(f.N * f.HV)), dim3(256), 0, s, a.dht, f.V * f.K, a.amax_dht);
+    if (hipError_t e = hipGetLastError()) return e;
+  }
   if ((long long)f.B * f.T == 0) return hipSuccess;
-  const int cblocks = (f.HV * f.V / 8 + 255) / 256, NT = (f.T + 63) / 64;
+  const int cblocks = (f.HV * f.V / 8 + 255) / 256;
   const dim3 grid((unsigned)((long long)a.nslots * 4 * cblocks));
-  auto kern = f.V == 128 ? bwd_amax_kernel<16> : bwd_amax_kernel<8>;
-  hipLaunchKernelGGL(kern, grid, dim3(256), 0, s, (const bf16_t*)a.dout, a.amax, f.cu_seqlens, f.chunk_off, f.T, f.N, NT,
-                     f.HV, cblocks);
+  if (f.V == 128) hipLaunchKernelGGL((bwd_amax_kernel<16>), grid, dim3(256), 0, s, a, cblocks);
+  else hipLaunchKernelGGL((bwd_amax_kernel<8>), grid, dim3(256), 0, s, a, cblocks);
   return hipGetLastError();
 }
 

@@ -312,7 +312,7 @@ hipError_t launch_chunk_bwd(const ChunkBwdArgs& b, hipStream_t s) {
 // Workspace of the gradients: the prefill's, then what passes between the launches.
 struct BwdWorkspace {
   ChunkWorkspace f;
-  size_t amax, hs, ds, vn, dr, total;
+  size_t amax, amax_dht, part, hs, ds, vn, dr, total;
   int nslots;
 };
 static BwdWorkspace bwd_workspace_layout(int B, int T, int HV, int K, int V, int N, bool varlen, bool bf16) {
@@ -322,7 +322,9 @@ static BwdWorkspace bwd_workspace_layout(int B, int T, int HV, int K, int V, int
   w.f = chunk_workspace_layout((long long)B * T, HV, K, N, NT * B + N, eb, false);
   const size_t cells = (size_t)w.nslots * HV;
   w.amax = w.f.total;
-  w.hs = w.amax + up((size_t)N * HV * 4);
+  w.amax_dht = w.amax + up((size_t)N * HV * 4);
+  w.part = w.amax_dht + up((size_t)N * HV * 4);
+  w.hs = w.part + up(cells * 16);
   w.ds = w.hs + up(cells * K * V * eb);
   w.vn = w.ds + up(cells * K * V * eb);
   w.dr = w.vn + up(cells * V * 64 * eb);
@@ -455,6 +457,7 @@ int gdn_chunk_bwd(const void* q, const void* k, const void* v, const float* g, c
   f.seq_order = cu_seqlens ? (int32_t*)(ws + L.f.order_off) : nullptr;
   a.dout = dout; a.dht = dht; a.dq = dq; a.dk = dk; a.dv = dv; a.dg = dg; a.dbeta = dbeta; a.dh0 = dh0;
   a.amax = bf16 ? (uint32_t*)(ws + L.amax) : nullptr;
+  a.amax_dht = (uint32_t*)(ws + L.amax_dht); a.part = (uint32_t*)(ws + L.part);
   a.hs = ws + L.hs; a.ds = ws + L.ds; a.vn = ws + L.vn; a.dr = ws + L.dr;
   a.nslots = L.nslots;
   const hipError_t e = launch_chunk_bwd(a, (hipStream_t)stream);
