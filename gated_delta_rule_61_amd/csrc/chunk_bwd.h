@@ -100,9 +100,14 @@ __device__ __forceinline__ void store_io8(float* p, const f32x8& x) {
 // An LDS tile of rows of COLS elements.  16-bit: 16-byte units swizzled by row as
 // in the prefill's scan (row fragments and transposing reads without bank
 // conflicts).  fp32: rows padded by 16 bytes.
+//
+// A lane's fragments lie at one offset each for a set of them (rows(), cols()) plus
+// constants: the swizzle of a row does not change with the 4 and 32 rows that
+// separate them.
 template <typename C, int COLS> struct Tile;
 template <int COLS> struct Tile<f16_t, COLS> {
   static constexpr int pitch = 2 * COLS;
+  static constexpr int odd = 8;   // from block 2 m of a permuted pair to block 2 m + 1
   static constexpr int bytes(int rows) { return rows * pitch; }
   static __device__ __forceinline__ int off(int row, int col) {   // byte of an element; col a multiple of 4
     int u;
@@ -118,19 +123,21 @@ template <int COLS> struct Tile<f16_t, COLS> {
     typedef _Float16 f16x4 __attribute__((ext_vector_type(4)));
     *reinterpret_cast<f16x4*>(t + off(row, col)) = __builtin_convertvector(x, f16x4);
   }
-  // row `row`, columns col .. col + 7
-  static __device__ __forceinline__ Frag<f16_t> row8(const char* t, int row, int col) {
+  static __device__ __forceinline__ Frag<f16_t> row(const char* t) {   // 8 values of a row
     Frag<f16_t> f;
-    f.v = *reinterpret_cast<const f16x8*>(t + off(row, col));
+    f.v = *reinterpret_cast<const f16x8*>(t);
     return f;
   }
-  // rows r0 .. r0 + 7 of the lane's column: column n of the block's 16 (NATURAL:
-  // col0 + n; else the permuted order of block col0 / 16 of a pair)
-  template <bool NATURAL>
-  static __device__ __forceinline__ Frag<f16_t> col8(const char* t, int r0, int blk, int n) {
-    const int c = NATURAL ? 16 * blk + 4 * (n & 3) : perm_row(blk, 4 * (n & 3));
-    const int r = r0 + (n >> 2);
-    const uint2 lo = tiles::ld_tr(t + off(r, c)), hi = tiles::ld_tr(t + off(r + 4, c));
+  static __device__ __forceinline__ Frag<f16_t> row8(const char* t, int r, int col) { return row(t + off(r, col)); }
+  // offset of rows 8 g .. 8 g + 7 of the lane's column: column 32 pair + perm_row(0, n), or 16 blk + n
+  static __device__ __forceinline__ int pair_cols(int pair, int n, int g) {
+    return off(8 * g + (n >> 2), 32 * pair + 8 * (n & 3));
+  }
+  static __device__ __forceinline__ int block_cols(int blk, int n, int g) {
+    return off(8 * g + (n >> 2), 16 * blk + 4 * (n & 3));
+  }
+  static __device__ __forceinline__ Frag<f16_t> col(const char* t) {   // 8 values of a column, by transposing reads
+    const uint2 lo = tiles::ld_tr(t), hi = tiles::ld_tr(t + 4 * pitch);
     Frag<f16_t> f;
     f.v = __builtin_bit_cast(f16x8, tiles::u32x4{lo.x, lo.y, hi.x, hi.y});
     return f;
@@ -138,6 +145,7 @@ template <int COLS> struct Tile<f16_t, COLS> {
 };
 template <int COLS> struct Tile<float, COLS> {
   static constexpr int pitch = 4 * COLS + 16;
+  static constexpr int odd = 16;
   static constexpr int bytes(int rows) { return rows * pitch; }
   static __device__ __forceinline__ int off(int row, int col) { return row * pitch + 4 * col; }
   static __device__ __forceinline__ void put(char* t, int row, int col, const Frag<float>& f) {
@@ -148,17 +156,19 @@ template <int COLS> struct Tile<float, COLS> {
   static __device__ __forceinline__ void put4(char* t, int row, int col, const f32x4& x) {
     *reinterpret_cast<f32x4*>(t + off(row, col)) = x;
   }
-  static __device__ __forceinline__ Frag<float> row8(const char* t, int row, int col) {
+  static __device__ __forceinline__ Frag<float> row(const char* t) {
+    const f32x4 a = *reinterpret_cast<const f32x4*>(t), b = *reinterpret_cast<const f32x4*>(t + 16);
     Frag<float> f;
-    load8(f, reinterpret_cast<const float*>(t + off(row, col)));
+    f.v = both(a, b);
     return f;
   }
-  template <bool NATURAL>
-  static __device__ __forceinline__ Frag<float> col8(const char* t, int r0, int blk, int n) {
-    const int c = NATURAL ? 16 * blk + n : perm_row(blk, n);
+  static __device__ __forceinline__ Frag<float> row8(const char* t, int r, int col) { return row(t + off(r, col)); }
+  static __device__ __forceinline__ int pair_cols(int pair, int n, int g) { return off(8 * g, 32 * pair + perm_row(0, n)); }
+  static __device__ __forceinline__ int block_cols(int blk, int n, int g) { return off(8 * g, 16 * blk + n); }
+  static __device__ __forceinline__ Frag<float> col(const char* t) {
     Frag<float> f;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) f.v[e] = *reinterpret_cast<const float*>(t + off(r0 + e, c));
+    for (int e = 0; e < 8; ++e) f.v[e] = *reinterpret_cast<const float*>(t + e * pitch);
     return f;
   }
 };

@@ -174,15 +174,15 @@ __global__ __launch_bounds__(256) void gdn_bwd_grad_kernel(ChunkBwdArgs a) {
         Frag<C> hf[2], df[2];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          hf[h] = TD::template col8<false>(lds + L::H, r0, 2 * kw + h, n);
-          df[h] = TD::template col8<false>(lds + L::DS, r0, 2 * kw + h, n);
+          hf[h] = TD::col(lds + L::H + TD::pair_cols(kw, n, g) + 32 * s * TD::pitch + h * TD::odd);
+          df[h] = TD::col(lds + L::DS + TD::pair_cols(kw, n, g) + 32 * s * TD::pitch + h * TD::odd);
         }
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
           const int tb = tb0 + t;
           const Frag<C> of = T64::row8(lds + L::O, 16 * tb + n, r0);
-          const Frag<C> rf = T64::template col8<true>(lds + L::DR, r0, tb, n);
-          const Frag<C> vf = T64::template col8<true>(lds + L::VN, r0, tb, n);
+          const Frag<C> rf = T64::col(lds + L::DR + T64::block_cols(tb, n, g) + 32 * s * T64::pitch);
+          const Frag<C> vf = T64::col(lds + L::VN + T64::block_cols(tb, n, g) + 32 * s * T64::pitch);
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             dq[h][t] = mma(hf[h], of, dq[h][t]);
@@ -197,15 +197,15 @@ __global__ __launch_bounds__(256) void gdn_bwd_grad_kernel(ChunkBwdArgs a) {
           const int b = w + 4 * i;
           const int m = b >= 10 ? b - 10 : b;
           const int tb = m >= 6 ? 3 : m >= 3 ? 2 : m >= 1 ? 1 : 0, sb = m - tb * (tb + 1) / 2;
-          const Frag<C> vf = T64::template col8<true>(lds + L::VN, r0, sb, n);
-          const Frag<C> xf = b >= 10 ? T64::template col8<true>(lds + L::DR, r0, tb, n)
+          const Frag<C> vf = T64::col(lds + L::VN + T64::block_cols(sb, n, g) + 32 * s * T64::pitch);
+          const Frag<C> xf = b >= 10 ? T64::col(lds + L::DR + T64::block_cols(tb, n, g) + 32 * s * T64::pitch)
                                      : T64::row8(lds + L::O, 16 * tb + n, r0);
           M[i] = mma(vf, xf, M[i]);
         }
         // dv of token 16 w + n, and v . dR
         const int t = 16 * w + n;
         if (t < nrow) {
-          const f32x8 x = values(T64::template col8<true>(lds + L::DR, r0, w, n));
+          const f32x8 x = values(T64::col(lds + L::DR + T64::block_cols(w, n, g) + 32 * s * T64::pitch));
           const size_t at = (size_t)t * vstride + 64 * vb + r0;
           Frag<T> vv;
           load8(vv, vp + at);
@@ -292,8 +292,8 @@ __global__ __launch_bounds__(256) void gdn_bwd_grad_kernel(ChunkBwdArgs a) {
       Frag<C> ka[2], qa[2];
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        ka[h] = TD::template col8<false>(sK, r0, 2 * kw + h, n);
-        qa[h] = TD::template col8<false>(sQ, r0, 2 * kw + h, n);
+        ka[h] = TD::col(sK + TD::pair_cols(kw, n, g) + 32 * p * TD::pitch + h * TD::odd);
+        qa[h] = TD::col(sQ + TD::pair_cols(kw, n, g) + 32 * p * TD::pitch + h * TD::odd);
       }
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
@@ -307,7 +307,7 @@ __global__ __launch_bounds__(256) void gdn_bwd_grad_kernel(ChunkBwdArgs a) {
           }
         }
         if (2 * p + 1 >= tb) {   // t of the slab from s = 16 tb + n on
-          const Frag<C> s1 = T64::template col8<true>(S1, r0, tb, n), s3 = T64::template col8<true>(S3, r0, tb, n);
+          const Frag<C> s1 = T64::col(S1 + T64::block_cols(tb, n, g) + 32 * p * T64::pitch), s3 = T64::col(S3 + T64::block_cols(tb, n, g) + 32 * p * T64::pitch);
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             W[h][t] = mma(qa[h], s1, W[h][t]);

@@ -227,103 +227,177 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
   C* const st_out = reinterpret_cast<C*>(back ? a.ds : a.hs) + ((size_t)j * D + vrow) * D;
   C* const col_out = reinterpret_cast<C*>(back ? a.dr : a.vn) + ((size_t)j * D + vrow) * BT;
 
-  if constexpr (TWO) tiles::lds_barrier();
-  for (int i = 0; i < NC; ++i) {
-    const size_t slot = (size_t)(slot0 + chunk_of(i));
-    const char* const st = lds + (TWO ? (i & 1) * L::bytes : 0);
-    const char* const sK = st + L::K;
-    const char* const sA = st + L::A;
-    const char* const sV = st + L::V;
-    const float* const sG = reinterpret_cast<const float*>(st + L::G);
-    const char* const sQ = st + L::Q;
-    const char* const sP = st + L::P;
-    if constexpr (!TWO) tiles::lds_barrier();
-
-    // lane: tokens perm_row(tb, 4 g + i), column n
-    f32x4 X[4], Z[4], ex[4], ey[4], bz[4];
-    Frag<C> Sh[KS], Zf[2], dO[2];
+  // Keeps the order of what is issued around it: left to itself the compiler reads each
+  // fragment right before its product and waits out the LDS latency every time.  (fp32
+  // fragments are twice as large and do not fit that way.)
+  auto fence = [&]() __attribute__((always_inline)) {
+    if constexpr (sizeof(C) == 2) __builtin_amdgcn_sched_barrier(0);
+  };
+  // offsets of the lane's fragments in a stage
+  int o_row[KS], o_k[KS];   // K (Q) rows of slab s, columns of block pair m
 #pragma unroll
-    for (int tb = 0; tb < 4; ++tb) {
-      ex[tb] = *reinterpret_cast<const f32x4*>(sG + perm_row(tb, 4 * g));
-      ey[tb] = *reinterpret_cast<const f32x4*>(sG + BT + perm_row(tb, 4 * g));
-      bz[tb] = *reinterpret_cast<const f32x4*>(sG + 2 * BT + perm_row(tb, 4 * g));
-    }
-    const float eGl = sG[3 * BT];
-#pragma unroll
-    for (int s = 0; s < KS; ++s) join(Sh[s], S[2 * s], S[2 * s + 1]);
-    if (back) {
-      // P^T dO first: it waits for nothing
-#pragma unroll
-      for (int p = 0; p < 2; ++p) dO[p] = TA::template col8<true>(sV, 32 * p + 8 * g, w, n);
-#pragma unroll
-      for (int tb = 0; tb < 4; ++tb) {
-        Z[tb] = mma(TA::template col8<false>(sP, 32 + 8 * g, tb, n), dO[1], zero4());
-        if (tb < 2) Z[tb] = mma(TA::template col8<false>(sP, 8 * g, tb, n), dO[0], Z[tb]);
-      }
-    }
-    // X = K S
-#pragma unroll
-    for (int tb = 0; tb < 4; ++tb) X[tb] = zero4();
-#pragma unroll
-    for (int s = 0; s < KS; ++s)
-#pragma unroll
-      for (int tb = 0; tb < 4; ++tb) X[tb] = mma(TK::row8(sK, perm_row(tb, n), 32 * s + 8 * g), Sh[s], X[tb]);
-#pragma unroll
-    for (int s = 0; s < KS; ++s) store8(st_out + slot * chunk_state + 32 * s + 8 * g, Sh[s]);
-#pragma unroll
-    for (int kb = 0; kb < KB; ++kb) S[kb] = S[kb] * eGl;
-    if (!back) {
-      // R = beta (v - e^G X), Vn = A R (block lower triangular in 32-token slabs)
-#pragma unroll
-      for (int tb = 0; tb < 4; ++tb) X[tb] = bz[tb] * (VTile<T>::get(sV, tb, w, n, g) - ex[tb] * X[tb]);
-      Frag<C> R0, R1;
-      join(R0, X[0], X[1]);
-      join(R1, X[2], X[3]);
-#pragma unroll
-      for (int tb = 0; tb < 4; ++tb) Z[tb] = mma(TA::row8(sA, perm_row(tb, n), 8 * g), R0, zero4());
-#pragma unroll
-      for (int tb = 2; tb < 4; ++tb) Z[tb] = mma(TA::row8(sA, perm_row(tb, n), 32 + 8 * g), R1, Z[tb]);
-#pragma unroll
-      for (int p = 0; p < 2; ++p) {
-        join(Zf[p], Z[2 * p], Z[2 * p + 1]);
-        store8(col_out + slot * chunk_cols + 32 * p + 8 * g, Zf[p]);
-        join(Zf[p], Z[2 * p] * ey[2 * p], Z[2 * p + 1] * ey[2 * p + 1]);
-      }
-    } else {
-      // dh' <- e^{G_last} dh' + Q^T (scale e^G dO), which waits for nothing either
-#pragma unroll
-      for (int p = 0; p < 2; ++p) {   // slots 8 g + e are the tokens of blocks 2 p and 2 p + 1
-        const f32x8 x = values(dO[p]);
-        join(dO[p], f32x4{x[0], x[1], x[2], x[3]} * (ex[2 * p] * a.f.scale),
-             f32x4{x[4], x[5], x[6], x[7]} * (ex[2 * p + 1] * a.f.scale));
-      }
-#pragma unroll
-      for (int kb = 0; kb < KB; ++kb) S[kb] = mma(TK::template col8<false>(sQ, 8 * g, kb, n), dO[0], S[kb]);
-      // Y = e^{G_last - G} X + P^T dO, dR = A^T Y
-      Frag<C> Y0, Y1;
-      join(Y0, X[0] * ey[0] + Z[0], X[1] * ey[1] + Z[1]);
-      join(Y1, X[2] * ey[2] + Z[2], X[3] * ey[3] + Z[3]);
-#pragma unroll
-      for (int tb = 0; tb < 4; ++tb) {
-        Z[tb] = mma(TA::template col8<false>(sA, 32 + 8 * g, tb, n), Y1, zero4());
-        if (tb < 2) Z[tb] = mma(TA::template col8<false>(sA, 8 * g, tb, n), Y0, Z[tb]);
-      }
-#pragma unroll
-      for (int kb = 0; kb < KB; ++kb) S[kb] = mma(TK::template col8<false>(sQ, 32 + 8 * g, kb, n), dO[1], S[kb]);
-#pragma unroll
-      for (int p = 0; p < 2; ++p) {
-        join(Zf[p], Z[2 * p], Z[2 * p + 1]);
-        store8(col_out + slot * chunk_cols + 32 * p + 8 * g, Zf[p]);
-        join(Zf[p], Z[2 * p] * (-bz[2 * p] * ex[2 * p]), Z[2 * p + 1] * (-bz[2 * p + 1] * ex[2 * p + 1]));
-      }
-    }
-    // ... + K^T Z
-#pragma unroll
-    for (int p = 0; p < 2; ++p)
-#pragma unroll
-      for (int kb = 0; kb < KB; ++kb) S[kb] = mma(TK::template col8<false>(sK, 32 * p + 8 * g, kb, n), Zf[p], S[kb]);
-    tiles::lds_barrier();
+  for (int s = 0; s < KS; ++s) {
+    o_row[s] = TK::off(perm_row(0, n), 32 * s + 8 * g);
+    o_k[s] = TK::pair_cols(s, n, g);
   }
+  const int o_a[2] = {TA::off(perm_row(0, n), 8 * g), TA::off(perm_row(0, n), 32 + 8 * g)};
+  const int o_at[2] = {TA::pair_cols(0, n, g), TA::pair_cols(1, n, g)};
+  const int o_do = TA::block_cols(w, n, g);
+  // K^T (Q^T): channels of block kb, tokens 32 p + 8 g + [0, 8); A^T, P^T alike; rows of A
+  auto kt = [&](const char* t, int kb, int p) __attribute__((always_inline)) {
+    return TK::col(t + o_k[kb / 2] + 32 * p * TK::pitch + (kb & 1) * TK::odd);
+  };
+  auto at = [&](const char* t, int tb, int p) __attribute__((always_inline)) {
+    return TA::col(t + o_at[tb / 2] + 32 * p * TA::pitch + (tb & 1) * TA::odd);
+  };
+  auto ar = [&](const char* t, int tb, int p) __attribute__((always_inline)) {
+    return TA::row(t + o_a[p] + tiles::blk_rows(tb) * TA::pitch);
+  };
+  if constexpr (TWO) tiles::lds_barrier();
+  auto walk = [&](auto direction) __attribute__((always_inline)) {
+    constexpr bool BACK = decltype(direction)::value;
+    for (int i = 0; i < NC; ++i) {
+      const size_t slot = (size_t)(slot0 + chunk_of(i));
+      const char* const st = lds + (TWO ? (i & 1) * L::bytes : 0);
+      const char* const sK = st + L::K;
+      const char* const sA = st + L::A;
+      const char* const sV = st + L::V;
+      const float* const sG = reinterpret_cast<const float*>(st + L::G);
+      const char* const sQ = st + L::Q;
+      const char* const sP = st + L::P;
+      if constexpr (!TWO) tiles::lds_barrier();
+
+      // lane: tokens perm_row(tb, 4 g + i), column n
+      f32x4 X[4], Z[4], ex[4], ey[4], bz[4], v[4];
+      Frag<C> Kr[KS][4], Ar[6], Pt[6], Sh[KS], Zf[2], dO[2], Q0[KB], Q1[KB], K0[KB], K1[KB];
+      // ---- what the first products need
+      auto gates = [&](f32x4 (&x)[4], int plane) __attribute__((always_inline)) {
+#pragma unroll
+        for (int tb = 0; tb < 4; ++tb) x[tb] = *reinterpret_cast<const f32x4*>(sG + plane * BT + perm_row(tb, 4 * g));
+      };
+      const float eGl = sG[3 * BT];
+      if constexpr (BACK) {
+#pragma unroll
+        for (int p = 0; p < 2; ++p) dO[p] = TA::col(sV + o_do + 32 * p * TA::pitch);
+#pragma unroll
+        for (int tb = 0; tb < 4; ++tb) Pt[tb] = at(sP, tb, 1);
+#pragma unroll
+        for (int tb = 0; tb < 2; ++tb) Pt[4 + tb] = at(sP, tb, 0);
+      } else {
+#pragma unroll
+        for (int tb = 0; tb < 4; ++tb) v[tb] = VTile<T>::get(sV, tb, w, n, g);
+      }
+      auto k_rows = [&](int s) __attribute__((always_inline)) {
+#pragma unroll
+        for (int tb = 0; tb < 4; ++tb) Kr[s][tb] = TK::row(sK + o_row[s] + tiles::blk_rows(tb) * TK::pitch);
+      };
+#pragma unroll
+      for (int s = 0; s < KS / 2; ++s) k_rows(s);
+#pragma unroll
+      for (int s = 0; s < KS; ++s) {
+        join(Sh[s], S[2 * s], S[2 * s + 1]);
+        store8(st_out + slot * chunk_state + 32 * s + 8 * g, Sh[s]);
+      }
+      fence();
+      // ---- P^T dO and X = K S; meanwhile the rows of A (A^T), then Q^T or K^T
+      if constexpr (BACK) {
+#pragma unroll
+        for (int tb = 0; tb < 4; ++tb) Z[tb] = mma(Pt[tb], dO[1], zero4());
+#pragma unroll
+        for (int tb = 0; tb < 2; ++tb) Z[tb] = mma(Pt[4 + tb], dO[0], Z[tb]);
+      }
+#pragma unroll
+      for (int tb = 0; tb < 4; ++tb) X[tb] = zero4();
+#pragma unroll
+      for (int s = 0; s < KS; ++s) {
+#pragma unroll
+        for (int tb = 0; tb < 4; ++tb) X[tb] = mma(Kr[s][tb], Sh[s], X[tb]);
+        if (s < KS / 2) k_rows(s + KS / 2);
+        if (s == KS / 2 - 1) {
+#pragma unroll
+          for (int tb = 0; tb < 4; ++tb) Ar[tb] = BACK ? at(sA, tb, 1) : ar(sA, tb, 0);
+#pragma unroll
+          for (int tb = 0; tb < 2; ++tb) Ar[4 + tb] = BACK ? at(sA, tb, 0) : ar(sA, 2 + tb, 1);
+        }
+        if (s == KS - 1) {
+          gates(ex, 0);
+          if constexpr (BACK) gates(ey, 1);
+          else gates(bz, 2);
+#pragma unroll
+          for (int kb = 0; kb < KB; ++kb) (BACK ? Q0 : K0)[kb] = kt(BACK ? sQ : sK, kb, 0);
+        }
+        fence();
+      }
+#pragma unroll
+      for (int kb = 0; kb < KB; ++kb) S[kb] = S[kb] * eGl;
+      if constexpr (!BACK) {
+        // R = beta (v - e^G X), Vn = A R (block lower triangular in 32-token slabs)
+#pragma unroll
+        for (int tb = 0; tb < 4; ++tb) X[tb] = bz[tb] * (v[tb] - ex[tb] * X[tb]);
+        Frag<C> R0, R1;
+        join(R0, X[0], X[1]);
+        join(R1, X[2], X[3]);
+#pragma unroll
+        for (int tb = 0; tb < 4; ++tb) Z[tb] = mma(Ar[tb], R0, zero4());
+#pragma unroll
+        for (int tb = 2; tb < 4; ++tb) Z[tb] = mma(Ar[2 + tb], R1, Z[tb]);
+#pragma unroll
+        for (int kb = 0; kb < KB; ++kb) K1[kb] = kt(sK, kb, 1);
+        gates(ey, 1);
+        fence();
+#pragma unroll
+        for (int p = 0; p < 2; ++p) {
+          join(Zf[p], Z[2 * p], Z[2 * p + 1]);
+          store8(col_out + slot * chunk_cols + 32 * p + 8 * g, Zf[p]);
+          join(Zf[p], Z[2 * p] * ey[2 * p], Z[2 * p + 1] * ey[2 * p + 1]);
+        }
+      } else {
+        // dh' <- e^{G_last} dh' + Q^T (scale e^G dO), which waits for nothing; Y =
+        // e^{G_last - G} X + P^T dO, dR = A^T Y
+#pragma unroll
+        for (int p = 0; p < 2; ++p) {   // slots 8 g + e are the tokens of blocks 2 p and 2 p + 1
+          const f32x8 x = values(dO[p]);
+          join(dO[p], f32x4{x[0], x[1], x[2], x[3]} * (ex[2 * p] * a.f.scale),
+               f32x4{x[4], x[5], x[6], x[7]} * (ex[2 * p + 1] * a.f.scale));
+        }
+#pragma unroll
+        for (int kb = 0; kb < KB; ++kb) Q1[kb] = kt(sQ, kb, 1);
+        fence();
+#pragma unroll
+        for (int kb = 0; kb < KB; ++kb) S[kb] = mma(Q0[kb], dO[0], S[kb]);
+        Frag<C> Y0, Y1;
+        join(Y0, X[0] * ey[0] + Z[0], X[1] * ey[1] + Z[1]);
+        join(Y1, X[2] * ey[2] + Z[2], X[3] * ey[3] + Z[3]);
+#pragma unroll
+        for (int kb = 0; kb < KB; ++kb) K0[kb] = kt(sK, kb, 0);
+        gates(bz, 2);
+        fence();
+#pragma unroll
+        for (int tb = 0; tb < 4; ++tb) Z[tb] = mma(Ar[tb], Y1, zero4());
+#pragma unroll
+        for (int tb = 0; tb < 2; ++tb) Z[tb] = mma(Ar[4 + tb], Y0, Z[tb]);
+#pragma unroll
+        for (int kb = 0; kb < KB; ++kb) S[kb] = mma(Q1[kb], dO[1], S[kb]);
+#pragma unroll
+        for (int kb = 0; kb < KB; ++kb) K1[kb] = kt(sK, kb, 1);
+        fence();
+#pragma unroll
+        for (int p = 0; p < 2; ++p) {
+          join(Zf[p], Z[2 * p], Z[2 * p + 1]);
+          store8(col_out + slot * chunk_cols + 32 * p + 8 * g, Zf[p]);
+          join(Zf[p], Z[2 * p] * (-bz[2 * p] * ex[2 * p]), Z[2 * p + 1] * (-bz[2 * p + 1] * ex[2 * p + 1]));
+        }
+      }
+      // ... + K^T Z
+#pragma unroll
+      for (int kb = 0; kb < KB; ++kb) S[kb] = mma(K0[kb], Zf[0], S[kb]);
+#pragma unroll
+      for (int kb = 0; kb < KB; ++kb) S[kb] = mma(K1[kb], Zf[1], S[kb]);
+      tiles::lds_barrier();
+    }
+  };
+  if (back) walk(tiles::Stage1{});
+  else walk(tiles::Stage0{});
   if (back && a.dh0) {
     T* out = reinterpret_cast<T*>(a.dh0) + sbase;
 #pragma unroll
