@@ -50,6 +50,14 @@ __device__ __forceinline__ f32x8 both(const f32x4& a, const f32x4& b) {
   return f32x8{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
 }
 
+// Hides where a value comes from: offsets made from it are made where they are used, a
+// cheap operation each, instead of once in front of all loops, which takes more registers
+// than there are.
+__device__ __forceinline__ int opaque(int x) {
+  asm volatile("" : "+v"(x));
+  return x;
+}
+
 // Two accumulators as one operand fragment.  fp16 without saturation: a value past
 // 65504 becomes an infinity, which shows in the result.
 __device__ __forceinline__ void join(Frag<f16_t>& f, const f32x4& a, const f32x4& b) {
@@ -136,6 +144,11 @@ template <int COLS> struct Tile<f16_t, COLS> {
   static __device__ __forceinline__ int block_cols(int blk, int n, int g) {
     return off(8 * g + (n >> 2), 16 * blk + 4 * (n & 3));
   }
+  // from the offset of block 0 to that of block b of the columns, of 16 rows b and 32-column slab s (of 64 columns)
+  static __device__ __forceinline__ int to_block(int o, int b) { return o ^ (b << 5); }
+  static __device__ __forceinline__ int to_rows(int o, int b, int s = 0) {
+    return (o ^ (((b & 1) << 5) | (s << 6))) + b * 16 * pitch;
+  }
   static __device__ __forceinline__ Frag<f16_t> col(const char* t) {   // 8 values of a column, by transposing reads
     const uint2 lo = tiles::ld_tr(t), hi = tiles::ld_tr(t + 4 * pitch);
     Frag<f16_t> f;
@@ -165,6 +178,8 @@ template <int COLS> struct Tile<float, COLS> {
   static __device__ __forceinline__ Frag<float> row8(const char* t, int r, int col) { return row(t + off(r, col)); }
   static __device__ __forceinline__ int pair_cols(int pair, int n, int g) { return off(8 * g, 32 * pair + perm_row(0, n)); }
   static __device__ __forceinline__ int block_cols(int blk, int n, int g) { return off(8 * g, 16 * blk + n); }
+  static __device__ __forceinline__ int to_block(int o, int b) { return o + 64 * b; }
+  static __device__ __forceinline__ int to_rows(int o, int b, int s = 0) { return o + b * 16 * pitch + 128 * s; }
   static __device__ __forceinline__ Frag<float> col(const char* t) {
     Frag<float> f;
 #pragma unroll

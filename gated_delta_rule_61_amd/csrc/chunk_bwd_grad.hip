@@ -6,12 +6,12 @@
 // head in turn and adds their dq and dk in registers, in order.  Products run
 // transposed ([K channels] x [tokens]), so that a lane ends with 8 consecutive
 // channels of a token: 16-byte stores, and the dot products with q and k (which
-// make dg and dbeta) in registers.  Each wave has 32 channels (K = 64: and half
-// the tokens); reductions over V go in blocks of 64 columns, whose tiles (dO, Vn,
-// dR, h, dh') pass through LDS once, the next block's in flight in registers.  The
-// scores dO Vn^T and dR Vn^T are dealt out to the waves in 16 x 16 blocks, gated
-// and masked there and shared through LDS, in the bytes of the tiles that are no
-// longer needed.
+// make dg and dbeta) in registers.  Each of the eight waves has 32 channels of some
+// token blocks; reductions over V go in blocks of 32 columns, whose tiles (Vn, dR,
+// h, dh' straight to LDS, dO through registers, scaled on its way) fill one half of
+// a double buffer while the other is used: one barrier a block.  The scores dO Vn^T
+// and dR Vn^T are dealt out to the waves in 16 x 16 blocks, gated and masked there
+// and shared through LDS, in the bytes of the tiles that are no longer needed.
 
 #include "chunk_bwd.h"
 #include "chunk_common.h"
@@ -22,44 +22,94 @@ namespace {
 
 using namespace bwd;
 
+constexpr int NTHREADS = 512;
+constexpr int VC = 32;   // V columns of a block
+
+// A stage holds a block's Vn^T and dR^T [v][t], h and dh' [v][k], and dO [t][v].  Later
+// the scores lie in the first stage, k and q [t][channel] in the second.
 template <typename C, int D>
 struct GradLds {
-  static constexpr int T64 = Tile<C, 64>::bytes(BT), TD = Tile<C, D>::bytes(BT);
-  // a block of 64 V columns: dO [t][v], Vn^T and dR^T [v][t], h and dh' [v][k];
-  // later the scores in the first three, k and q [t][channel] in the last two
-  static constexpr int O = 0, VN = T64, DR = 2 * T64, H = 3 * T64, DS = H + TD;
-  static constexpr int G = DS + TD;             // G, e^G, e^{G_last - G}, beta of the tokens
-  static constexpr int RED = G + 4 * BT * 4;    // dot products [4][4][64], one row for 32 channels
-  static constexpr int VDR = RED + 16 * BT * 4; // v . dR [64], <h, dh'> of each wave [4]
-  static constexpr int bytes = VDR + BT * 4 + 16;
+  typedef Tile<C, 64> T64;
+  typedef Tile<C, D> TD;
+  // dO rows: 64 bytes of fp16 (a fragment read takes 1 KiB in a row), fp32 padded
+  static constexpr int orow = sizeof(C) == 2 ? 64 : 4 * VC + 16;
+  static constexpr int VN = 0, DR = T64::bytes(VC), H = 2 * DR, DS = H + TD::bytes(VC), O = DS + TD::bytes(VC);
+  static constexpr int tiles = O + BT * orow;
+  static constexpr int S1 = 0, S2 = T64::bytes(BT), S3 = 2 * S2, scores = 3 * S2;
+  static constexpr int K = 0, Q = TD::bytes(BT), rows = 2 * Q;
+  static constexpr int max3(int a, int b) { return a > b ? a : b; }
+  static constexpr int first = max3(tiles, scores), second = max3(tiles, rows);
 };
 
-// Vectors of 8 elements that 256 threads move of a [64][COLS] tile.
-template <typename T, int COLS> struct Moved {
-  static constexpr int N = BT * COLS / 8 / 256;
-  Frag<T> f[N];
-  static __device__ __forceinline__ int row(int i, int tid) { return (tid + 256 * i) / (COLS / 8); }
-  static __device__ __forceinline__ int col(int i, int tid) { return (tid + 256 * i) % (COLS / 8) * 8; }
+// The copies of a block's four tiles on their way: straight to LDS (fp16, 16-byte units
+// at the places that the tiles' swizzle gives them), or through registers (fp32).
+template <typename C, int D> struct BlockIn;
+template <int D> struct BlockIn<f16_t, D> {
+  typedef GradLds<f16_t, D> L;
+  static constexpr int N64 = VC * 64 * 2 / 1024, ND = VC * D * 2 / 1024;   // 1 KiB pieces of a tile
+  static constexpr int N = (2 * N64 + 2 * ND) / 8;   // of each wave
+  uint32_t from[N];   // byte of the lane's unit in its tile
+  __device__ __forceinline__ void init(int w, int lane) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int p = w + 8 * i, q = p < 2 * N64 ? p % N64 : (p - 2 * N64) % ND, slot = q * 64 + lane;
+      if (p < 2 * N64) from[i] = slot / 8 * 128 + (slot % 8 ^ tiles::a_swz(slot / 8)) * 16;
+      else from[i] = slot / (D / 8) * (2 * D) + (slot % (D / 8) ^ tiles::qk_swz<D>(slot / (D / 8))) * 16;
+    }
+  }
+  __device__ __forceinline__ void issue(const f16_t* vn, const f16_t* dr, const f16_t* h, const f16_t* ds, char* st, int w) {
+    typedef __attribute__((address_space(3))) char lchar;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int p = w + 8 * i;   // uniform
+      const bool cols = p < 2 * N64;
+      const int q = cols ? p : p - 2 * N64, per = cols ? N64 : ND;
+      const f16_t* src = cols ? (q < per ? vn : dr) : (q < per ? h : ds);
+      const int to = (cols ? (q < per ? L::VN : L::DR) : (q < per ? L::H : L::DS)) + q % per * 1024;
+      tiles::dma16(reinterpret_cast<const char*>(src) + from[i], (lchar*)(st + to));
+    }
+  }
+  __device__ __forceinline__ void commit(char*, int) { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+};
+template <int D> struct BlockIn<float, D> {
+  typedef GradLds<float, D> L;
+  static constexpr int NW = VC * D / 8 / (NTHREADS / 2);   // vectors of h or dh' for each half of the threads
+  Frag<float> cols, wide[NW];
+  int t;
+  __device__ __forceinline__ void init(int w, int lane) { t = (w & 3) * 64 + lane; }
+  __device__ __forceinline__ void issue(const float* vn, const float* dr, const float* h, const float* ds, char*, int w) {
+    load8(cols, (w < 4 ? vn : dr) + t * 8);
+#pragma unroll
+    for (int i = 0; i < NW; ++i) load8(wide[i], (w < 4 ? h : ds) + (t + 256 * i) * 8);
+  }
+  __device__ __forceinline__ void commit(char* st, int tid) {
+    const bool first = tid < 256;
+    Tile<float, 64>::put(st + (first ? L::VN : L::DR), t / 8, t % 8 * 8, cols);
+#pragma unroll
+    for (int i = 0; i < NW; ++i) {
+      const int v = t + 256 * i;
+      Tile<float, D>::put(st + (first ? L::H : L::DS), v / (D / 8), v % (D / 8) * 8, wide[i]);
+    }
+  }
 };
 
 template <typename T, int D, bool GROUPED>
-__global__ __launch_bounds__(256) void gdn_bwd_grad_kernel(ChunkBwdArgs a) {
+__global__ __launch_bounds__(NTHREADS) __attribute__((amdgpu_waves_per_eu(sizeof(T) == 2 ? 4 : 2, sizeof(T) == 2 ? 4 : 2))) void gdn_bwd_grad_kernel(ChunkBwdArgs a) {
   typedef typename ComputeOf<T>::type C;
   typedef GradLds<C, D> L;
   typedef Tile<C, D> TD;
   typedef Tile<C, 64> T64;
-  constexpr int VB = D / 64;          // blocks of V columns
+  constexpr int VB = D / VC;          // blocks of V columns (an even number)
   constexpr int KW = D / 32;          // waves side by side over the channels
-  constexpr int NT = KW;              // 16-token blocks of a wave
-  extern __shared__ __attribute__((aligned(16))) char lds[];
-  float* const sG = reinterpret_cast<float*>(lds + L::G);
-  float* const red = reinterpret_cast<float*>(lds + L::RED);
-  float* const sVdr = reinterpret_cast<float*>(lds + L::VDR);
+  constexpr int NT = KW / 2;          // 16-token blocks of a wave
+  __shared__ __attribute__((aligned(16))) char st0[L::first], st1[L::second];
+  // G, e^G, e^{G_last - G}, beta of the tokens; dot products, one row for 32 channels;
+  // v . dR; <h, dh'> of each wave
+  __shared__ __attribute__((aligned(16))) float sG[4 * BT], red[16 * BT], sVdr[2 * BT], sHd[8];
 
-  const int tid = threadIdx.x, lane = tid & 63, n = lane & 15, g = lane >> 4;
-  const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int kw = w % KW, tb0 = w / KW * NT;   // the wave's channels 32 kw .. and token blocks
-  const int Hk = a.f.Hk, HV = a.f.HV, GR = HV / Hk;
+  const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int kw = w % KW, th = w / KW, tb0 = th * NT;   // the wave's channels 32 kw .. and token blocks
+  const int Hk = a.f.Hk, HV = a.f.HV, GR = GROUPED ? HV / Hk : 1;
   const int NTC = (a.f.T + BT - 1) / BT;
   int slot, jk, c0, nrow;
   if (!intra::slot_of_block(a.nslots, Hk, slot, jk)) return;
@@ -87,8 +137,23 @@ __global__ __launch_bounds__(256) void gdn_bwd_grad_kernel(ChunkBwdArgs a) {
 #pragma unroll
       for (int t = 0; t < NT; ++t) dq_sum[h][t] = dk_sum[h][t] = zero4();
   }
-
+  // the wave's block of the scores: lower blocks (tb, sb) in the order of tix
+  const int tbw = w >= 6 ? 3 : w >= 3 ? 2 : w >= 1 ? 1 : 0, sbw = w - tbw * (tbw + 1) / 2;
   for (int r = 0; r < GR; ++r) {
+    // what a lane derives from its place it derives once a head (see opaque)
+    const int tid = opaque(threadIdx.x), lane = tid & 63, n = lane & 15, g = lane >> 4;
+    // where the lane's fragments lie in a tile
+    const int pair0 = TD::pair_cols(kw, n, g);       // channels 32 kw .., 8 rows
+    const int block0 = T64::block_cols(0, n, g);      // 16 columns, 8 rows
+    const int row0 = n * L::orow + 8 * g * (int)sizeof(C);
+    // the rows of dO that this thread brings (the first 256), the token and columns whose v it meets
+    const int ot = tid / 4 & 63, oc = tid % 4 * 8;
+    const int vt = 16 * (w & 3) + n;
+    // 32-bit offsets of this thread's rows behind uniform addresses
+    const uint32_t o_off = (uint32_t)(ot < nrow ? ot : nrow - 1) * (uint32_t)vstride + oc;
+    const uint32_t v_off = (uint32_t)(vt < nrow ? vt : nrow - 1) * (uint32_t)vstride + 8 * g;
+    BlockIn<C, D> in;
+    in.init(w, lane);
     const int j = jk * GR + r;
     float inv = 1.f, gs = 1.f;
     if (a.amax) gs = grad_scale(a.amax[(size_t)ns * HV + j], inv);
@@ -101,32 +166,25 @@ __global__ __launch_bounds__(256) void gdn_bwd_grad_kernel(ChunkBwdArgs a) {
     const C* const hp = reinterpret_cast<const C*>(a.hs) + cell * D * D;
     const C* const dsp = reinterpret_cast<const C*>(a.ds) + cell * D * D;
 
-    Moved<T, 64> o_in;
-    Moved<C, 64> vn_in, dr_in;
-    Moved<C, D> h_in, ds_in;
-    auto fetch = [&](int vb) {
-#pragma unroll
-      for (int i = 0; i < o_in.N; ++i) {
-        const int t = o_in.row(i, tid), v = 64 * vb + o_in.col(i, tid);
-        if (t < nrow) load8(o_in.f[i], dop + (size_t)t * vstride + v);
-        else o_in.f[i].zero();
-      }
-#pragma unroll
-      for (int i = 0; i < vn_in.N; ++i) {
-        const size_t at = (size_t)(64 * vb + vn_in.row(i, tid)) * BT + vn_in.col(i, tid);
-        load8(vn_in.f[i], vnp + at);
-        load8(dr_in.f[i], drp + at);
-      }
-#pragma unroll
-      for (int i = 0; i < h_in.N; ++i) {
-        const size_t at = (size_t)(64 * vb + h_in.row(i, tid)) * D + h_in.col(i, tid);
-        load8(h_in.f[i], hp + at);
-        load8(ds_in.f[i], dsp + at);
+    Frag<T> o_in, v_in, k_in[D / 64], q_in[D / 64];
+    auto issue = [&](int vb, char* st) __attribute__((always_inline)) {
+      const int v0 = VC * vb;
+      if (tid < 256) load8(o_in, dop + v0 + o_off);
+      if ((vb & 1) == w >> 2) load8(v_in, vp + v0 + v_off);
+      in.issue(vnp + v0 * BT, drp + v0 * BT, hp + v0 * D, dsp + v0 * D, st, w);
+    };
+    auto commit = [&](char* st) __attribute__((always_inline)) {
+      in.commit(st, tid);
+      if (tid < 256) {
+        Frag<C> f = widen(o_in, gs);
+        if (ot >= nrow) f.zero();
+        if constexpr (sizeof(C) == 2) *reinterpret_cast<f16x8*>(st + L::O + ot * L::orow + 2 * oc) = f.v;
+        else *reinterpret_cast<f32x8*>(st + L::O + ot * L::orow + 4 * oc) = f.v;
       }
     };
-    fetch(0);
+    issue(0, st0);
     // the gates: G again from its terms, beta
-    if (w == 0) {
+    if (w == 7) {
       const int tl = lane < nrow ? lane : nrow - 1;
       const float graw = a.f.g ? a.f.g[(size_t)(c0 + tl) * HV + j] : (a.f.g_gamma ? a.f.g_gamma[j] : 0.f);
       const float b = a.f.beta[(size_t)(c0 + tl) * HV + j];
@@ -138,114 +196,81 @@ __global__ __launch_bounds__(256) void gdn_bwd_grad_kernel(ChunkBwdArgs a) {
       sG[3 * BT + lane] = lane < nrow ? b : 0.f;
     }
 
-    f32x4 dq[2][NT], E[2][NT], W[2][NT], M[5];
+    f32x4 dq[2][NT], E[2][NT], W[2][NT], M[3];
 #pragma unroll
     for (int h = 0; h < 2; ++h)
 #pragma unroll
       for (int t = 0; t < NT; ++t) dq[h][t] = E[h][t] = W[h][t] = zero4();
 #pragma unroll
-    for (int i = 0; i < 5; ++i) M[i] = zero4();
-    float hd = 0.f;     // <h, dh'>, this thread's elements
-    float vdr = 0.f;    // v . dR of token 16 w + n, this lane's channels
-
-    for (int vb = 0; vb < VB; ++vb) {
-      __syncthreads();
+    for (int i = 0; i < 3; ++i) M[i] = zero4();
+    float hd = 0.f;        // <h, dh'>, the lane's elements
+    float vdr = 0.f;       // v . dR of token vt, the lane's columns
+    auto step = [&](int vb, char* st, char* next) __attribute__((always_inline)) {
+      commit(st);
+      tiles::lds_barrier();
+      const int o_pair = opaque(pair0), o_block = opaque(block0), o_row = opaque(row0);
+      // dv of token vt, and v . dR (a transposing read takes part of its addresses from
+      // other lanes: all of them, also behind the end, where dR is 0)
+      if ((vb & 1) == w >> 2) {
+        const f32x8 x = values(T64::col(st + L::DR + T64::to_block(o_block, w & 3))), y = values(v_in);
 #pragma unroll
-      for (int i = 0; i < o_in.N; ++i) T64::put(lds + L::O, o_in.row(i, tid), o_in.col(i, tid), widen(o_in.f[i], gs));
-#pragma unroll
-      for (int i = 0; i < vn_in.N; ++i) {
-        T64::put(lds + L::VN, vn_in.row(i, tid), vn_in.col(i, tid), vn_in.f[i]);
-        T64::put(lds + L::DR, dr_in.row(i, tid), dr_in.col(i, tid), dr_in.f[i]);
+        for (int e = 0; e < 8; ++e) vdr = fmaf(x[e], y[e], vdr);
+        if (vt < nrow) store_io8(dvp + VC * vb + v_off, x * (sG[3 * BT + vt] * inv));
       }
+      if (vb + 1 < VB) issue(vb + 1, next);
+      Frag<C> hf[2], df[2];
 #pragma unroll
-      for (int i = 0; i < h_in.N; ++i) {
-        TD::put(lds + L::H, h_in.row(i, tid), h_in.col(i, tid), h_in.f[i]);
-        TD::put(lds + L::DS, ds_in.row(i, tid), ds_in.col(i, tid), ds_in.f[i]);
-        const f32x8 x = values(h_in.f[i]), y = values(ds_in.f[i]);
+      for (int h = 0; h < 2; ++h) {
+        hf[h] = TD::col(st + L::H + o_pair + h * TD::odd);
+        df[h] = TD::col(st + L::DS + o_pair + h * TD::odd);
+      }
+      // each pair of waves with the same channels takes one half of <h, dh'>
+      if (th < 2) {
+        const f32x8 x = values(th ? hf[1] : hf[0]), y = values(th ? df[1] : df[0]);
 #pragma unroll
         for (int e = 0; e < 8; ++e) hd = fmaf(x[e], y[e], hd);
       }
-      if (vb + 1 < VB) fetch(vb + 1);
-      __syncthreads();
-
 #pragma unroll
-      for (int s = 0; s < 2; ++s) {
-        const int r0 = 32 * s + 8 * g;   // the lane's 8 V columns of the block
-        Frag<C> hf[2], df[2];
+      for (int t = 0; t < NT; ++t) {
+        const int tb = tb0 + t;
+        const Frag<C> of = T64::row(st + L::O + 16 * tb * L::orow + o_row);
+        const Frag<C> rf = T64::col(st + L::DR + T64::to_block(o_block, tb));
+        const Frag<C> vf = T64::col(st + L::VN + T64::to_block(o_block, tb));
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          hf[h] = TD::col(lds + L::H + TD::pair_cols(kw, n, g) + 32 * s * TD::pitch + h * TD::odd);
-          df[h] = TD::col(lds + L::DS + TD::pair_cols(kw, n, g) + 32 * s * TD::pitch + h * TD::odd);
-        }
-#pragma unroll
-        for (int t = 0; t < NT; ++t) {
-          const int tb = tb0 + t;
-          const Frag<C> of = T64::row8(lds + L::O, 16 * tb + n, r0);
-          const Frag<C> rf = T64::col(lds + L::DR + T64::block_cols(tb, n, g) + 32 * s * T64::pitch);
-          const Frag<C> vf = T64::col(lds + L::VN + T64::block_cols(tb, n, g) + 32 * s * T64::pitch);
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            dq[h][t] = mma(hf[h], of, dq[h][t]);
-            E[h][t] = mma(hf[h], rf, E[h][t]);
-            W[h][t] = mma(df[h], vf, W[h][t]);
-          }
-        }
-        // scores, transposed: block i of the wave is one of dO Vn^T (0 .. 9) or dR Vn^T
-        // (10 .. 19), lower blocks (tb, sb) in the order of tix
-#pragma unroll
-        for (int i = 0; i < 5; ++i) {
-          const int b = w + 4 * i;
-          const int m = b >= 10 ? b - 10 : b;
-          const int tb = m >= 6 ? 3 : m >= 3 ? 2 : m >= 1 ? 1 : 0, sb = m - tb * (tb + 1) / 2;
-          const Frag<C> vf = T64::col(lds + L::VN + T64::block_cols(sb, n, g) + 32 * s * T64::pitch);
-          const Frag<C> xf = b >= 10 ? T64::col(lds + L::DR + T64::block_cols(tb, n, g) + 32 * s * T64::pitch)
-                                     : T64::row8(lds + L::O, 16 * tb + n, r0);
-          M[i] = mma(vf, xf, M[i]);
-        }
-        // dv of token 16 w + n, and v . dR
-        const int t = 16 * w + n;
-        if (t < nrow) {
-          const f32x8 x = values(T64::col(lds + L::DR + T64::block_cols(w, n, g) + 32 * s * T64::pitch));
-          const size_t at = (size_t)t * vstride + 64 * vb + r0;
-          Frag<T> vv;
-          load8(vv, vp + at);
-          const f32x8 y = values(vv);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) vdr = fmaf(x[e], y[e], vdr);
-          store_io8(dvp + at, x * (sG[3 * BT + t] * inv));
+          dq[h][t] = mma(hf[h], of, dq[h][t]);
+          E[h][t] = mma(hf[h], rf, E[h][t]);
+          W[h][t] = mma(df[h], vf, W[h][t]);
         }
       }
-    }
-    // k and q rows for the products within the chunk, in flight over the barrier
-    Moved<T, D> k_in, q_in;
-#pragma unroll
-    for (int i = 0; i < k_in.N; ++i) {
-      const int t = k_in.row(i, tid), c = k_in.col(i, tid);
-      if (t < nrow) {
-        load8(k_in.f[i], kp + (size_t)t * krow + c);
-        load8(q_in.f[i], qp + (size_t)t * krow + c);
-      } else {
-        k_in.f[i].zero();
-        q_in.f[i].zero();
+      // scores, transposed: blocks `w` (and 8 + w % 2, dealt to four waves) of both
+      const Frag<C> vf = T64::col(st + L::VN + T64::to_block(o_block, sbw));
+      M[0] = mma(vf, T64::row(st + L::O + 16 * tbw * L::orow + o_row), M[0]);
+      M[1] = mma(vf, T64::col(st + L::DR + T64::to_block(o_block, tbw)), M[1]);
+      if (w < 4) {
+        const Frag<C> vl = T64::col(st + L::VN + T64::to_block(o_block, 2 + (w & 1)));
+        M[2] = mma(vl, w < 2 ? T64::row(st + L::O + 48 * L::orow + o_row)
+                             : T64::col(st + L::DR + T64::to_block(o_block, 3)), M[2]);
       }
+    };
+    for (int vb = 0; vb < VB; vb += 2) {
+      step(vb, st0, st1);
+      step(vb + 1, st1, st0);
     }
-    __syncthreads();
-    char* const sK = lds + L::H;
-    char* const sQ = lds + L::DS;
-    char* const S1 = lds + L::O;    // scale dO Vn^T o Gamma, s <= t
-    char* const S2 = lds + L::VN;   // -dR Vn^T o Gamma, s < t
-    char* const S3 = lds + L::DR;   // beta_t times that
+
+    // k and q rows for the products within the chunk
 #pragma unroll
-    for (int i = 0; i < k_in.N; ++i) {
-      TD::put(sK, k_in.row(i, tid), k_in.col(i, tid), widen(k_in.f[i]));
-      TD::put(sQ, q_in.row(i, tid), q_in.col(i, tid), widen(q_in.f[i]));
+    for (int i = 0; i < D / 64; ++i) {
+      const int x = tid + NTHREADS * i, t = x / (D / 8), c = x % (D / 8) * 8;
+      const uint32_t off = (uint32_t)(t < nrow ? t : nrow - 1) * (uint32_t)krow + c;
+      load8(k_in[i], kp + off);
+      load8(q_in[i], qp + off);
     }
-#pragma unroll
-    for (int i = 0; i < 5; ++i) {
-      const int b = w + 4 * i;
-      const bool second = b >= 10;
-      const int m = second ? b - 10 : b;
-      const int tb = m >= 6 ? 3 : m >= 3 ? 2 : m >= 1 ? 1 : 0, sb = m - tb * (tb + 1) / 2;
+    // the scores into the first stage, whose last readers have passed a barrier
+    char* const S1 = st0 + L::S1;    // scale dO Vn^T o Gamma, s <= t
+    char* const S2 = st0 + L::S2;    // -dR Vn^T o Gamma, s < t
+    char* const S3 = st0 + L::S3;    // beta_t times that
+    auto put_score = [&](const f32x4& m, bool second, int tb, int sb) __attribute__((always_inline)) {
       const int t = 16 * tb + n, s = 16 * sb + 4 * g;
       const float Gt = sG[t], f = second ? -1.f : a.f.scale;
       const f32x4 Gs = *reinterpret_cast<const f32x4*>(sG + s);
@@ -253,26 +278,45 @@ __global__ __launch_bounds__(256) void gdn_bwd_grad_kernel(ChunkBwdArgs a) {
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const bool keep = second ? s + e < t : s + e <= t;
-        x[e] = keep ? f * M[i][e] * __expf(Gt - Gs[e]) : 0.f;
+        x[e] = keep ? f * m[e] * __expf(Gt - Gs[e]) : 0.f;
       }
       T64::put4(second ? S2 : S1, t, s, x);
       if (second) T64::put4(S3, t, s, x * sG[3 * BT + t]);
-    }
+    };
+    put_score(M[0], false, tbw, sbw);
+    put_score(M[1], true, tbw, sbw);
+    if (w < 4) put_score(M[2], w >= 2, 3, 2 + (w & 1));
     // the blocks above the diagonal that a 32-wide slab takes in
-    for (int i = w; i < 6; i += 4) {
-      char* const tile = i / 2 == 0 ? S1 : i / 2 == 1 ? S2 : S3;
-      T64::put4(tile, 32 * (i & 1) + n, 32 * (i & 1) + 16 + 4 * g, zero4());
+    if (w < 6) {
+      char* const tile = w / 2 == 0 ? S1 : w / 2 == 1 ? S2 : S3;
+      T64::put4(tile, 32 * (w & 1) + n, 32 * (w & 1) + 16 + 4 * g, zero4());
     }
-    __syncthreads();
+    tiles::lds_barrier();
+    char* const sK = st1 + L::K;
+    char* const sQ = st1 + L::Q;
+#pragma unroll
+    for (int i = 0; i < D / 64; ++i) {
+      const int x = tid + NTHREADS * i, t = x / (D / 8), c = x % (D / 8) * 8;
+      Frag<C> kk = widen(k_in[i]), qq = widen(q_in[i]);
+      if (t >= nrow) {
+        kk.zero();
+        qq.zero();
+      }
+      TD::put(sK, t, c, kk);
+      TD::put(sQ, t, c, qq);
+    }
+    tiles::lds_barrier();
 
+    const int o_pair = opaque(pair0), o_block = opaque(block0);
+    const int o_score = opaque(T64::off(n, 8 * g)), o_chan = opaque(TD::off(n, 32 * kw + 8 * g));
     // row factors, the dot product with k of what crosses the chunk's end
     Frag<C> kf[NT], qf[NT];
     float wi[NT];
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
       const int tok = 16 * (tb0 + t) + n;
-      kf[t] = TD::row8(sK, tok, 32 * kw + 8 * g);
-      qf[t] = TD::row8(sQ, tok, 32 * kw + 8 * g);
+      kf[t] = TD::row(sK + TD::to_rows(o_chan, tb0 + t));
+      qf[t] = TD::row(sQ + TD::to_rows(o_chan, tb0 + t));
       const float ex = sG[BT + tok], ey = sG[2 * BT + tok];
       const f32x8 k8 = values(kf[t]);
       wi[t] = 0.f;
@@ -288,18 +332,18 @@ __global__ __launch_bounds__(256) void gdn_bwd_grad_kernel(ChunkBwdArgs a) {
     // products within the chunk: only slabs that meet entries below the diagonal
 #pragma unroll
     for (int p = 0; p < 2; ++p) {
-      const int r0 = 32 * p + 8 * g;
       Frag<C> ka[2], qa[2];
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        ka[h] = TD::col(sK + TD::pair_cols(kw, n, g) + 32 * p * TD::pitch + h * TD::odd);
-        qa[h] = TD::col(sQ + TD::pair_cols(kw, n, g) + 32 * p * TD::pitch + h * TD::odd);
+        ka[h] = TD::col(sK + o_pair + 32 * p * TD::pitch + h * TD::odd);
+        qa[h] = TD::col(sQ + o_pair + 32 * p * TD::pitch + h * TD::odd);
       }
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
         const int tb = tb0 + t;
         if (2 * p <= tb) {   // s of the slab up to t
-          const Frag<C> s1 = T64::row8(S1, 16 * tb + n, r0), s2 = T64::row8(S2, 16 * tb + n, r0);
+          const int at = T64::to_rows(o_score, tb, p);
+          const Frag<C> s1 = T64::row(S1 + at), s2 = T64::row(S2 + at);
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             dq[h][t] = mma(ka[h], s1, dq[h][t]);
@@ -307,7 +351,8 @@ __global__ __launch_bounds__(256) void gdn_bwd_grad_kernel(ChunkBwdArgs a) {
           }
         }
         if (2 * p + 1 >= tb) {   // t of the slab from s = 16 tb + n on
-          const Frag<C> s1 = T64::col(S1 + T64::block_cols(tb, n, g) + 32 * p * T64::pitch), s3 = T64::col(S3 + T64::block_cols(tb, n, g) + 32 * p * T64::pitch);
+          const int at = T64::to_block(o_block, tb) + 32 * p * T64::pitch;
+          const Frag<C> s1 = T64::col(S1 + at), s3 = T64::col(S3 + at);
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             W[h][t] = mma(qa[h], s1, W[h][t]);
@@ -316,21 +361,20 @@ __global__ __launch_bounds__(256) void gdn_bwd_grad_kernel(ChunkBwdArgs a) {
         }
       }
     }
-    // dots over the wave's channels, and the sums of k . E and the rest
+    // dots over the wave's channels
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
       const int tok = 16 * (tb0 + t) + n;
       const f32x8 k8 = values(kf[t]), q8 = values(qf[t]);
-      float qd = 0.f, ke = 0.f, kW = 0.f;
+      float d[4] = {0.f, 0.f, 0.f, wi[t]};   // q . dq, k . E, k . W, and the part of k . W that crosses the end
 #pragma unroll
       for (int h = 0; h < 2; ++h)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          qd = fmaf(q8[4 * h + e], dq[h][t][e], qd);
-          ke = fmaf(k8[4 * h + e], E[h][t][e], ke);
-          kW = fmaf(k8[4 * h + e], W[h][t][e], kW);
+          d[0] = fmaf(q8[4 * h + e], dq[h][t][e], d[0]);
+          d[1] = fmaf(k8[4 * h + e], E[h][t][e], d[1]);
+          d[2] = fmaf(k8[4 * h + e], W[h][t][e], d[2]);
         }
-      float d[4] = {qd, ke, kW, wi[t]};
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         d[i] += __shfl_xor(d[i], 16, 64);
@@ -359,11 +403,11 @@ __global__ __launch_bounds__(256) void gdn_bwd_grad_kernel(ChunkBwdArgs a) {
     }
     vdr += __shfl_xor(vdr, 16, 64);
     vdr += __shfl_xor(vdr, 32, 64);
-    if (g == 0) sVdr[16 * w + n] = vdr;
+    if (g == 0) sVdr[(w >> 2) * BT + vt] = vdr;
 #pragma unroll
     for (int off = 1; off < 64; off <<= 1) hd += __shfl_xor(hd, off, 64);
-    if (lane == 0) sVdr[BT + w] = hd;
-    __syncthreads();
+    if (lane == 0) sHd[w] = hd;
+    tiles::lds_barrier();
     if (w == 0) {
       float d[4];
 #pragma unroll
@@ -379,7 +423,10 @@ __global__ __launch_bounds__(256) void gdn_bwd_grad_kernel(ChunkBwdArgs a) {
       float cross = live ? d[3] : 0.f;
 #pragma unroll
       for (int off = 1; off < 64; off <<= 1) cross += __shfl_xor(cross, off, 64);
-      cross += sG[BT + nrow - 1] * ((sVdr[BT] + sVdr[BT + 1]) + (sVdr[BT + 2] + sVdr[BT + 3]));
+      float hh = 0.f;
+#pragma unroll
+      for (int c = 0; c < 8; ++c) hh += sHd[c];
+      cross += sG[BT + nrow - 1] * hh;
       // sums from each row to the end
 #pragma unroll
       for (int off = 1; off < 64; off <<= 1) {
@@ -389,12 +436,13 @@ __global__ __launch_bounds__(256) void gdn_bwd_grad_kernel(ChunkBwdArgs a) {
       if (live) {
         const size_t at = (size_t)(c0 + lane) * HV + j;
         if (a.dg) reinterpret_cast<T*>(a.dg)[at] = from_f<T>((dG + cross) * inv);
-        reinterpret_cast<T*>(a.dbeta)[at] = from_f<T>((sVdr[lane] + d[1]) * inv);
+        reinterpret_cast<T*>(a.dbeta)[at] = from_f<T>((sVdr[lane] + sVdr[BT + lane] + d[1]) * inv);
       }
     }
-    __syncthreads();   // the gates and dots are written again for the next head
+    if (r + 1 < GR) tiles::lds_barrier();   // the tiles, gates and dots are written again for the next head
   }
   if constexpr (GROUPED) {
+    const int lane = threadIdx.x & 63, n = lane & 15, g = lane >> 4;
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
       const int tok = 16 * (tb0 + t) + n;
@@ -409,12 +457,8 @@ __global__ __launch_bounds__(256) void gdn_bwd_grad_kernel(ChunkBwdArgs a) {
 
 template <typename T, int D, bool GROUPED>
 hipError_t launch_grad(const ChunkBwdArgs& a, hipStream_t s) {
-  typedef GradLds<typename ComputeOf<T>::type, D> L;
-  const void* kern = reinterpret_cast<const void*>(gdn_bwd_grad_kernel<T, D, GROUPED>);
-  if (L::bytes > 65536)
-    if (hipError_t e = hipFuncSetAttribute(kern, hipFuncAttributeMaxDynamicSharedMemorySize, L::bytes)) return e;
-  hipLaunchKernelGGL((gdn_bwd_grad_kernel<T, D, GROUPED>), dim3(intra::intra_blocks(a.nslots, a.f.Hk)), dim3(256),
-                     L::bytes, s, a);
+  hipLaunchKernelGGL((gdn_bwd_grad_kernel<T, D, GROUPED>), dim3(intra::intra_blocks(a.nslots, a.f.Hk)), dim3(NTHREADS), 0,
+                     s, a);
   return hipGetLastError();
 }
 
