@@ -37,8 +37,8 @@ struct GradLds {
   static constexpr int tiles = O + BT * orow;
   static constexpr int S1 = 0, S2 = T64::bytes(BT), S3 = 2 * S2, scores = 3 * S2;
   static constexpr int K = 0, Q = TD::bytes(BT), rows = 2 * Q;
-  static constexpr int max3(int a, int b) { return a > b ? a : b; }
-  static constexpr int first = max3(tiles, scores), second = max3(tiles, rows);
+  static constexpr int more(int a, int b) { return a > b ? a : b; }
+  static constexpr int first = more(tiles, scores), second = more(tiles, rows);
 };
 
 // The copies of a block's four tiles on their way: straight to LDS (fp16, 16-byte units
@@ -94,7 +94,7 @@ template <int D> struct BlockIn<float, D> {
 };
 
 template <typename T, int D, bool GROUPED>
-__global__ __launch_bounds__(NTHREADS) __attribute__((amdgpu_waves_per_eu(sizeof(T) == 2 ? 4 : 2, sizeof(T) == 2 ? 4 : 2))) void gdn_bwd_grad_kernel(ChunkBwdArgs a) {
+__global__ __launch_bounds__(NTHREADS) __attribute__((amdgpu_waves_per_eu(sizeof(T) == 2 && !(GROUPED && D == 128) ? 4 : 2))) void gdn_bwd_grad_kernel(ChunkBwdArgs a) {
   typedef typename ComputeOf<T>::type C;
   typedef GradLds<C, D> L;
   typedef Tile<C, D> TD;
@@ -102,7 +102,12 @@ __global__ __launch_bounds__(NTHREADS) __attribute__((amdgpu_waves_per_eu(sizeof
   constexpr int VB = D / VC;          // blocks of V columns (an even number)
   constexpr int KW = D / 32;          // waves side by side over the channels
   constexpr int NT = KW / 2;          // 16-token blocks of a wave
-  __shared__ __attribute__((aligned(16))) char st0[L::first], st1[L::second];
+  // Several heads a work-group (one a CU, for its registers): the scores and k, q have room of
+  // their own, so k and q come once and the next head's first block while this one's chunk
+  // products run.
+  constexpr bool APART = GROUPED && sizeof(C) == 2;
+  __shared__ __attribute__((aligned(16))) char st0[APART ? L::tiles : L::first], st1[APART ? L::tiles : L::second];
+  __shared__ __attribute__((aligned(16))) char own_scores[APART ? L::scores : 16], own_rows[APART ? L::rows : 16];
   // G, e^G, e^{G_last - G}, beta of the tokens; dot products, one row for 32 channels;
   // v . dR; <h, dh'> of each wave
   __shared__ __attribute__((aligned(16))) float sG[4 * BT], red[16 * BT], sVdr[2 * BT], sHd[8];
@@ -139,6 +144,7 @@ __global__ __launch_bounds__(NTHREADS) __attribute__((amdgpu_waves_per_eu(sizeof
   }
   // the wave's block of the scores: lower blocks (tb, sb) in the order of tix
   const int tbw = w >= 6 ? 3 : w >= 3 ? 2 : w >= 1 ? 1 : 0, sbw = w - tbw * (tbw + 1) / 2;
+  Frag<T> o_in, v_in;   // dO and v of the block on its way
   for (int r = 0; r < GR; ++r) {
     // what a lane derives from its place it derives once a head (see opaque)
     const int tid = opaque(threadIdx.x), lane = tid & 63, n = lane & 15, g = lane >> 4;
@@ -157,21 +163,39 @@ __global__ __launch_bounds__(NTHREADS) __attribute__((amdgpu_waves_per_eu(sizeof
     const int j = jk * GR + r;
     float inv = 1.f, gs = 1.f;
     if (a.amax) gs = grad_scale(a.amax[(size_t)ns * HV + j], inv);
-    const size_t cell = (size_t)slot * HV + j;
-    const T* const dop = reinterpret_cast<const T*>(a.dout) + (size_t)c0 * vstride + (size_t)j * D;
-    const T* const vp = reinterpret_cast<const T*>(a.f.v) + (size_t)c0 * vstride + (size_t)j * D;
     T* const dvp = reinterpret_cast<T*>(a.dv) + (size_t)c0 * vstride + (size_t)j * D;
-    const C* const vnp = reinterpret_cast<const C*>(a.vn) + cell * D * BT;
-    const C* const drp = reinterpret_cast<const C*>(a.dr) + cell * D * BT;
-    const C* const hp = reinterpret_cast<const C*>(a.hs) + cell * D * D;
-    const C* const dsp = reinterpret_cast<const C*>(a.ds) + cell * D * D;
 
-    Frag<T> o_in, v_in, k_in[D / 64], q_in[D / 64];
-    auto issue = [&](int vb, char* st) __attribute__((always_inline)) {
-      const int v0 = VC * vb;
-      if (tid < 256) load8(o_in, dop + v0 + o_off);
-      if ((vb & 1) == w >> 2) load8(v_in, vp + v0 + v_off);
-      in.issue(vnp + v0 * BT, drp + v0 * BT, hp + v0 * D, dsp + v0 * D, st, w);
+    Frag<T> k_in[D / 64], q_in[D / 64];
+    auto issue = [&](int jj, int vb, char* st) __attribute__((always_inline)) {
+      const size_t cell = (size_t)slot * HV + jj, first = (size_t)c0 * vstride + (size_t)jj * D + VC * vb;
+      if (tid < 256) load8(o_in, reinterpret_cast<const T*>(a.dout) + first + o_off);
+      if ((vb & 1) == w >> 2) load8(v_in, reinterpret_cast<const T*>(a.f.v) + first + v_off);
+      in.issue(reinterpret_cast<const C*>(a.vn) + (cell * D + VC * vb) * BT,
+               reinterpret_cast<const C*>(a.dr) + (cell * D + VC * vb) * BT,
+               reinterpret_cast<const C*>(a.hs) + (cell * D + VC * vb) * D,
+               reinterpret_cast<const C*>(a.ds) + (cell * D + VC * vb) * D, st, w);
+    };
+    auto fetch_rows = [&]() __attribute__((always_inline)) {   // k and q for the products within the chunk
+#pragma unroll
+      for (int i = 0; i < D / 64; ++i) {
+        const int x = tid + NTHREADS * i, t = x / (D / 8), c = x % (D / 8) * 8;
+        const uint32_t off = (uint32_t)(t < nrow ? t : nrow - 1) * (uint32_t)krow + c;
+        load8(k_in[i], kp + off);
+        load8(q_in[i], qp + off);
+      }
+    };
+    auto put_rows = [&](char* sK, char* sQ) __attribute__((always_inline)) {
+#pragma unroll
+      for (int i = 0; i < D / 64; ++i) {
+        const int x = tid + NTHREADS * i, t = x / (D / 8), c = x % (D / 8) * 8;
+        Frag<C> kk = widen(k_in[i]), qq = widen(q_in[i]);
+        if (t >= nrow) {
+          kk.zero();
+          qq.zero();
+        }
+        TD::put(sK, t, c, kk);
+        TD::put(sQ, t, c, qq);
+      }
     };
     auto commit = [&](char* st) __attribute__((always_inline)) {
       in.commit(st, tid);
@@ -182,7 +206,11 @@ __global__ __launch_bounds__(NTHREADS) __attribute__((amdgpu_waves_per_eu(sizeof
         else *reinterpret_cast<f32x8*>(st + L::O + ot * L::orow + 4 * oc) = f.v;
       }
     };
-    issue(0, st0);
+    if (!APART || r == 0) issue(j, 0, st0);
+    if (APART && r == 0) {
+      fetch_rows();
+      put_rows(own_rows + L::K, own_rows + L::Q);
+    }
     // the gates: G again from its terms, beta
     if (w == 7) {
       const int tl = lane < nrow ? lane : nrow - 1;
@@ -217,7 +245,8 @@ __global__ __launch_bounds__(NTHREADS) __attribute__((amdgpu_waves_per_eu(sizeof
         for (int e = 0; e < 8; ++e) vdr = fmaf(x[e], y[e], vdr);
         if (vt < nrow) store_io8(dvp + VC * vb + v_off, x * (sG[3 * BT + vt] * inv));
       }
-      if (vb + 1 < VB) issue(vb + 1, next);
+      if (vb + 1 < VB) issue(j, vb + 1, next);
+      else if (APART && r + 1 < GR) issue(j + 1, 0, next);   // `next` is the first stage
       Frag<C> hf[2], df[2];
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
@@ -258,18 +287,12 @@ __global__ __launch_bounds__(NTHREADS) __attribute__((amdgpu_waves_per_eu(sizeof
       step(vb + 1, st1, st0);
     }
 
-    // k and q rows for the products within the chunk
-#pragma unroll
-    for (int i = 0; i < D / 64; ++i) {
-      const int x = tid + NTHREADS * i, t = x / (D / 8), c = x % (D / 8) * 8;
-      const uint32_t off = (uint32_t)(t < nrow ? t : nrow - 1) * (uint32_t)krow + c;
-      load8(k_in[i], kp + off);
-      load8(q_in[i], qp + off);
-    }
-    // the scores into the first stage, whose last readers have passed a barrier
-    char* const S1 = st0 + L::S1;    // scale dO Vn^T o Gamma, s <= t
-    char* const S2 = st0 + L::S2;    // -dR Vn^T o Gamma, s < t
-    char* const S3 = st0 + L::S3;    // beta_t times that
+    if constexpr (!APART) fetch_rows();
+    // the scores, in the bytes of the first stage, whose last readers have passed a barrier
+    char* const scores = APART ? own_scores : st0;
+    char* const S1 = scores + L::S1;    // scale dO Vn^T o Gamma, s <= t
+    char* const S2 = scores + L::S2;    // -dR Vn^T o Gamma, s < t
+    char* const S3 = scores + L::S3;    // beta_t times that
     auto put_score = [&](const f32x4& m, bool second, int tb, int sb) __attribute__((always_inline)) {
       const int t = 16 * tb + n, s = 16 * sb + 4 * g;
       const float Gt = sG[t], f = second ? -1.f : a.f.scale;
@@ -292,20 +315,12 @@ __global__ __launch_bounds__(NTHREADS) __attribute__((amdgpu_waves_per_eu(sizeof
       T64::put4(tile, 32 * (w & 1) + n, 32 * (w & 1) + 16 + 4 * g, zero4());
     }
     tiles::lds_barrier();
-    char* const sK = st1 + L::K;
-    char* const sQ = st1 + L::Q;
-#pragma unroll
-    for (int i = 0; i < D / 64; ++i) {
-      const int x = tid + NTHREADS * i, t = x / (D / 8), c = x % (D / 8) * 8;
-      Frag<C> kk = widen(k_in[i]), qq = widen(q_in[i]);
-      if (t >= nrow) {
-        kk.zero();
-        qq.zero();
-      }
-      TD::put(sK, t, c, kk);
-      TD::put(sQ, t, c, qq);
+    char* const sK = (APART ? own_rows : st1) + L::K;
+    char* const sQ = (APART ? own_rows : st1) + L::Q;
+    if constexpr (!APART) {
+      put_rows(sK, sQ);
+      tiles::lds_barrier();
     }
-    tiles::lds_barrier();
 
     const int o_pair = opaque(pair0), o_block = opaque(block0);
     const int o_score = opaque(T64::off(n, 8 * g)), o_chan = opaque(TD::off(n, 32 * kw + 8 * g));
