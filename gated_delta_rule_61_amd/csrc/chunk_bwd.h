@@ -96,13 +96,15 @@ __device__ __forceinline__ void store8(float* p, const Frag<float>& f) {
   store_nt16(p, f32x4{f.v[0], f.v[1], f.v[2], f.v[3]});
   store_nt16(p + 4, f32x4{f.v[4], f.v[5], f.v[6], f.v[7]});
 }
-// ... eight fp32 values in the io type
+// ... eight fp32 values in the io type.  Not as streaming stores: the waves of a
+// work-group write the halves of a line, which the L2 joins.
 __device__ __forceinline__ void store_io8(bf16_t* p, const f32x8& x) {
-  store_nt16(p, tiles::u32x4{pack_bf2(x[0], x[1]), pack_bf2(x[2], x[3]), pack_bf2(x[4], x[5]), pack_bf2(x[6], x[7])});
+  *reinterpret_cast<tiles::u32x4*>(p) =
+      tiles::u32x4{pack_bf2(x[0], x[1]), pack_bf2(x[2], x[3]), pack_bf2(x[4], x[5]), pack_bf2(x[6], x[7])};
 }
 __device__ __forceinline__ void store_io8(float* p, const f32x8& x) {
-  store_nt16(p, f32x4{x[0], x[1], x[2], x[3]});
-  store_nt16(p + 4, f32x4{x[4], x[5], x[6], x[7]});
+  *reinterpret_cast<f32x4*>(p) = f32x4{x[0], x[1], x[2], x[3]};
+  *reinterpret_cast<f32x4*>(p + 4) = f32x4{x[4], x[5], x[6], x[7]};
 }
 
 // An LDS tile of rows of COLS elements.  16-bit: 16-byte units swizzled by row as
@@ -186,6 +188,48 @@ template <int COLS> struct Tile<float, COLS> {
     for (int e = 0; e < 8; ++e) f.v[e] = *reinterpret_cast<const float*>(t + e * pitch);
     return f;
   }
+};
+
+// [rows of V][COLS] arrays that the scans leave for the chunks' gradients (h, dh': COLS =
+// K; Vn^T, dR^T: 64 tokens), in memory and, 32 rows at a time, in LDS alike.  fp16: for 16
+// rows and 32 columns one piece of 1 KiB, which a wave stores in one go: the 16 bytes
+// (columns 8 g .. 8 g + 7) of row n at unit 16 g + (n ^ 4 g).  That order, copied as it is,
+// leaves the transposing reads without bank conflicts.  fp32: rows.
+template <typename C, int COLS> struct Kept;
+template <int COLS> struct Kept<f16_t, COLS> {
+  static constexpr int odd = 8;
+  static constexpr int bytes = 32 * COLS * 2;   // of 32 rows
+  // element of the 8 columns 32 s + 8 g of row 16 blk + n
+  static __device__ __forceinline__ uint32_t at(int blk, int s, int n, int g) {
+    return (uint32_t)((blk * (COLS / 32) + s) * 64 + g * 16 + (n ^ 4 * g)) * 8;
+  }
+  // as in Tile: columns of block pair `pair` in the permuted order, of 16-column block 0, of block b
+  static __device__ __forceinline__ int pair_cols(int pair, int n, int g) {
+    return ((g >> 1) * (COLS / 32) + pair) * 1024 + (n & 3) * 256 + ((8 * (g & 1) + (n >> 2)) ^ 4 * (n & 3)) * 16;
+  }
+  static __device__ __forceinline__ int block_cols(int n, int g) {
+    const int u = (n & 3) >> 1;
+    return (g >> 1) * (COLS / 32) * 1024 + u * 256 + ((8 * (g & 1) + (n >> 2)) ^ 4 * u) * 16 + (n & 1) * 8;
+  }
+  static __device__ __forceinline__ int to_block(int o, int b) { return (o ^ (b & 1) * 128) + (b & 1) * 512 + (b >> 1) * 1024; }
+  static __device__ __forceinline__ Frag<f16_t> col(const char* t, int o) {   // rows four on: the other bit of the unit
+    const uint2 lo = tiles::ld_tr(t + o), hi = tiles::ld_tr(t + (o ^ 64));
+    Frag<f16_t> f;
+    f.v = __builtin_bit_cast(f16x8, tiles::u32x4{lo.x, lo.y, hi.x, hi.y});
+    return f;
+  }
+};
+template <int COLS> struct Kept<float, COLS> {
+  typedef Tile<float, COLS> L;
+  static constexpr int odd = L::odd;
+  static constexpr int bytes = L::bytes(32);
+  static __device__ __forceinline__ uint32_t at(int blk, int s, int n, int g) {
+    return (uint32_t)((16 * blk + n) * COLS + 32 * s + 8 * g);
+  }
+  static __device__ __forceinline__ int pair_cols(int pair, int n, int g) { return L::pair_cols(pair, n, g); }
+  static __device__ __forceinline__ int block_cols(int n, int g) { return L::block_cols(0, n, g); }
+  static __device__ __forceinline__ int to_block(int o, int b) { return L::to_block(o, b); }
+  static __device__ __forceinline__ Frag<float> col(const char* t, int o) { return L::col(t + o); }
 };
 
 }  // namespace bwd

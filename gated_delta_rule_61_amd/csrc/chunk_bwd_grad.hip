@@ -33,7 +33,7 @@ struct GradLds {
   typedef Tile<C, D> TD;
   // dO rows: 64 bytes of fp16 (a fragment read takes 1 KiB in a row), fp32 padded
   static constexpr int orow = sizeof(C) == 2 ? 64 : 4 * VC + 16;
-  static constexpr int VN = 0, DR = T64::bytes(VC), H = 2 * DR, DS = H + TD::bytes(VC), O = DS + TD::bytes(VC);
+  static constexpr int VN = 0, DR = Kept<C, 64>::bytes, H = 2 * DR, DS = H + Kept<C, D>::bytes, O = DS + Kept<C, D>::bytes;
   static constexpr int tiles = O + BT * orow;
   static constexpr int S1 = 0, S2 = T64::bytes(BT), S3 = 2 * S2, scores = 3 * S2;
   static constexpr int K = 0, Q = TD::bytes(BT), rows = 2 * Q;
@@ -41,32 +41,24 @@ struct GradLds {
   static constexpr int first = more(tiles, scores), second = more(tiles, rows);
 };
 
-// The copies of a block's four tiles on their way: straight to LDS (fp16, 16-byte units
-// at the places that the tiles' swizzle gives them), or through registers (fp32).
+// The copies of a block's four tiles on their way: straight to LDS, as they are (fp16), or
+// through registers (fp32).
 template <typename C, int D> struct BlockIn;
 template <int D> struct BlockIn<f16_t, D> {
   typedef GradLds<f16_t, D> L;
   static constexpr int N64 = VC * 64 * 2 / 1024, ND = VC * D * 2 / 1024;   // 1 KiB pieces of a tile
-  static constexpr int N = (2 * N64 + 2 * ND) / 8;   // of each wave
-  uint32_t from[N];   // byte of the lane's unit in its tile
-  __device__ __forceinline__ void init(int w, int lane) {
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const int p = w + 8 * i, q = p < 2 * N64 ? p % N64 : (p - 2 * N64) % ND, slot = q * 64 + lane;
-      if (p < 2 * N64) from[i] = slot / 8 * 128 + (slot % 8 ^ tiles::a_swz(slot / 8)) * 16;
-      else from[i] = slot / (D / 8) * (2 * D) + (slot % (D / 8) ^ tiles::qk_swz<D>(slot / (D / 8))) * 16;
-    }
-  }
+  uint32_t from;
+  __device__ __forceinline__ void init(int, int lane) { from = 16 * lane; }
   __device__ __forceinline__ void issue(const f16_t* vn, const f16_t* dr, const f16_t* h, const f16_t* ds, char* st, int w) {
     typedef __attribute__((address_space(3))) char lchar;
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
+    for (int i = 0; i < (2 * N64 + 2 * ND) / 8; ++i) {
       const int p = w + 8 * i;   // uniform
       const bool cols = p < 2 * N64;
-      const int q = cols ? p : p - 2 * N64, per = cols ? N64 : ND;
+      const int q = cols ? p : p - 2 * N64, per = cols ? N64 : ND, piece = q % per * 1024;
       const f16_t* src = cols ? (q < per ? vn : dr) : (q < per ? h : ds);
-      const int to = (cols ? (q < per ? L::VN : L::DR) : (q < per ? L::H : L::DS)) + q % per * 1024;
-      tiles::dma16(reinterpret_cast<const char*>(src) + from[i], (lchar*)(st + to));
+      const int to = cols ? (q < per ? L::VN : L::DR) : (q < per ? L::H : L::DS);
+      tiles::dma16(reinterpret_cast<const char*>(src) + piece + from, (lchar*)(st + to + piece));
     }
   }
   __device__ __forceinline__ void commit(char*, int) { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
@@ -93,12 +85,20 @@ template <int D> struct BlockIn<float, D> {
   }
 };
 
+// `bytes` behind a uniform address: one 32-bit register for the lane
+template <typename P>
+__device__ __forceinline__ P* ahead(P* p, uint32_t bytes) {
+  return reinterpret_cast<P*>(reinterpret_cast<uintptr_t>(p) + bytes);
+}
+
 template <typename T, int D, bool GROUPED>
 __global__ __launch_bounds__(NTHREADS) __attribute__((amdgpu_waves_per_eu(sizeof(T) == 2 && !(GROUPED && D == 128) ? 4 : 2))) void gdn_bwd_grad_kernel(ChunkBwdArgs a) {
   typedef typename ComputeOf<T>::type C;
   typedef GradLds<C, D> L;
   typedef Tile<C, D> TD;
   typedef Tile<C, 64> T64;
+  typedef Kept<C, D> KD;
+  typedef Kept<C, 64> K64;
   constexpr int VB = D / VC;          // blocks of V columns (an even number)
   constexpr int KW = D / 32;          // waves side by side over the channels
   constexpr int NT = KW / 2;          // 16-token blocks of a wave
@@ -149,15 +149,15 @@ __global__ __launch_bounds__(NTHREADS) __attribute__((amdgpu_waves_per_eu(sizeof
     // what a lane derives from its place it derives once a head (see opaque)
     const int tid = opaque(threadIdx.x), lane = tid & 63, n = lane & 15, g = lane >> 4;
     // where the lane's fragments lie in a tile
-    const int pair0 = TD::pair_cols(kw, n, g);       // channels 32 kw .., 8 rows
-    const int block0 = T64::block_cols(0, n, g);      // 16 columns, 8 rows
+    const int pair0 = KD::pair_cols(kw, n, g);       // channels 32 kw .., 8 rows
+    const int block0 = K64::block_cols(n, g);        // 16 tokens, 8 rows
     const int row0 = n * L::orow + 8 * g * (int)sizeof(C);
     // the rows of dO that this thread brings (the first 256), the token and columns whose v it meets
     const int ot = tid / 4 & 63, oc = tid % 4 * 8;
     const int vt = 16 * (w & 3) + n;
-    // 32-bit offsets of this thread's rows behind uniform addresses
-    const uint32_t o_off = (uint32_t)(ot < nrow ? ot : nrow - 1) * (uint32_t)vstride + oc;
-    const uint32_t v_off = (uint32_t)(vt < nrow ? vt : nrow - 1) * (uint32_t)vstride + 8 * g;
+    // byte offsets of this thread's rows behind uniform addresses (64 rows: below 2^32)
+    const uint32_t o_off = ((uint32_t)(ot < nrow ? ot : nrow - 1) * (uint32_t)vstride + oc) * sizeof(T);
+    const uint32_t v_off = ((uint32_t)(vt < nrow ? vt : nrow - 1) * (uint32_t)vstride + 8 * g) * sizeof(T);
     BlockIn<C, D> in;
     in.init(w, lane);
     const int j = jk * GR + r;
@@ -168,8 +168,8 @@ __global__ __launch_bounds__(NTHREADS) __attribute__((amdgpu_waves_per_eu(sizeof
     Frag<T> k_in[D / 64], q_in[D / 64];
     auto issue = [&](int jj, int vb, char* st) __attribute__((always_inline)) {
       const size_t cell = (size_t)slot * HV + jj, first = (size_t)c0 * vstride + (size_t)jj * D + VC * vb;
-      if (tid < 256) load8(o_in, reinterpret_cast<const T*>(a.dout) + first + o_off);
-      if ((vb & 1) == w >> 2) load8(v_in, reinterpret_cast<const T*>(a.f.v) + first + v_off);
+      if (tid < 256) load8(o_in, ahead(reinterpret_cast<const T*>(a.dout) + first, o_off));
+      if ((vb & 1) == w >> 2) load8(v_in, ahead(reinterpret_cast<const T*>(a.f.v) + first, v_off));
       in.issue(reinterpret_cast<const C*>(a.vn) + (cell * D + VC * vb) * BT,
                reinterpret_cast<const C*>(a.dr) + (cell * D + VC * vb) * BT,
                reinterpret_cast<const C*>(a.hs) + (cell * D + VC * vb) * D,
@@ -179,9 +179,9 @@ __global__ __launch_bounds__(NTHREADS) __attribute__((amdgpu_waves_per_eu(sizeof
 #pragma unroll
       for (int i = 0; i < D / 64; ++i) {
         const int x = tid + NTHREADS * i, t = x / (D / 8), c = x % (D / 8) * 8;
-        const uint32_t off = (uint32_t)(t < nrow ? t : nrow - 1) * (uint32_t)krow + c;
-        load8(k_in[i], kp + off);
-        load8(q_in[i], qp + off);
+        const uint32_t off = ((uint32_t)(t < nrow ? t : nrow - 1) * (uint32_t)krow + c) * sizeof(T);
+        load8(k_in[i], ahead(kp, off));
+        load8(q_in[i], ahead(qp, off));
       }
     };
     auto put_rows = [&](char* sK, char* sQ) __attribute__((always_inline)) {
@@ -240,18 +240,18 @@ __global__ __launch_bounds__(NTHREADS) __attribute__((amdgpu_waves_per_eu(sizeof
       // dv of token vt, and v . dR (a transposing read takes part of its addresses from
       // other lanes: all of them, also behind the end, where dR is 0)
       if ((vb & 1) == w >> 2) {
-        const f32x8 x = values(T64::col(st + L::DR + T64::to_block(o_block, w & 3))), y = values(v_in);
+        const f32x8 x = values(K64::col(st + L::DR, K64::to_block(o_block, w & 3))), y = values(v_in);
 #pragma unroll
         for (int e = 0; e < 8; ++e) vdr = fmaf(x[e], y[e], vdr);
-        if (vt < nrow) store_io8(dvp + VC * vb + v_off, x * (sG[3 * BT + vt] * inv));
+        if (vt < nrow) store_io8(ahead(dvp + VC * vb, v_off), x * (sG[3 * BT + vt] * inv));
       }
       if (vb + 1 < VB) issue(j, vb + 1, next);
       else if (APART && r + 1 < GR) issue(j + 1, 0, next);   // `next` is the first stage
       Frag<C> hf[2], df[2];
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        hf[h] = TD::col(st + L::H + o_pair + h * TD::odd);
-        df[h] = TD::col(st + L::DS + o_pair + h * TD::odd);
+        hf[h] = KD::col(st + L::H + h * KD::odd, o_pair);
+        df[h] = KD::col(st + L::DS + h * KD::odd, o_pair);
       }
       // each pair of waves with the same channels takes one half of <h, dh'>
       if (th < 2) {
@@ -263,8 +263,8 @@ __global__ __launch_bounds__(NTHREADS) __attribute__((amdgpu_waves_per_eu(sizeof
       for (int t = 0; t < NT; ++t) {
         const int tb = tb0 + t;
         const Frag<C> of = T64::row(st + L::O + 16 * tb * L::orow + o_row);
-        const Frag<C> rf = T64::col(st + L::DR + T64::to_block(o_block, tb));
-        const Frag<C> vf = T64::col(st + L::VN + T64::to_block(o_block, tb));
+        const Frag<C> rf = K64::col(st + L::DR, K64::to_block(o_block, tb));
+        const Frag<C> vf = K64::col(st + L::VN, K64::to_block(o_block, tb));
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           dq[h][t] = mma(hf[h], of, dq[h][t]);
@@ -273,15 +273,16 @@ __global__ __launch_bounds__(NTHREADS) __attribute__((amdgpu_waves_per_eu(sizeof
         }
       }
       // scores, transposed: blocks `w` (and 8 + w % 2, dealt to four waves) of both
-      const Frag<C> vf = T64::col(st + L::VN + T64::to_block(o_block, sbw));
+      const Frag<C> vf = K64::col(st + L::VN, K64::to_block(o_block, sbw));
       M[0] = mma(vf, T64::row(st + L::O + 16 * tbw * L::orow + o_row), M[0]);
-      M[1] = mma(vf, T64::col(st + L::DR + T64::to_block(o_block, tbw)), M[1]);
+      M[1] = mma(vf, K64::col(st + L::DR, K64::to_block(o_block, tbw)), M[1]);
       if (w < 4) {
-        const Frag<C> vl = T64::col(st + L::VN + T64::to_block(o_block, 2 + (w & 1)));
+        const Frag<C> vl = K64::col(st + L::VN, K64::to_block(o_block, 2 + (w & 1)));
         M[2] = mma(vl, w < 2 ? T64::row(st + L::O + 48 * L::orow + o_row)
-                             : T64::col(st + L::DR + T64::to_block(o_block, 3)), M[2]);
+                             : K64::col(st + L::DR, K64::to_block(o_block, 3)), M[2]);
       }
     };
+#pragma unroll 1
     for (int vb = 0; vb < VB; vb += 2) {
       step(vb, st0, st1);
       step(vb + 1, st1, st0);
@@ -322,18 +323,15 @@ __global__ __launch_bounds__(NTHREADS) __attribute__((amdgpu_waves_per_eu(sizeof
       tiles::lds_barrier();
     }
 
-    const int o_pair = opaque(pair0), o_block = opaque(block0);
+    const int o_pair = opaque(TD::pair_cols(kw, n, g)), o_block = opaque(T64::block_cols(0, n, g));
     const int o_score = opaque(T64::off(n, 8 * g)), o_chan = opaque(TD::off(n, 32 * kw + 8 * g));
     // row factors, the dot product with k of what crosses the chunk's end
-    Frag<C> kf[NT], qf[NT];
     float wi[NT];
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
       const int tok = 16 * (tb0 + t) + n;
-      kf[t] = TD::row(sK + TD::to_rows(o_chan, tb0 + t));
-      qf[t] = TD::row(sQ + TD::to_rows(o_chan, tb0 + t));
       const float ex = sG[BT + tok], ey = sG[2 * BT + tok];
-      const f32x8 k8 = values(kf[t]);
+      const f32x8 k8 = values(TD::row(sK + TD::to_rows(o_chan, tb0 + t)));
       wi[t] = 0.f;
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
@@ -376,11 +374,12 @@ __global__ __launch_bounds__(NTHREADS) __attribute__((amdgpu_waves_per_eu(sizeof
         }
       }
     }
-    // dots over the wave's channels
+    // dots over the wave's channels (k and q read again: registers)
+    const int o_again = opaque(o_chan);
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
-      const int tok = 16 * (tb0 + t) + n;
-      const f32x8 k8 = values(kf[t]), q8 = values(qf[t]);
+      const int tok = 16 * (tb0 + t) + n, at = TD::to_rows(o_again, tb0 + t);
+      const f32x8 k8 = values(TD::row(sK + at)), q8 = values(TD::row(sQ + at));
       float d[4] = {0.f, 0.f, 0.f, wi[t]};   // q . dq, k . E, k . W, and the part of k . W that crosses the end
 #pragma unroll
       for (int h = 0; h < 2; ++h)

@@ -16,8 +16,8 @@
 // dO^T come from the same tiles by transposing reads.  (fp32 tiles fit once: the
 // movers then write between two barriers.)
 //
-// h and dh' leave as [V][K] rows, Vn and dR transposed ([V][64]): what a lane's
-// accumulators hold in order.
+// h and dh' leave as [V][K], Vn and dR transposed ([V][64]): what a lane's
+// accumulators hold in order, a wave's stores 1 KiB in a row.
 
 #include "chunk_bwd.h"
 #include "chunk_common.h"
@@ -224,8 +224,9 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
   }
   // state and column stores of a chunk
   const size_t chunk_state = (size_t)HV * D * D, chunk_cols = (size_t)HV * D * BT;
-  C* const st_out = reinterpret_cast<C*>(back ? a.ds : a.hs) + ((size_t)j * D + vrow) * D;
-  C* const col_out = reinterpret_cast<C*>(back ? a.dr : a.vn) + ((size_t)j * D + vrow) * BT;
+  C* const st_out = reinterpret_cast<C*>(back ? a.ds : a.hs) + (size_t)j * D * D;
+  C* const col_out = reinterpret_cast<C*>(back ? a.dr : a.vn) + (size_t)j * D * BT;
+  const int vblk = v0 / 16 + w;
 
   // Keeps the order of what is issued around it: left to itself the compiler reads each
   // fragment right before its product and waits out the LDS latency every time.  (fp32
@@ -296,7 +297,7 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
 #pragma unroll
       for (int s = 0; s < KS; ++s) {
         join(Sh[s], S[2 * s], S[2 * s + 1]);
-        store8(st_out + slot * chunk_state + 32 * s + 8 * g, Sh[s]);
+        store8(st_out + slot * chunk_state + Kept<C, D>::at(vblk, s, n, g), Sh[s]);
       }
       fence();
       // ---- P^T dO and X = K S; meanwhile the rows of A (A^T), then Q^T or K^T
@@ -348,7 +349,7 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
 #pragma unroll
         for (int p = 0; p < 2; ++p) {
           join(Zf[p], Z[2 * p], Z[2 * p + 1]);
-          store8(col_out + slot * chunk_cols + 32 * p + 8 * g, Zf[p]);
+          store8(col_out + slot * chunk_cols + Kept<C, 64>::at(vblk, p, n, g), Zf[p]);
           join(Zf[p], Z[2 * p] * ey[2 * p], Z[2 * p + 1] * ey[2 * p + 1]);
         }
       } else {
@@ -384,7 +385,7 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
 #pragma unroll
         for (int p = 0; p < 2; ++p) {
           join(Zf[p], Z[2 * p], Z[2 * p + 1]);
-          store8(col_out + slot * chunk_cols + 32 * p + 8 * g, Zf[p]);
+          store8(col_out + slot * chunk_cols + Kept<C, 64>::at(vblk, p, n, g), Zf[p]);
           join(Zf[p], Z[2 * p] * (-bz[2 * p] * ex[2 * p]), Z[2 * p + 1] * (-bz[2 * p + 1] * ex[2 * p + 1]));
         }
       }

@@ -437,6 +437,8 @@ int gdn_chunk_bwd(const void* q, const void* k, const void* v, const float* g, c
   const void* ptrs[] = {dht, dq, dk, dv, dg, dbeta, dh0};
   for (const void* p : ptrs)
     if (p && !aligned16(p)) return fail(GDN_ERR_INVALID_ARGUMENT, "tensor pointers must be 16-byte aligned");
+  // 64 rows of a tensor are addressed with 32-bit byte offsets
+  if ((long long)HV * V >= (1 << 23)) return fail(GDN_ERR_UNSUPPORTED, "HV * V must stay below 2^23");
   const bool bf16 = dtype == GDN_DTYPE_BF16;
   const BwdWorkspace L = bwd_workspace_layout(B, T, HV, K, V, P.N, cu_seqlens != nullptr, bf16);
   if (!workspace || workspace_bytes < L.total)
