@@ -18,7 +18,7 @@
 //               dg = the sums of dG from each row to the chunk's end
 //
 // Every array that holds a gradient is kept times a power of two, one for each
-// (sequence, v-head), that brings the largest of its dO and dht to 2 .. 4: with
+// (sequence, key head), that brings the largest of its dO and dht to 2 .. 4: with
 // bf16 io the operands of the products are fp16 (2^-11 where bf16 has 2^-8), and
 // the gradients of a mean over many tokens lie far below fp16's normal numbers.
 #pragma once
@@ -34,7 +34,7 @@ constexpr int BT = 64;
 using tiles::perm_row;
 
 // The power of two that brings `amax` to 2 .. 4 (and its inverse); NaN where it is
-// not finite, which then every gradient of the (sequence, head) becomes.
+// not finite, which then every gradient of the (sequence, key head) becomes.
 __device__ __forceinline__ float grad_scale(uint32_t amax_bits, float& inverse) {
   const int e = (int)(amax_bits >> 23);   // biased exponent; the sign is clear
   int up = amax_bits == 0 ? 0 : 128 - e;  // 2^up amax in [2, 4)
@@ -53,7 +53,8 @@ __device__ __forceinline__ f32x8 both(const f32x4& a, const f32x4& b) {
 // Hides where a value comes from: offsets made from it are made where they are used, a
 // cheap operation each, instead of once in front of all loops, which takes more registers
 // than there are.
-__device__ __forceinline__ int opaque(int x) {
+template <typename I>
+__device__ __forceinline__ I opaque(I x) {
   asm volatile("" : "+v"(x));
   return x;
 }
@@ -84,6 +85,18 @@ __device__ __forceinline__ Frag<float> widen(const Frag<float>& a, float s) {
   return r;
 }
 __device__ __forceinline__ Frag<float> widen(const Frag<float>& a) { return a; }
+
+// ... times a factor (fp16: one more rounding of each)
+__device__ __forceinline__ Frag<f16_t> times(const Frag<f16_t>& a, float s) {
+  Frag<f16_t> r;
+  r.v = a.v * (_Float16)s;
+  return r;
+}
+__device__ __forceinline__ Frag<float> times(const Frag<float>& a, float s) {
+  Frag<float> r;
+  r.v = a.v * s;
+  return r;
+}
 
 __device__ __forceinline__ f32x8 values(const Frag<f16_t>& a) { return __builtin_convertvector(a.v, f32x8); }
 __device__ __forceinline__ f32x8 values(const Frag<float>& a) { return a.v; }

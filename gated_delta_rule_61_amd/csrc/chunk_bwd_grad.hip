@@ -3,7 +3,9 @@
 // gradients, Vn and dR that the two scans left.
 //
 // A work-group is one (chunk, key head): it takes the v-heads that share the key
-// head in turn and adds their dq and dk in registers, in order.  Products run
+// head in turn, in order, and their dq and dk add up where they are made: the rows
+// of dO, dR and Vn enter the products times their tokens' gate factors, so that the
+// accumulators need none (a head's share of q . dq and k . dk is what they grew by).  Products run
 // transposed ([K channels] x [tokens]), so that a lane ends with 8 consecutive
 // channels of a token: 16-byte stores, and the dot products with q and k (which
 // make dg and dbeta) in registers.  Each of the eight waves has 32 channels of some
@@ -41,6 +43,16 @@ struct GradLds {
   static constexpr int first = more(tiles, scores), second = more(tiles, rows);
 };
 
+// `bytes` behind a uniform address: one 32-bit register for the lane
+template <typename T>
+__device__ __forceinline__ const T* ahead(const T* p, uint32_t bytes) {
+  return reinterpret_cast<const T*>(reinterpret_cast<const char*>(p) + bytes);
+}
+template <typename T>
+__device__ __forceinline__ T* ahead(T* p, uint32_t bytes) {
+  return reinterpret_cast<T*>(reinterpret_cast<char*>(p) + bytes);
+}
+
 // The copies of a block's four tiles on their way: straight to LDS, as they are (fp16), or
 // through registers (fp32).
 template <typename C, int D> struct BlockIn;
@@ -51,6 +63,7 @@ template <int D> struct BlockIn<f16_t, D> {
   __device__ __forceinline__ void init(int, int lane) { from = 16 * lane; }
   __device__ __forceinline__ void issue(const f16_t* vn, const f16_t* dr, const f16_t* h, const f16_t* ds, char* st, int w) {
     typedef __attribute__((address_space(3))) char lchar;
+    const uint32_t at = opaque(from);
 #pragma unroll
     for (int i = 0; i < (2 * N64 + 2 * ND) / 8; ++i) {
       const int p = w + 8 * i;   // uniform
@@ -58,7 +71,7 @@ template <int D> struct BlockIn<f16_t, D> {
       const int q = cols ? p : p - 2 * N64, per = cols ? N64 : ND, piece = q % per * 1024;
       const f16_t* src = cols ? (q < per ? vn : dr) : (q < per ? h : ds);
       const int to = cols ? (q < per ? L::VN : L::DR) : (q < per ? L::H : L::DS);
-      tiles::dma16(reinterpret_cast<const char*>(src) + piece + from, (lchar*)(st + to + piece));
+      tiles::dma16(ahead(reinterpret_cast<const char*>(src) + piece, at), (lchar*)(st + to + piece));
     }
   }
   __device__ __forceinline__ void commit(char*, int) { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
@@ -85,14 +98,9 @@ template <int D> struct BlockIn<float, D> {
   }
 };
 
-// `bytes` behind a uniform address: one 32-bit register for the lane
-template <typename P>
-__device__ __forceinline__ P* ahead(P* p, uint32_t bytes) {
-  return reinterpret_cast<P*>(reinterpret_cast<uintptr_t>(p) + bytes);
-}
-
-template <typename T, int D, bool GROUPED>
-__global__ __launch_bounds__(NTHREADS) __attribute__((amdgpu_waves_per_eu(sizeof(T) == 2 && !(GROUPED && D == 128) ? 4 : 2))) void gdn_bwd_grad_kernel(ChunkBwdArgs a) {
+template <typename T, int D>
+__global__ __launch_bounds__(NTHREADS) __attribute__((amdgpu_waves_per_eu(sizeof(T) == 2 ? 4 : 2))) void gdn_bwd_grad_kernel(
+    ChunkBwdArgs a) {
   typedef typename ComputeOf<T>::type C;
   typedef GradLds<C, D> L;
   typedef Tile<C, D> TD;
@@ -102,19 +110,14 @@ __global__ __launch_bounds__(NTHREADS) __attribute__((amdgpu_waves_per_eu(sizeof
   constexpr int VB = D / VC;          // blocks of V columns (an even number)
   constexpr int KW = D / 32;          // waves side by side over the channels
   constexpr int NT = KW / 2;          // 16-token blocks of a wave
-  // Several heads a work-group (one a CU, for its registers): the scores and k, q have room of
-  // their own, so k and q come once and the next head's first block while this one's chunk
-  // products run.
-  constexpr bool APART = GROUPED && sizeof(C) == 2;
-  __shared__ __attribute__((aligned(16))) char st0[APART ? L::tiles : L::first], st1[APART ? L::tiles : L::second];
-  __shared__ __attribute__((aligned(16))) char own_scores[APART ? L::scores : 16], own_rows[APART ? L::rows : 16];
+  __shared__ __attribute__((aligned(16))) char st0[L::first], st1[L::second];
   // G, e^G, e^{G_last - G}, beta of the tokens; dot products, one row for 32 channels;
   // v . dR; <h, dh'> of each wave
   __shared__ __attribute__((aligned(16))) float sG[4 * BT], red[16 * BT], sVdr[2 * BT], sHd[8];
 
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int kw = w % KW, th = w / KW, tb0 = th * NT;   // the wave's channels 32 kw .. and token blocks
-  const int Hk = a.f.Hk, HV = a.f.HV, GR = GROUPED ? HV / Hk : 1;
+  const int Hk = a.f.Hk, HV = a.f.HV, GR = HV / Hk;
   const int NTC = (a.f.T + BT - 1) / BT;
   int slot, jk, c0, nrow;
   if (!intra::slot_of_block(a.nslots, Hk, slot, jk)) return;
@@ -135,19 +138,25 @@ __global__ __launch_bounds__(NTHREADS) __attribute__((amdgpu_waves_per_eu(sizeof
   const T* const qp = reinterpret_cast<const T*>(a.f.q) + (size_t)c0 * krow + (size_t)jk * D;
   const T* const kp = reinterpret_cast<const T*>(a.f.k) + (size_t)c0 * krow + (size_t)jk * D;
 
-  f32x4 dq_sum[GROUPED ? 2 : 1][GROUPED ? NT : 1], dk_sum[GROUPED ? 2 : 1][GROUPED ? NT : 1];
-  if constexpr (GROUPED) {
+  // sums over the heads: dq, and dk; what of q . dq and k . dk (the lane's channels) the heads
+  // before made up
+  f32x4 dq[2][NT], dk[2][NT];
+  float q_dq[NT], k_dk[NT];
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
+  for (int t = 0; t < NT; ++t) {
+    q_dq[t] = k_dk[t] = 0.f;
 #pragma unroll
-      for (int t = 0; t < NT; ++t) dq_sum[h][t] = dk_sum[h][t] = zero4();
+    for (int h = 0; h < 2; ++h) dq[h][t] = dk[h][t] = zero4();
   }
+  // every gradient of the key head's v-heads is kept times one power of two
+  float inv = 1.f, gs = 1.f;
+  if (a.amax) gs = grad_scale(a.amax[(size_t)ns * Hk + jk], inv);
   // the wave's block of the scores: lower blocks (tb, sb) in the order of tix
   const int tbw = w >= 6 ? 3 : w >= 3 ? 2 : w >= 1 ? 1 : 0, sbw = w - tbw * (tbw + 1) / 2;
   Frag<T> o_in, v_in;   // dO and v of the block on its way
   for (int r = 0; r < GR; ++r) {
     // what a lane derives from its place it derives once a head (see opaque)
-    const int tid = opaque(threadIdx.x), lane = tid & 63, n = lane & 15, g = lane >> 4;
+    const int tid = opaque((int)threadIdx.x), lane = tid & 63, n = lane & 15, g = lane >> 4;
     // where the lane's fragments lie in a tile
     const int pair0 = KD::pair_cols(kw, n, g);       // channels 32 kw .., 8 rows
     const int block0 = K64::block_cols(n, g);        // 16 tokens, 8 rows
@@ -161,21 +170,19 @@ __global__ __launch_bounds__(NTHREADS) __attribute__((amdgpu_waves_per_eu(sizeof
     BlockIn<C, D> in;
     in.init(w, lane);
     const int j = jk * GR + r;
-    float inv = 1.f, gs = 1.f;
-    if (a.amax) gs = grad_scale(a.amax[(size_t)ns * HV + j], inv);
     T* const dvp = reinterpret_cast<T*>(a.dv) + (size_t)c0 * vstride + (size_t)j * D;
 
     Frag<T> k_in[D / 64], q_in[D / 64];
-    auto issue = [&](int jj, int vb, char* st) __attribute__((always_inline)) {
-      const size_t cell = (size_t)slot * HV + jj, first = (size_t)c0 * vstride + (size_t)jj * D + VC * vb;
-      if (tid < 256) load8(o_in, ahead(reinterpret_cast<const T*>(a.dout) + first, o_off));
-      if ((vb & 1) == w >> 2) load8(v_in, ahead(reinterpret_cast<const T*>(a.f.v) + first, v_off));
+    auto issue = [&](int vb, char* st) __attribute__((always_inline)) {
+      const size_t cell = (size_t)slot * HV + j, first = (size_t)c0 * vstride + (size_t)j * D + VC * vb;
+      if (tid < 256) load8(o_in, ahead(reinterpret_cast<const T*>(a.dout) + first, opaque(o_off)));
+      if ((vb & 1) == w >> 2) load8(v_in, ahead(reinterpret_cast<const T*>(a.f.v) + first, opaque(v_off)));
       in.issue(reinterpret_cast<const C*>(a.vn) + (cell * D + VC * vb) * BT,
                reinterpret_cast<const C*>(a.dr) + (cell * D + VC * vb) * BT,
                reinterpret_cast<const C*>(a.hs) + (cell * D + VC * vb) * D,
                reinterpret_cast<const C*>(a.ds) + (cell * D + VC * vb) * D, st, w);
     };
-    auto fetch_rows = [&]() __attribute__((always_inline)) {   // k and q for the products within the chunk
+    auto fetch_rows = [&](int tid) __attribute__((always_inline)) {   // k and q for the products within the chunk
 #pragma unroll
       for (int i = 0; i < D / 64; ++i) {
         const int x = tid + NTHREADS * i, t = x / (D / 8), c = x % (D / 8) * 8;
@@ -184,7 +191,7 @@ __global__ __launch_bounds__(NTHREADS) __attribute__((amdgpu_waves_per_eu(sizeof
         load8(q_in[i], ahead(qp, off));
       }
     };
-    auto put_rows = [&](char* sK, char* sQ) __attribute__((always_inline)) {
+    auto put_rows = [&](int tid, char* sK, char* sQ) __attribute__((always_inline)) {
 #pragma unroll
       for (int i = 0; i < D / 64; ++i) {
         const int x = tid + NTHREADS * i, t = x / (D / 8), c = x % (D / 8) * 8;
@@ -206,11 +213,7 @@ __global__ __launch_bounds__(NTHREADS) __attribute__((amdgpu_waves_per_eu(sizeof
         else *reinterpret_cast<f32x8*>(st + L::O + ot * L::orow + 4 * oc) = f.v;
       }
     };
-    if (!APART || r == 0) issue(j, 0, st0);
-    if (APART && r == 0) {
-      fetch_rows();
-      put_rows(own_rows + L::K, own_rows + L::Q);
-    }
+    issue(0, st0);
     // the gates: G again from its terms, beta
     if (w == 7) {
       const int tl = lane < nrow ? lane : nrow - 1;
@@ -224,11 +227,11 @@ __global__ __launch_bounds__(NTHREADS) __attribute__((amdgpu_waves_per_eu(sizeof
       sG[3 * BT + lane] = lane < nrow ? b : 0.f;
     }
 
-    f32x4 dq[2][NT], E[2][NT], W[2][NT], M[3];
+    f32x4 E[2][NT], M[3];
 #pragma unroll
     for (int h = 0; h < 2; ++h)
 #pragma unroll
-      for (int t = 0; t < NT; ++t) dq[h][t] = E[h][t] = W[h][t] = zero4();
+      for (int t = 0; t < NT; ++t) E[h][t] = zero4();
 #pragma unroll
     for (int i = 0; i < 3; ++i) M[i] = zero4();
     float hd = 0.f;        // <h, dh'>, the lane's elements
@@ -243,10 +246,9 @@ __global__ __launch_bounds__(NTHREADS) __attribute__((amdgpu_waves_per_eu(sizeof
         const f32x8 x = values(K64::col(st + L::DR, K64::to_block(o_block, w & 3))), y = values(v_in);
 #pragma unroll
         for (int e = 0; e < 8; ++e) vdr = fmaf(x[e], y[e], vdr);
-        if (vt < nrow) store_io8(ahead(dvp + VC * vb, v_off), x * (sG[3 * BT + vt] * inv));
+        if (vt < nrow) store_io8(ahead(dvp + VC * vb, opaque(v_off)), x * (sG[3 * BT + vt] * inv));
       }
-      if (vb + 1 < VB) issue(j, vb + 1, next);
-      else if (APART && r + 1 < GR) issue(j + 1, 0, next);   // `next` is the first stage
+      if (vb + 1 < VB) issue(vb + 1, next);
       Frag<C> hf[2], df[2];
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
@@ -262,14 +264,16 @@ __global__ __launch_bounds__(NTHREADS) __attribute__((amdgpu_waves_per_eu(sizeof
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
         const int tb = tb0 + t;
-        const Frag<C> of = T64::row(st + L::O + 16 * tb * L::orow + o_row);
-        const Frag<C> rf = K64::col(st + L::DR, K64::to_block(o_block, tb));
-        const Frag<C> vf = K64::col(st + L::VN, K64::to_block(o_block, tb));
+        // with their tokens' factors: the accumulators go on from head to head
+        const float ex = sG[BT + 16 * tb + n], ey = sG[2 * BT + 16 * tb + n];
+        const Frag<C> of = times(T64::row(st + L::O + 16 * tb * L::orow + o_row), a.f.scale * ex);
+        const Frag<C> rf = times(K64::col(st + L::DR, K64::to_block(o_block, tb)), -ex);
+        const Frag<C> vf = times(K64::col(st + L::VN, K64::to_block(o_block, tb)), ey);
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           dq[h][t] = mma(hf[h], of, dq[h][t]);
           E[h][t] = mma(hf[h], rf, E[h][t]);
-          W[h][t] = mma(df[h], vf, W[h][t]);
+          dk[h][t] = mma(df[h], vf, dk[h][t]);
         }
       }
       // scores, transposed: blocks `w` (and 8 + w % 2, dealt to four waves) of both
@@ -288,205 +292,180 @@ __global__ __launch_bounds__(NTHREADS) __attribute__((amdgpu_waves_per_eu(sizeof
       step(vb + 1, st1, st0);
     }
 
-    if constexpr (!APART) fetch_rows();
-    // the scores, in the bytes of the first stage, whose last readers have passed a barrier
-    char* const scores = APART ? own_scores : st0;
-    char* const S1 = scores + L::S1;    // scale dO Vn^T o Gamma, s <= t
-    char* const S2 = scores + L::S2;    // -dR Vn^T o Gamma, s < t
-    char* const S3 = scores + L::S3;    // beta_t times that
-    auto put_score = [&](const f32x4& m, bool second, int tb, int sb) __attribute__((always_inline)) {
-      const int t = 16 * tb + n, s = 16 * sb + 4 * g;
-      const float Gt = sG[t], f = second ? -1.f : a.f.scale;
-      const f32x4 Gs = *reinterpret_cast<const f32x4*>(sG + s);
-      f32x4 x;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const bool keep = second ? s + e < t : s + e <= t;
-        x[e] = keep ? f * m[e] * __expf(Gt - Gs[e]) : 0.f;
-      }
-      T64::put4(second ? S2 : S1, t, s, x);
-      if (second) T64::put4(S3, t, s, x * sG[3 * BT + t]);
-    };
-    put_score(M[0], false, tbw, sbw);
-    put_score(M[1], true, tbw, sbw);
-    if (w < 4) put_score(M[2], w >= 2, 3, 2 + (w & 1));
-    // the blocks above the diagonal that a 32-wide slab takes in
-    if (w < 6) {
-      char* const tile = w / 2 == 0 ? S1 : w / 2 == 1 ? S2 : S3;
-      T64::put4(tile, 32 * (w & 1) + n, 32 * (w & 1) + 16 + 4 * g, zero4());
-    }
-    tiles::lds_barrier();
-    char* const sK = (APART ? own_rows : st1) + L::K;
-    char* const sQ = (APART ? own_rows : st1) + L::Q;
-    if constexpr (!APART) {
-      put_rows(sK, sQ);
-      tiles::lds_barrier();
-    }
-
-    const int o_pair = opaque(TD::pair_cols(kw, n, g)), o_block = opaque(T64::block_cols(0, n, g));
-    const int o_score = opaque(T64::off(n, 8 * g)), o_chan = opaque(TD::off(n, 32 * kw + 8 * g));
-    // row factors, the dot product with k of what crosses the chunk's end
-    float wi[NT];
-#pragma unroll
-    for (int t = 0; t < NT; ++t) {
-      const int tok = 16 * (tb0 + t) + n;
-      const float ex = sG[BT + tok], ey = sG[2 * BT + tok];
-      const f32x8 k8 = values(TD::row(sK + TD::to_rows(o_chan, tb0 + t)));
-      wi[t] = 0.f;
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        dq[h][t] = dq[h][t] * (a.f.scale * ex);
-        E[h][t] = E[h][t] * -ex;
-        W[h][t] = W[h][t] * ey;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) wi[t] = fmaf(k8[4 * h + e], W[h][t][e], wi[t]);
-      }
-    }
-    // products within the chunk: only slabs that meet entries below the diagonal
-#pragma unroll
-    for (int p = 0; p < 2; ++p) {
-      Frag<C> ka[2], qa[2];
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        ka[h] = TD::col(sK + o_pair + 32 * p * TD::pitch + h * TD::odd);
-        qa[h] = TD::col(sQ + o_pair + 32 * p * TD::pitch + h * TD::odd);
-      }
-#pragma unroll
-      for (int t = 0; t < NT; ++t) {
-        const int tb = tb0 + t;
-        if (2 * p <= tb) {   // s of the slab up to t
-          const int at = T64::to_rows(o_score, tb, p);
-          const Frag<C> s1 = T64::row(S1 + at), s2 = T64::row(S2 + at);
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            dq[h][t] = mma(ka[h], s1, dq[h][t]);
-            E[h][t] = mma(ka[h], s2, E[h][t]);
-          }
-        }
-        if (2 * p + 1 >= tb) {   // t of the slab from s = 16 tb + n on
-          const int at = T64::to_block(o_block, tb) + 32 * p * T64::pitch;
-          const Frag<C> s1 = T64::col(S1 + at), s3 = T64::col(S3 + at);
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            W[h][t] = mma(qa[h], s1, W[h][t]);
-            W[h][t] = mma(ka[h], s3, W[h][t]);
-          }
-        }
-      }
-    }
-    // dots over the wave's channels (k and q read again: registers)
-    const int o_again = opaque(o_chan);
-#pragma unroll
-    for (int t = 0; t < NT; ++t) {
-      const int tok = 16 * (tb0 + t) + n, at = TD::to_rows(o_again, tb0 + t);
-      const f32x8 k8 = values(TD::row(sK + at)), q8 = values(TD::row(sQ + at));
-      float d[4] = {0.f, 0.f, 0.f, wi[t]};   // q . dq, k . E, k . W, and the part of k . W that crosses the end
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
+    {
+      // the lane's place once more: what is derived from it stays out of the blocks' registers
+      const int tid = opaque((int)threadIdx.x), lane = tid & 63, n = lane & 15, g = lane >> 4;
+      const int vt = 16 * (w & 3) + n;
+      fetch_rows(tid);
+      // the scores, in the bytes of the first stage, whose last readers have passed a barrier
+      char* const S1 = st0 + L::S1;    // scale dO Vn^T o Gamma, s <= t
+      char* const S2 = st0 + L::S2;    // -dR Vn^T o Gamma, s < t
+      char* const S3 = st0 + L::S3;    // beta_t times that
+      auto put_score = [&](const f32x4& m, bool second, int tb, int sb) __attribute__((always_inline)) {
+        const int t = 16 * tb + n, s = 16 * sb + 4 * g;
+        const float Gt = sG[t], f = second ? -1.f : a.f.scale;
+        const f32x4 Gs = *reinterpret_cast<const f32x4*>(sG + s);
+        f32x4 x;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          d[0] = fmaf(q8[4 * h + e], dq[h][t][e], d[0]);
-          d[1] = fmaf(k8[4 * h + e], E[h][t][e], d[1]);
-          d[2] = fmaf(k8[4 * h + e], W[h][t][e], d[2]);
+          const bool keep = second ? s + e < t : s + e <= t;
+          x[e] = keep ? f * m[e] * __expf(Gt - Gs[e]) : 0.f;
+        }
+        T64::put4(second ? S2 : S1, t, s, x);
+        if (second) T64::put4(S3, t, s, x * sG[3 * BT + t]);
+      };
+      put_score(M[0], false, tbw, sbw);
+      put_score(M[1], true, tbw, sbw);
+      if (w < 4) put_score(M[2], w >= 2, 3, 2 + (w & 1));
+      // the blocks above the diagonal that a 32-wide slab takes in
+      if (w < 6) {
+        char* const tile = w / 2 == 0 ? S1 : w / 2 == 1 ? S2 : S3;
+        T64::put4(tile, 32 * (w & 1) + n, 32 * (w & 1) + 16 + 4 * g, zero4());
+      }
+      tiles::lds_barrier();
+      char* const sK = st1 + L::K;
+      char* const sQ = st1 + L::Q;
+      put_rows(tid, sK, sQ);
+      tiles::lds_barrier();
+
+      const int o_pair = opaque(TD::pair_cols(kw, n, g)), o_block = opaque(T64::block_cols(0, n, g));
+      const int o_score = opaque(T64::off(n, 8 * g)), o_chan = opaque(TD::off(n, 32 * kw + 8 * g));
+      // the dot product with k of what crosses the chunk's end
+      float wi[NT];
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        const f32x8 k8 = values(TD::row(sK + TD::to_rows(o_chan, tb0 + t)));
+        wi[t] = -k_dk[t];
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) wi[t] = fmaf(k8[4 * h + e], dk[h][t][e], wi[t]);
+      }
+      // products within the chunk: only slabs that meet entries below the diagonal
+#pragma unroll
+      for (int p = 0; p < 2; ++p) {
+        Frag<C> ka[2], qa[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          ka[h] = TD::col(sK + o_pair + 32 * p * TD::pitch + h * TD::odd);
+          qa[h] = TD::col(sQ + o_pair + 32 * p * TD::pitch + h * TD::odd);
         }
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        d[i] += __shfl_xor(d[i], 16, 64);
-        d[i] += __shfl_xor(d[i], 32, 64);
-        if (g == 0) red[(i * 4 + kw) * BT + tok] = d[i];
-      }
-      // dk = beta E + W
-      const float b = sG[3 * BT + tok];
-      f32x4 x[2], y[2];
+        for (int t = 0; t < NT; ++t) {
+          const int tb = tb0 + t;
+          if (2 * p <= tb) {   // s of the slab up to t
+            const int at = T64::to_rows(o_score, tb, p);
+            const Frag<C> s1 = T64::row(S1 + at), s2 = T64::row(S2 + at);
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        x[h] = dq[h][t] * inv;
-        y[h] = (E[h][t] * b + W[h][t]) * inv;
-        if constexpr (GROUPED) {
-          dq_sum[h][t] += x[h];
-          dk_sum[h][t] += y[h];
+            for (int h = 0; h < 2; ++h) {
+              dq[h][t] = mma(ka[h], s1, dq[h][t]);
+              E[h][t] = mma(ka[h], s2, E[h][t]);
+            }
+          }
+          if (2 * p + 1 >= tb) {   // t of the slab from s = 16 tb + n on
+            const int at = T64::to_block(o_block, tb) + 32 * p * T64::pitch;
+            const Frag<C> s1 = T64::col(S1 + at), s3 = T64::col(S3 + at);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              dk[h][t] = mma(qa[h], s1, dk[h][t]);
+              dk[h][t] = mma(ka[h], s3, dk[h][t]);
+            }
+          }
         }
       }
-      if constexpr (!GROUPED) {
-        if (tok < nrow) {
-          const size_t at = (size_t)(c0 + tok) * krow + (size_t)jk * D + 32 * kw + 8 * g;
-          store_io8(reinterpret_cast<T*>(a.dq) + at, both(x[0], x[1]));
-          store_io8(reinterpret_cast<T*>(a.dk) + at, both(y[0], y[1]));
+      // dots over the wave's channels (k and q read again: registers)
+      const int o_again = opaque(o_chan);
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        const int tok = 16 * (tb0 + t) + n, at = TD::to_rows(o_again, tb0 + t);
+        const f32x8 k8 = values(TD::row(sK + at)), q8 = values(TD::row(sQ + at));
+        // q . dq, k . E, k . W and the part of k . W that crosses the end, of this head
+        float d[4] = {-q_dq[t], 0.f, -k_dk[t], wi[t]};
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            d[0] = fmaf(q8[4 * h + e], dq[h][t][e], d[0]);
+            d[1] = fmaf(k8[4 * h + e], E[h][t][e], d[1]);
+            d[2] = fmaf(k8[4 * h + e], dk[h][t][e], d[2]);
+          }
+        // dk = beta E + W
+        const float b = sG[3 * BT + tok];
+        q_dq[t] += d[0];
+        k_dk[t] += fmaf(b, d[1], d[2]);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) dk[h][t] += E[h][t] * b;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          d[i] += __shfl_xor(d[i], 16, 64);
+          d[i] += __shfl_xor(d[i], 32, 64);
+          if (g == 0) red[(i * 4 + kw) * BT + tok] = d[i];
         }
       }
-    }
-    vdr += __shfl_xor(vdr, 16, 64);
-    vdr += __shfl_xor(vdr, 32, 64);
-    if (g == 0) sVdr[(w >> 2) * BT + vt] = vdr;
+      vdr += __shfl_xor(vdr, 16, 64);
+      vdr += __shfl_xor(vdr, 32, 64);
+      if (g == 0) sVdr[(w >> 2) * BT + vt] = vdr;
 #pragma unroll
-    for (int off = 1; off < 64; off <<= 1) hd += __shfl_xor(hd, off, 64);
-    if (lane == 0) sHd[w] = hd;
-    tiles::lds_barrier();
-    if (w == 0) {
-      float d[4];
+      for (int off = 1; off < 64; off <<= 1) hd += __shfl_xor(hd, off, 64);
+      if (lane == 0) sHd[w] = hd;
+      tiles::lds_barrier();
+      if (w == 0) {
+        float d[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        d[i] = 0.f;
+        for (int i = 0; i < 4; ++i) {
+          d[i] = 0.f;
 #pragma unroll
-        for (int c = 0; c < KW; ++c) d[i] += red[(i * 4 + c) * BT + lane];
-      }
-      const float b = sG[3 * BT + lane];
-      const bool live = lane < nrow;
-      float dG = live ? d[0] + b * d[1] - d[2] : 0.f;
-      // at the last row: the state at the chunk's end and its gradient
-      float cross = live ? d[3] : 0.f;
+          for (int c = 0; c < KW; ++c) d[i] += red[(i * 4 + c) * BT + lane];
+        }
+        const float b = sG[3 * BT + lane];
+        const bool live = lane < nrow;
+        float dG = live ? d[0] + b * d[1] - d[2] : 0.f;
+        // at the last row: the state at the chunk's end and its gradient
+        float cross = live ? d[3] : 0.f;
 #pragma unroll
-      for (int off = 1; off < 64; off <<= 1) cross += __shfl_xor(cross, off, 64);
-      float hh = 0.f;
+        for (int off = 1; off < 64; off <<= 1) cross += __shfl_xor(cross, off, 64);
+        float hh = 0.f;
 #pragma unroll
-      for (int c = 0; c < 8; ++c) hh += sHd[c];
-      cross += sG[BT + nrow - 1] * hh;
-      // sums from each row to the end
+        for (int c = 0; c < 8; ++c) hh += sHd[c];
+        cross += sG[BT + nrow - 1] * hh;
+        // sums from each row to the end
 #pragma unroll
-      for (int off = 1; off < 64; off <<= 1) {
-        const float y = __shfl_down(dG, off, 64);
-        if (lane + off < 64) dG += y;
-      }
-      if (live) {
-        const size_t at = (size_t)(c0 + lane) * HV + j;
-        if (a.dg) reinterpret_cast<T*>(a.dg)[at] = from_f<T>((dG + cross) * inv);
-        reinterpret_cast<T*>(a.dbeta)[at] = from_f<T>((sVdr[lane] + sVdr[BT + lane] + d[1]) * inv);
+        for (int off = 1; off < 64; off <<= 1) {
+          const float y = __shfl_down(dG, off, 64);
+          if (lane + off < 64) dG += y;
+        }
+        if (live) {
+          const size_t at = (size_t)(c0 + lane) * HV + j;
+          if (a.dg) reinterpret_cast<T*>(a.dg)[at] = from_f<T>((dG + cross) * inv);
+          reinterpret_cast<T*>(a.dbeta)[at] = from_f<T>((sVdr[lane] + sVdr[BT + lane] + d[1]) * inv);
+        }
       }
     }
     if (r + 1 < GR) tiles::lds_barrier();   // the tiles, gates and dots are written again for the next head
   }
-  if constexpr (GROUPED) {
-    const int lane = threadIdx.x & 63, n = lane & 15, g = lane >> 4;
+  const int lane = threadIdx.x & 63, n = lane & 15, g = lane >> 4;
 #pragma unroll
-    for (int t = 0; t < NT; ++t) {
-      const int tok = 16 * (tb0 + t) + n;
-      if (tok < nrow) {
-        const size_t at = (size_t)(c0 + tok) * krow + (size_t)jk * D + 32 * kw + 8 * g;
-        store_io8(reinterpret_cast<T*>(a.dq) + at, both(dq_sum[0][t], dq_sum[1][t]));
-        store_io8(reinterpret_cast<T*>(a.dk) + at, both(dk_sum[0][t], dk_sum[1][t]));
-      }
+  for (int t = 0; t < NT; ++t) {
+    const int tok = 16 * (tb0 + t) + n;
+    if (tok < nrow) {
+      const size_t at = (size_t)(c0 + tok) * krow + (size_t)jk * D + 32 * kw + 8 * g;
+      store_io8(reinterpret_cast<T*>(a.dq) + at, both(dq[0][t], dq[1][t]) * inv);
+      store_io8(reinterpret_cast<T*>(a.dk) + at, both(dk[0][t], dk[1][t]) * inv);
     }
   }
 }
 
-template <typename T, int D, bool GROUPED>
+template <typename T, int D>
 hipError_t launch_grad(const ChunkBwdArgs& a, hipStream_t s) {
-  hipLaunchKernelGGL((gdn_bwd_grad_kernel<T, D, GROUPED>), dim3(intra::intra_blocks(a.nslots, a.f.Hk)), dim3(NTHREADS), 0,
-                     s, a);
+  hipLaunchKernelGGL((gdn_bwd_grad_kernel<T, D>), dim3(intra::intra_blocks(a.nslots, a.f.Hk)), dim3(NTHREADS), 0, s, a);
   return hipGetLastError();
-}
-
-template <typename T>
-hipError_t launch_io(const ChunkBwdArgs& a, hipStream_t s) {
-  const bool grouped = a.f.HV != a.f.Hk;
-  if (a.f.K == 128) return grouped ? launch_grad<T, 128, true>(a, s) : launch_grad<T, 128, false>(a, s);
-  return grouped ? launch_grad<T, 64, true>(a, s) : launch_grad<T, 64, false>(a, s);
 }
 
 }  // namespace
 
 hipError_t launch_chunk_bwd_grad(const ChunkBwdArgs& a, hipStream_t s) {
-  return a.f.bf16 ? launch_io<bf16_t>(a, s) : launch_io<float>(a, s);
+  if (a.f.bf16) return a.f.K == 128 ? launch_grad<bf16_t, 128>(a, s) : launch_grad<bf16_t, 64>(a, s);
+  return a.f.K == 128 ? launch_grad<float, 128>(a, s) : launch_grad<float, 64>(a, s);
 }
 
 }  // namespace gdn

@@ -139,10 +139,15 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
 
   float inv = 1.f, gs = 1.f;
   if (back && a.amax) {
-    // the largest gradient of the (sequence, head): of dht, and of the chunks' quarters
+    // the largest gradient of the (sequence, key head): of dht, and of the chunks' quarters
     uint32_t* const sm = reinterpret_cast<uint32_t*>(lds);
-    uint32_t m = a.dht ? a.amax_dht[(size_t)ns * HV + j] : 0;
-    for (int i = threadIdx.x; i < 4 * NC; i += 512) m = max(m, a.part[((size_t)slot0 * 4 + i) * HV + j]);
+    uint32_t m = 0;
+    for (int i = threadIdx.x; i < 4 * NC * GR; i += 512) {
+      const int row = i / GR;
+      m = max(m, a.part[((size_t)slot0 * 4 + row) * HV + jk * GR + (i - row * GR)]);
+    }
+    if (a.dht)
+      for (int i = threadIdx.x; i < GR; i += 512) m = max(m, a.amax_dht[(size_t)ns * HV + jk * GR + i]);
 #pragma unroll
     for (int off = 32; off > 0; off >>= 1) m = max(m, (uint32_t)__shfl_xor((int)m, off, 64));
     if (lane == 0) sm[threadIdx.x >> 6] = m;
@@ -151,7 +156,7 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
     for (int i = 0; i < 8; ++i) m = max(m, sm[i]);
     __syncthreads();
     gs = grad_scale(m, inv);
-    if (v0 == 0 && threadIdx.x == 0) a.amax[(size_t)ns * HV + j] = m;   // for the chunks' gradients
+    if (v0 == 0 && j == jk * GR && threadIdx.x == 0) a.amax[(size_t)ns * Hk + jk] = m;   // for the chunks' gradients
   }
   auto chunk_of = [&](int i) { return back ? NC - 1 - i : i; };
 

@@ -123,7 +123,7 @@ struct ChunkBwdArgs {
   void* dh0;             // [N, HV, V, K] or nullptr
   // workspace
   uint32_t *amax_dht, *part;   // bf16 io: bits of the largest |dht| [N, HV], |dout| [chunks, 4, HV]
-  uint32_t* amax;        // [N, HV] ... of both; nullptr with fp32 io
+  uint32_t* amax;        // [N, Hk] ... of both and of a key head's v-heads; nullptr with fp32 io
   void *hs, *ds;         // [chunks, HV, V, K] states at the chunks' starts, gradients at their ends
   void *vn, *dr;         // [chunks, HV, V, 64] new values, their gradients, a column a row
   int nslots;            // chunks that these hold

@@ -211,12 +211,11 @@ int gdn_chunk_fwd_noalloc(const void* q, const void* k, const void* v,
  * Every gradient is of the io dtype.  With bf16 io the operands of the products
  * (states, gradients of states and of the new values, scores) are fp16 with fp32
  * sums, which limits all of them alike; the gradients among them are kept times a
- * power of two, one for each (sequence, v-head), that brings the largest |dout|
- * and |dht| of it to 2 .. 4, so gradients of any size keep their precision, and
- * one 2^-16 of its head's largest still has a bf16's.  A value past 65504 times
- * that scale becomes an infinity; where dout or dht hold an infinity or NaN, all
- * gradients of that sequence and head (of the key head, for dq and dk, in the
- * chunks of the sequence) are NaN.  fp32 io: fp32 throughout.  The same bits in
+ * power of two, one for each (sequence, key head), that brings the largest |dout|
+ * and |dht| of its v-heads to 2 .. 4, so gradients of any size keep their
+ * precision, and one 2^-16 of that largest still has a bf16's.  A value past 65504
+ * times that scale becomes an infinity; where dout or dht hold an infinity or NaN,
+ * all gradients of that sequence and key head are NaN.  fp32 io: fp32 throughout.  The same bits in
  * every run.  Supported sizes and errors as in gdn_chunk_fwd.  T = 0 (or all
  * sequences empty) is valid: dh0 = dht (or zeros) is written.
  */
