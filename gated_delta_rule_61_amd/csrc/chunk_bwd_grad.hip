@@ -114,6 +114,8 @@ __global__ __launch_bounds__(NTHREADS) __attribute__((amdgpu_waves_per_eu(sizeof
   // G, e^G, e^{G_last - G}, beta of the tokens; dot products, one row for 32 channels;
   // v . dR; <h, dh'> of each wave
   __shared__ __attribute__((aligned(16))) float sG[4 * BT], red[16 * BT], sVdr[2 * BT], sHd[8];
+  // q . dq and k . dk (the lane's channels) of the heads so far
+  __shared__ float sDone[2 * NT][NTHREADS];
 
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int kw = w % KW, th = w / KW, tb0 = th * NT;   // the wave's channels 32 kw .. and token blocks
@@ -138,16 +140,11 @@ __global__ __launch_bounds__(NTHREADS) __attribute__((amdgpu_waves_per_eu(sizeof
   const T* const qp = reinterpret_cast<const T*>(a.f.q) + (size_t)c0 * krow + (size_t)jk * D;
   const T* const kp = reinterpret_cast<const T*>(a.f.k) + (size_t)c0 * krow + (size_t)jk * D;
 
-  // sums over the heads: dq, and dk; what of q . dq and k . dk (the lane's channels) the heads
-  // before made up
-  f32x4 dq[2][NT], dk[2][NT];
-  float q_dq[NT], k_dk[NT];
+  f32x4 dq[2][NT], dk[2][NT];   // sums over the heads
 #pragma unroll
-  for (int t = 0; t < NT; ++t) {
-    q_dq[t] = k_dk[t] = 0.f;
+  for (int t = 0; t < NT; ++t)
 #pragma unroll
     for (int h = 0; h < 2; ++h) dq[h][t] = dk[h][t] = zero4();
-  }
   // every gradient of the key head's v-heads is kept times one power of two
   float inv = 1.f, gs = 1.f;
   if (a.amax) gs = grad_scale(a.amax[(size_t)ns * Hk + jk], inv);
@@ -220,7 +217,7 @@ __global__ __launch_bounds__(NTHREADS) __attribute__((amdgpu_waves_per_eu(sizeof
       const float graw = a.f.g ? a.f.g[(size_t)(c0 + tl) * HV + j] : (a.f.g_gamma ? a.f.g_gamma[j] : 0.f);
       const float b = a.f.beta[(size_t)(c0 + tl) * HV + j];
       const float G = intra::wave_incl_scan(lane < nrow ? graw : 0.f, lane);
-      const float Gl = __shfl(G, nrow - 1, 64);
+      const float Gl = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, G), nrow - 1));
       sG[lane] = G;
       sG[BT + lane] = __expf(G);
       sG[2 * BT + lane] = lane < nrow ? __expf(Gl - G) : 0.f;
@@ -316,11 +313,13 @@ __global__ __launch_bounds__(NTHREADS) __attribute__((amdgpu_waves_per_eu(sizeof
       };
       put_score(M[0], false, tbw, sbw);
       put_score(M[1], true, tbw, sbw);
-      if (w < 4) put_score(M[2], w >= 2, 3, 2 + (w & 1));
+      if (w < 2) put_score(M[2], false, 3, 2 + w);
+      else if (w < 4) put_score(M[2], true, 3, w);
       // the blocks above the diagonal that a 32-wide slab takes in
       if (w < 6) {
+        const float z = opaque(0.f);
         char* const tile = w / 2 == 0 ? S1 : w / 2 == 1 ? S2 : S3;
-        T64::put4(tile, 32 * (w & 1) + n, 32 * (w & 1) + 16 + 4 * g, zero4());
+        T64::put4(tile, 32 * (w & 1) + n, 32 * (w & 1) + 16 + 4 * g, f32x4{z, z, z, z});
       }
       tiles::lds_barrier();
       char* const sK = st1 + L::K;
@@ -335,7 +334,7 @@ __global__ __launch_bounds__(NTHREADS) __attribute__((amdgpu_waves_per_eu(sizeof
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
         const f32x8 k8 = values(TD::row(sK + TD::to_rows(o_chan, tb0 + t)));
-        wi[t] = -k_dk[t];
+        wi[t] = r == 0 ? 0.f : -sDone[NT + t][threadIdx.x];
 #pragma unroll
         for (int h = 0; h < 2; ++h)
 #pragma unroll
@@ -380,7 +379,12 @@ __global__ __launch_bounds__(NTHREADS) __attribute__((amdgpu_waves_per_eu(sizeof
         const int tok = 16 * (tb0 + t) + n, at = TD::to_rows(o_again, tb0 + t);
         const f32x8 k8 = values(TD::row(sK + at)), q8 = values(TD::row(sQ + at));
         // q . dq, k . E, k . W and the part of k . W that crosses the end, of this head
-        float d[4] = {-q_dq[t], 0.f, -k_dk[t], wi[t]};
+        float before_q = 0.f, before_k = 0.f;
+        if (r > 0) {
+          before_q = sDone[t][threadIdx.x];
+          before_k = sDone[NT + t][threadIdx.x];
+        }
+        float d[4] = {-before_q, 0.f, -before_k, wi[t]};
 #pragma unroll
         for (int h = 0; h < 2; ++h)
 #pragma unroll
@@ -391,8 +395,10 @@ __global__ __launch_bounds__(NTHREADS) __attribute__((amdgpu_waves_per_eu(sizeof
           }
         // dk = beta E + W
         const float b = sG[3 * BT + tok];
-        q_dq[t] += d[0];
-        k_dk[t] += fmaf(b, d[1], d[2]);
+        if (r + 1 < GR) {
+          sDone[t][threadIdx.x] = before_q + d[0];
+          sDone[NT + t][threadIdx.x] = before_k + fmaf(b, d[1], d[2]);
+        }
 #pragma unroll
         for (int h = 0; h < 2; ++h) dk[h][t] += E[h][t] * b;
 #pragma unroll
