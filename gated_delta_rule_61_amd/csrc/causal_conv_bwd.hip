@@ -259,7 +259,7 @@ int run_of(const ConvBwdArgs& a) {
   const int cblocks = (a.D / 8 + 63) / 64;
   const long long units = (long long)a.B * a.T * cblocks;
   long long run = (units / 2048 + 3) / 4 * 4;
-  return (int)(run < 8 ? 8 : run > 128 ? 128 : run);
+  return (int)(run < 4 ? 4 : run > 128 ? 128 : run);
 }
 
 template <typename T, int W>

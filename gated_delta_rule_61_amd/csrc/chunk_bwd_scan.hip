@@ -412,34 +412,33 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
 }
 
 // ---------------------------------------------------------- largest gradients
-// amax_dht[n, j] = bits of max |dht|: one work-group a (sequence, head).
-__global__ __launch_bounds__(256) void bwd_amax_dht_kernel(const float* __restrict__ dht, int per,
-                                                           uint32_t* __restrict__ amax) {
+// part[slot][quarter][head] = bits of max |dout| of 16 rows of a chunk, LPH lanes a head's
+// channels of a row; the last `states` work-groups: amax_dht[n, j] = bits of max |dht|.
+template <int LPH>
+__global__ __launch_bounds__(256) void bwd_amax_kernel(ChunkBwdArgs a, int cblocks, int states) {
   __shared__ uint32_t sm[4];
   uint32_t m = 0;
-  const uint4* p = reinterpret_cast<const uint4*>(dht + (size_t)blockIdx.x * per);
-  for (int i = threadIdx.x; i < per / 4; i += 256) {
-    const uint4 x = p[i];
-    m = max(m, max(max(x.x & 0x7FFFFFFFu, x.y & 0x7FFFFFFFu), max(x.z & 0x7FFFFFFFu, x.w & 0x7FFFFFFFu)));
-  }
+  const int first = (int)gridDim.x - states;
+  if ((int)blockIdx.x >= first) {
+    const int cell = (int)blockIdx.x - first, per = a.f.V * a.f.K;
+    const uint4* p = reinterpret_cast<const uint4*>(a.dht + (size_t)cell * per);
+    for (int i = threadIdx.x; i < per / 4; i += 256) {
+      const uint4 x = p[i];
+      m = max(m, max(max(x.x & 0x7FFFFFFFu, x.y & 0x7FFFFFFFu), max(x.z & 0x7FFFFFFFu, x.w & 0x7FFFFFFFu)));
+    }
 #pragma unroll
-  for (int off = 32; off > 0; off >>= 1) m = max(m, (uint32_t)__shfl_xor((int)m, off, 64));
-  if ((threadIdx.x & 63) == 0) sm[threadIdx.x >> 6] = m;
-  __syncthreads();
-  if (threadIdx.x == 0) amax[blockIdx.x] = max(max(sm[0], sm[1]), max(sm[2], sm[3]));
-}
-
-// part[slot][quarter][head] = bits of max |dout| of 16 rows of a chunk.  LPH lanes hold a
-// head's channels of a row.
-template <int LPH>
-__global__ __launch_bounds__(256) void bwd_amax_kernel(ChunkBwdArgs a, int cblocks) {
+    for (int off = 32; off > 0; off >>= 1) m = max(m, (uint32_t)__shfl_xor((int)m, off, 64));
+    if ((threadIdx.x & 63) == 0) sm[threadIdx.x >> 6] = m;
+    __syncthreads();
+    if (threadIdx.x == 0) a.amax_dht[cell] = max(max(sm[0], sm[1]), max(sm[2], sm[3]));
+    return;
+  }
   const int cb = blockIdx.x % cblocks, part = blockIdx.x / cblocks % 4, slot = blockIdx.x / cblocks / 4;
   int c0, nrow;
   if (!intra::locate_chunk(slot, a.f.cu_seqlens, a.f.chunk_off, a.f.N, a.f.T, (a.f.T + BT - 1) / BT, c0, nrow)) return;
   const int ch = (cb * 256 + threadIdx.x) * 8;
   const int HV = a.f.HV, C = HV * LPH * 8;
   if (ch >= C) return;   // whole heads
-  uint32_t m = 0;
   const bf16_t* p = reinterpret_cast<const bf16_t*>(a.dout) + (size_t)c0 * C + ch;
   uint4 x[16];
 #pragma unroll
@@ -475,15 +474,12 @@ hipError_t launch_scan(const ChunkBwdArgs& a, hipStream_t s) {
 
 hipError_t launch_chunk_bwd_amax(const ChunkBwdArgs& a, hipStream_t s) {
   const ChunkArgs& f = a.f;
-  if (a.dht) {
-    hipLaunchKernelGGL(bwd_amax_dht_kernel, dim3((unsigned)(f.N * f.HV)), dim3(256), 0, s, a.dht, f.V * f.K, a.amax_dht);
-    if (hipError_t e = hipGetLastError()) return e;
-  }
-  if ((long long)f.B * f.T == 0) return hipSuccess;
-  const int cblocks = (f.HV * f.V / 8 + 255) / 256;
-  const dim3 grid((unsigned)((long long)a.nslots * 4 * cblocks));
-  if (f.V == 128) hipLaunchKernelGGL((bwd_amax_kernel<16>), grid, dim3(256), 0, s, a, cblocks);
-  else hipLaunchKernelGGL((bwd_amax_kernel<8>), grid, dim3(256), 0, s, a, cblocks);
+  const int cblocks = (f.HV * f.V / 8 + 255) / 256, states = a.dht ? f.N * f.HV : 0;
+  const long long chunks = (long long)f.B * f.T > 0 ? (long long)a.nslots * 4 * cblocks : 0;
+  if (chunks + states == 0) return hipSuccess;
+  const dim3 grid((unsigned)(chunks + states));
+  if (f.V == 128) hipLaunchKernelGGL((bwd_amax_kernel<16>), grid, dim3(256), 0, s, a, cblocks, states);
+  else hipLaunchKernelGGL((bwd_amax_kernel<8>), grid, dim3(256), 0, s, a, cblocks, states);
   return hipGetLastError();
 }
 

@@ -265,7 +265,7 @@ int gdn_conv_bwd(const void* dout0, const void* dout1, const void* dout2, int wi
   if (!aligned16(dx) || !aligned16(dweight) || !aligned16(dbias))
     return fail(GDN_ERR_INVALID_ARGUMENT, "tensor pointers must be 16-byte aligned");
   if (int st = check_rows("x", f.x, B, T, 8)) return st;
-  if (too_many(((long long)B * T / 8 + 1) * (D / 512 + 1), 64))
+  if (too_many(((long long)B * T / 8 + 2048) * (D / 512 + 1), 64))   // runs of 8 tokens, or 2048 shorter ones
     return fail(GDN_ERR_UNSUPPORTED, "too many tokens x channels for one launch");
   ConvBwdArgs a{};
   a.x = f.x; a.weight = weight; a.bias = bias;
