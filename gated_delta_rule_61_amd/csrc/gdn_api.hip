@@ -441,6 +441,13 @@ int gdn_chunk_bwd(const void* q, const void* k, const void* v, const float* g, c
   if ((long long)HV * V >= (1 << 23)) return fail(GDN_ERR_UNSUPPORTED, "HV * V must stay below 2^23");
   const bool bf16 = dtype == GDN_DTYPE_BF16;
   const BwdWorkspace L = bwd_workspace_layout(B, T, HV, K, V, P.N, cu_seqlens != nullptr, bf16);
+  {   // a launch holds fewer than 2^32 threads: largest gradients, both scans, the chunks
+    const long long cblocks = (HV * V / 8 + 255) / 256, heads = (long long)P.N * HV;
+    if ((L.nslots * 4LL * cblocks + heads) * 256 >= (1LL << 32) || (heads + 8LL * (HV / Hk)) * (V / 64) * 1024 >= (1LL << 32) ||
+        (L.nslots + 8LL) * Hk * 512 >= (1LL << 32))
+      return fail(GDN_ERR_UNSUPPORTED, "too many chunks or sequences x heads for one launch (N=%d Hk=%d HV=%d)", P.N,
+                  Hk, HV);
+  }
   if (!workspace || workspace_bytes < L.total)
     return fail(GDN_ERR_WORKSPACE, "workspace of %zu bytes needed (got %zu)", L.total,
                 workspace ? workspace_bytes : (size_t)0);
