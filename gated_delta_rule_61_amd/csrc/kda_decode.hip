@@ -10,13 +10,21 @@
 // products are taken from the state before the decay, so that both row sums of
 // a token run together, in front of its update.
 //
-// HBM-bound: the state moves twice (2 x 32 KiB per head at K = V = 128 in
-// bf16).  A work-group of 256 threads takes one (row, head), or four of 64
-// threads a quarter of its value rows each when there are too few for the chip.
-// K / 8 lanes of a DPP row hold whole state rows: row sums are in-row
-// reductions.  The gates are the only thing threads share: each of the K T
-// exponentials is computed once a work-group and read from LDS.  The state's
-// loads are issued before everything else.
+// HBM-bound by the state, which moves twice (2 x 32 KiB per head at K = V = 128 in
+// bf16), as long as the vector work stays below that: 4 K V operations a token, with
+// four tokens about as long as the transfer.  So what a token's rows have in common
+// (gates, normalised q and k, k . q, beta) is computed once a work-group and read from
+// LDS, and outputs are added up in a way that leaves each to one lane.  256 rows x 32
+// heads of four tokens: 123 us, 580 MB at 4.7 TB/s (150 us with q and k in every wave,
+// registers for three waves a SIMD and outputs summed in all lanes; a large copy reaches
+// 5.2 TB/s).  One row of 32 heads, one token: 4.6 us, the launch and two trips to memory.
+//
+// A work-group of V K / 64 threads takes one (row, head), also when these are fewer than
+// the CUs (32 of them, one token: 4.1 us a launch in a graph; four times as many
+// work-groups of a wave each: 4.9, and 155 instead of 115 us for the 8192 of above).
+// K / 8 lanes of a DPP row hold whole state rows: row sums are in-row reductions.  The
+// state's loads are issued before everything else.  States and sums are fp32; the
+// pool's type rounds once, at the end.
 
 #include "gdn_device.h"
 #include "mixer_launch.h"
@@ -28,50 +36,70 @@ namespace {
 
 using namespace rows;
 
+// by value: a choice between two elements of an array would be one between addresses
+__device__ __forceinline__ float choose(bool c, float x, float y) { return c ? x : y; }
+
+// x[cl % 8]
+__device__ __forceinline__ float pick(const float (&x)[8], int cl) {
+  const bool b0 = cl & 1, b1 = cl & 2, b2 = cl & 4;
+  const float lo = choose(b1, choose(b0, x[3], x[2]), choose(b0, x[1], x[0]));
+  const float hi = choose(b1, choose(b0, x[7], x[6]), choose(b0, x[5], x[4]));
+  return choose(b2, hi, lo);
+}
+
+// Sums over the LPR lanes of a state row of the eight values x; lane cl gets that of
+// x[cl % 8].  Halves of the lanes swap halves of the values: 8 additions instead of
+// the 24 (32) of eight sums that every lane gets.
+template <int LPR>
+__device__ __forceinline__ float row_sum_each(const float (&x)[8], int cl) {
+  const bool b0 = cl & 1, b1 = cl & 2, b2 = cl & 4;
+  float y[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) y[i] = choose(b2, x[4 + i], x[i]) + dpp_f<0x141>(choose(b2, x[i], x[4 + i]));
+  const float p = choose(b1, y[2], y[0]) + dpp_f<0x4E>(choose(b1, y[0], y[2]));
+  const float q = choose(b1, y[3], y[1]) + dpp_f<0x4E>(choose(b1, y[1], y[3]));
+  float r = choose(b0, q, p) + dpp_f<0xB1>(choose(b0, p, q));
+  if constexpr (LPR == 16) r += dpp_f<0x128>(r);   // the lane 8 further on
+  return r;
+}
+
 // T: io type, S: pool type.  A thread holds R = 8 consecutive state rows.
-template <typename T, typename S, int K, int TT, int TPB>
-__global__ __launch_bounds__(TPB) void kda_decode_kernel(KdaStepArgs a, int parts) {
-  constexpr int LPR = K / 8, R = 8;
+template <typename T, typename S, int K, int V, int TT>
+__global__ __launch_bounds__(V * K / 64) __attribute__((amdgpu_waves_per_eu(4))) void kda_decode_kernel(KdaStepArgs a) {
+  constexpr int LPR = K / 8, R = 8, TPB = V * K / 64;
   __shared__ __attribute__((aligned(16))) float gate[TT][K];
-  const int bh = blockIdx.x / parts;
-  const int part = blockIdx.x - bh * parts;
-  const int bi = bh / a.HV;
-  const int hv = bh - bi * a.HV;
+  __shared__ __attribute__((aligned(16))) float kn[TT][K];
+  __shared__ __attribute__((aligned(16))) float qn[TT][K];
+  __shared__ __attribute__((aligned(16))) float vs[TT][V];
+  __shared__ float scal[TT][2];   // k . q, beta
+  const int bi = blockIdx.x / a.HV;
+  const int hv = blockIdx.x - bi * a.HV;
   const int hk = hv / (a.HV / a.H);
   const int cl = threadIdx.x % LPR;
-  const int row0 = (part * (TPB / LPR) + threadIdx.x / LPR) * R;   // < V: the launch has V K / 64 threads a state
+  const int row0 = threadIdx.x / LPR * R;
   const int slot = a.idx ? a.idx[bi] : bi;
   const bool valid = slot >= 0 && slot < a.pool;
-  T* const op = reinterpret_cast<T*>(a.o) + ((size_t)bi * TT * a.HV + hv) * a.V + row0;
+  T* const op = reinterpret_cast<T*>(a.o) + ((size_t)bi * TT * a.HV + hv) * V + row0;
   if (!valid) {   // o = 0, the pool is not touched (the whole work-group leaves)
     if (cl < R) {
 #pragma unroll
-      for (int t = 0; t < TT; ++t) op[(size_t)t * a.HV * a.V + cl] = from_f<T>(0.f);
+      for (int t = 0; t < TT; ++t) op[(size_t)t * a.HV * V + cl] = from_f<T>(0.f);
     }
     return;
   }
   constexpr int second = Cols<S, K>::second;
   const int c0 = Cols<S, K>::first(cl);
-  S* sp = reinterpret_cast<S*>(a.state) + (((size_t)slot * a.HV + hv) * a.V + row0) * K + c0;
+  S* sp = reinterpret_cast<S*>(a.state) + (((size_t)slot * a.HV + hv) * V + row0) * K + c0;
   Raw<S> raw[R];
 #pragma unroll
   for (int i = 0; i < R; ++i) raw[i].load(sp + (size_t)i * K, second);
 
   const size_t tok0 = (size_t)bi * TT;
   const T* ap = reinterpret_cast<const T*>(a.a) + (tok0 * a.HV + hv) * K;
-  const T* qp = reinterpret_cast<const T*>(a.q) + (tok0 * a.H + hk) * K + c0;
-  const T* kp = reinterpret_cast<const T*>(a.k) + (tok0 * a.H + hk) * K + c0;
-  const T* vp = reinterpret_cast<const T*>(a.v) + (tok0 * a.HV + hv) * a.V + row0;
-  float qq[TT][8], kk[TT][8], vv[TT][R], beta[TT];
-#pragma unroll
-  for (int t = 0; t < TT; ++t) {
-    load4(qp + (size_t)t * a.H * K, qq[t]);
-    load4(qp + (size_t)t * a.H * K + second, qq[t] + 4);
-    load4(kp + (size_t)t * a.H * K, kk[t]);
-    load4(kp + (size_t)t * a.H * K + second, kk[t] + 4);
-    load4(vp + (size_t)t * a.HV * a.V, vv[t]);
-    load4(vp + (size_t)t * a.HV * a.V + 4, vv[t] + 4);
-    beta[t] = to_f(reinterpret_cast<const T*>(a.b)[(tok0 + t) * a.HV + hv]);
+  const T* vp = reinterpret_cast<const T*>(a.v) + (tok0 * a.HV + hv) * V;
+  for (int i = threadIdx.x; i < TT * V / 4; i += TPB) {
+    const int t = i / (V / 4), r = i % (V / 4) * 4;
+    load4(vp + (size_t)t * a.HV * V + r, &vs[t][r]);
   }
   const float A = -expf(a.A_log[hv]);
   for (int i = threadIdx.x; i < TT * K; i += TPB) {
@@ -81,23 +109,23 @@ __global__ __launch_bounds__(TPB) void kda_decode_kernel(KdaStepArgs a, int part
     const float step = bu <= a.sp_thr ? log1pf(expf(bu)) / a.sp_beta : u;
     gate[t][c] = step == 0.f ? 1.f : expf(A * step);   // A may be infinite
   }
-  __syncthreads();
-
-  float st[R][8];
-#pragma unroll
-  for (int i = 0; i < R; ++i) raw[i].get(st[i]);
-
-#pragma unroll
-  for (int t = 0; t < TT; ++t) {
-    float e[8];
-    load4(&gate[t][c0], e);
-    load4(&gate[t][c0 + second], e + 4);
+  // q, k and the scalars of a token: LPR lanes of the last wave each
+  if (const int t = ((int)threadIdx.x - (TPB - 64)) / LPR; (int)threadIdx.x >= TPB - 64 && t < TT) {
+    const size_t at = ((tok0 + t) * a.H + hk) * K + c0;
+    const T* qp = reinterpret_cast<const T*>(a.q) + at;
+    const T* kp = reinterpret_cast<const T*>(a.k) + at;
+    float q[8], k[8];
+    load4(qp, q);
+    load4(qp + second, q + 4);
+    load4(kp, k);
+    load4(kp + second, k + 4);
+    const float bt = to_f(reinterpret_cast<const T*>(a.b)[(tok0 + t) * a.HV + hv]);
     float sq = 0.f, sk = 0.f, kq = 0.f;
 #pragma unroll
     for (int c = 0; c < 8; ++c) {
-      sq = fmaf(qq[t][c], qq[t][c], sq);
-      sk = fmaf(kk[t][c], kk[t][c], sk);
-      kq = fmaf(kk[t][c], qq[t][c], kq);
+      sq = fmaf(q[c], q[c], sq);
+      sk = fmaf(k[c], k[c], sk);
+      kq = fmaf(k[c], q[c], kq);
     }
     kq = row_sum<LPR>(kq);
     float qs = a.scale, ks = 1.f;
@@ -105,16 +133,41 @@ __global__ __launch_bounds__(TPB) void kda_decode_kernel(KdaStepArgs a, int part
       qs = a.scale / sqrtf(row_sum<LPR>(sq) + a.eps);
       ks = 1.f / sqrtf(row_sum<LPR>(sk) + a.eps);
     }
-    kq *= qs * ks;
-    float ek[8], eq[8], kn[8];
+    float* const kw = &kn[t][c0];
+    float* const qw = &qn[t][c0];
+    *reinterpret_cast<f32x4*>(kw) = f32x4{k[0], k[1], k[2], k[3]} * ks;
+    *reinterpret_cast<f32x4*>(kw + second) = f32x4{k[4], k[5], k[6], k[7]} * ks;
+    *reinterpret_cast<f32x4*>(qw) = f32x4{q[0], q[1], q[2], q[3]} * qs;
+    *reinterpret_cast<f32x4*>(qw + second) = f32x4{q[4], q[5], q[6], q[7]} * qs;
+    if (cl == 0) {
+      scal[t][0] = kq * (qs * ks);
+      scal[t][1] = 1.f / (1.f + expf(-bt));
+    }
+  }
+  __syncthreads();
+
+  float st[R][8];
+#pragma unroll
+  for (int i = 0; i < R; ++i) raw[i].get(st[i]);
+
+#pragma unroll 1
+  for (int t = 0; t < TT; ++t) {
+    float e[8], ek[8], eq[8], k[8], v[R];
+    load4(&vs[t][row0], v);
+    load4(&vs[t][row0 + 4], v + 4);
+    load4(&gate[t][c0], e);
+    load4(&gate[t][c0 + second], e + 4);
+    load4(&kn[t][c0], k);
+    load4(&kn[t][c0 + second], k + 4);
+    load4(&qn[t][c0], eq);
+    load4(&qn[t][c0 + second], eq + 4);
+    const float kq = scal[t][0], bt = scal[t][1];
 #pragma unroll
     for (int c = 0; c < 8; ++c) {
-      kn[c] = kk[t][c] * ks;
-      ek[c] = e[c] * kn[c];
-      eq[c] = e[c] * (qq[t][c] * qs);
+      ek[c] = e[c] * k[c];
+      eq[c] *= e[c];
     }
-    const float bt = 1.f / (1.f + expf(-beta[t]));
-    float pred[R], out[R];
+    float dlt[R], out[R];
 #pragma unroll
     for (int i = 0; i < R; ++i) {
       float p = 0.f, o = 0.f;
@@ -123,55 +176,38 @@ __global__ __launch_bounds__(TPB) void kda_decode_kernel(KdaStepArgs a, int part
         p = fmaf(st[i][c], ek[c], p);
         o = fmaf(st[i][c], eq[c], o);
       }
-      pred[i] = p;
+      dlt[i] = p;
       out[i] = o;
     }
 #pragma unroll
     for (int i = 0; i < R; ++i) {
-      pred[i] = row_sum<LPR>(pred[i]);
-      out[i] = row_sum<LPR>(out[i]);
-    }
+      dlt[i] = bt * (v[i] - row_sum<LPR>(dlt[i]));
 #pragma unroll
-    for (int i = 0; i < R; ++i) {
-      const float dlt = bt * (vv[t][i] - pred[i]);
-      out[i] = fmaf(kq, dlt, out[i]);
-#pragma unroll
-      for (int c = 0; c < 8; ++c) st[i][c] = fmaf(dlt, kn[c], st[i][c] * e[c]);
+      for (int c = 0; c < 8; ++c) st[i][c] = fmaf(dlt[i], k[c], st[i][c] * e[c]);
     }
     // lane i of the row group stores row i
-    float y = out[0];
-#pragma unroll
-    for (int i = 1; i < R; ++i) y = cl == i ? out[i] : y;
-    if (cl < R) op[(size_t)t * a.HV * a.V + cl] = from_f<T>(y);
+    const float y = fmaf(kq, pick(dlt, cl), row_sum_each<LPR>(out, cl));
+    if (cl < R) op[(size_t)t * a.HV * V + cl] = from_f<T>(y);
   }
 #pragma unroll
   for (int i = 0; i < R; ++i) put_state(sp + (size_t)i * K, second, st[i]);
 }
 
-template <typename T, typename S, int K, int TT>
-hipError_t launch_t(const KdaStepArgs& a, hipStream_t s) {
-  const long long pairs = (long long)a.B * a.HV;
-  const int threads = a.V * (K / 8) / 8;   // 64, 128 or 256 threads hold a state
-  // fewer (row, head) pairs than CUs, or a small state: work-groups of one wave
-  if constexpr (K == 128) {
-    if (pairs >= 256 && threads == 256) {
-      hipLaunchKernelGGL((kda_decode_kernel<T, S, K, TT, 256>), dim3((unsigned)pairs), dim3(256), 0, s, a, 1);
-      return hipGetLastError();
-    }
+template <typename T, typename S, int K, int V>
+hipError_t launch_v(const KdaStepArgs& a, hipStream_t s) {
+  const dim3 grid((unsigned)((long long)a.B * a.HV)), threads(V * K / 64);
+  switch (a.T) {
+    case 1: hipLaunchKernelGGL((kda_decode_kernel<T, S, K, V, 1>), grid, threads, 0, s, a); break;
+    case 2: hipLaunchKernelGGL((kda_decode_kernel<T, S, K, V, 2>), grid, threads, 0, s, a); break;
+    case 3: hipLaunchKernelGGL((kda_decode_kernel<T, S, K, V, 3>), grid, threads, 0, s, a); break;
+    default: hipLaunchKernelGGL((kda_decode_kernel<T, S, K, V, 4>), grid, threads, 0, s, a);
   }
-  const int parts = threads / 64;
-  hipLaunchKernelGGL((kda_decode_kernel<T, S, K, TT, 64>), dim3((unsigned)(pairs * parts)), dim3(64), 0, s, a, parts);
   return hipGetLastError();
 }
 
 template <typename T, typename S, int K>
 hipError_t launch_k(const KdaStepArgs& a, hipStream_t s) {
-  switch (a.T) {
-    case 1: return launch_t<T, S, K, 1>(a, s);
-    case 2: return launch_t<T, S, K, 2>(a, s);
-    case 3: return launch_t<T, S, K, 3>(a, s);
-    default: return launch_t<T, S, K, 4>(a, s);
-  }
+  return a.V == 128 ? launch_v<T, S, K, 128>(a, s) : launch_v<T, S, K, 64>(a, s);
 }
 
 template <typename T>
