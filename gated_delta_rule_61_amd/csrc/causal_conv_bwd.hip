@@ -18,6 +18,8 @@
 // run are computed a second time for the run's last dx.  Each run leaves one
 // row of sums in a workspace; a second launch adds them up in a fixed order.
 
+#include <type_traits>
+
 #include "gdn_device.h"
 #include "mixer_launch.h"
 #include "rows8.h"
@@ -105,17 +107,19 @@ __global__ __launch_bounds__(64) void conv_bwd_kernel(ConvBwdArgs a, int run, in
       raw.get(win[j]);
     }
     float open[W][8] = {};   // sums of dx_{t-W+1} .. dx_t
-    for (long long t = from; t < stop; t += U) {
+    // rows t .. t + U - 1; WHOLE: all of them this run's own
+    auto rows = [&](long long t, auto whole) __attribute__((always_inline)) {
+      constexpr bool WHOLE = decltype(whole)::value;
       Raw8<T> xr[U], gr[U];
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        const long long tt = t + u < stop ? t + u : stop - 1;
+        const long long tt = WHOLE || t + u < stop ? t + u : stop - 1;
         xr[u].load(x_row(tt));
         gr[u].load(gb + tt * gw);
       }
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        if (t + u >= stop) break;
+        if (!WHOLE && t + u >= stop) break;
         float x[8], g[8], y[8];
         xr[u].get(x);
         gr[u].get(g);
@@ -131,8 +135,8 @@ __global__ __launch_bounds__(64) void conv_bwd_kernel(ConvBwdArgs a, int run, in
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
             const float p = __builtin_amdgcn_rcpf(1.0f + __expf(-y[e]));
-            slope[e] = fmaf(y[e], p * (1.0f - p), p);
             y[e] *= p;
+            slope[e] = fmaf(-y[e], p, p + y[e]);   // p + silu (1 - p)
           }
         } else {
 #pragma unroll
@@ -169,7 +173,7 @@ __global__ __launch_bounds__(64) void conv_bwd_kernel(ConvBwdArgs a, int run, in
             for (int e = 0; e < 8; ++e) g[e] = rs * k * (g[e] - y[e] * dot);
           }
         }
-        const bool mine = t + u < own;   // uniform
+        const bool mine = WHOLE || t + u < own;   // uniform
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
           const float dc = g[e] * slope[e];
@@ -194,7 +198,10 @@ __global__ __launch_bounds__(64) void conv_bwd_kernel(ConvBwdArgs a, int run, in
           win[W - 2][e] = x[e];
         }
       }
-    }
+    };
+    long long t = from;
+    for (; t + U <= own; t += U) rows(t, std::true_type{});
+    for (; t < stop; t += U) rows(t, std::false_type{});
     // the sequence's last rows, which nothing behind them adds to
     if (stop == end && live) {
 #pragma unroll
