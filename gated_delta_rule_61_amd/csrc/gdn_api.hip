@@ -440,6 +440,8 @@ int gdn_chunk_bwd(const void* q, const void* k, const void* v, const float* g, c
   // 64 rows of a tensor are addressed with 32-bit byte offsets
   if ((long long)HV * V >= (1 << 23)) return fail(GDN_ERR_UNSUPPORTED, "HV * V must stay below 2^23");
   const bool bf16 = dtype == GDN_DTYPE_BF16;
+  if (bf16 && scale != 0.f && !(std::fabs(scale) >= 0x1p-14f && std::fabs(scale) <= 65504.f))
+    return fail(GDN_ERR_UNSUPPORTED, "scale must be 0 or one of fp16's normal numbers with bf16 io (got %g)", scale);
   const BwdWorkspace L = bwd_workspace_layout(B, T, HV, K, V, P.N, cu_seqlens != nullptr, bf16);
   {   // a launch holds fewer than 2^32 threads: largest gradients, both scans, the chunks
     const long long cblocks = (HV * V / 8 + 255) / 256, heads = (long long)P.N * HV;

@@ -12,7 +12,10 @@
 //   dw = sum over the tokens (and groups that share w) of da n,  db of da
 //
 // Memory-bound: three rows of C channels forward (x, z, y), five backward
-// (x, z, dy, dx, dz) against 10 and 25 operations a channel.  A lane owns 8
+// (x, z, dy, dx, dz) against 10 and 25 operations a channel.  16384 tokens of 16 groups
+// of 128 in bf16: 33 us forward (201 MB at 6 TB/s, part of it from the last-level cache),
+// 69 us backward (337 MB at 4.9 TB/s) and 4 for the sums of the weights' gradients; a
+// large copy reaches 5.2 TB/s.  One token: 2.7 us, a launch.  A lane owns 8
 // consecutive channels (16 bytes of bf16); LPG lanes of a wave hold a group,
 // so the sums are in-register: squares of x - mean, not differences of sums.
 // The gradient computes n again from x: nothing is kept from the forward pass.
@@ -385,10 +388,12 @@ struct Walks {
 Walks walks_of(const GroupNormArgs& a, bool bwd) {
   const Shape sh = shape_of(a.d);
   const long long per = (long long)a.G * sh.lpg, rows = (long long)a.B * a.T;
-  const long long want = bwd ? 1 << 18 : 1 << 19;   // threads: what the chip holds of these kernels
+  const long long want = bwd ? 1 << 18 : 1 << 19;   // threads: what the chip holds of these kernels (four, eight waves a SIMD)
   long long step = (want + per - 1) / per;
   if (step > rows) step = rows;
-  // sums of weights per channel: a walk's row of the workspace is worth some tokens
+  // sums of weights per channel: a walk leaves two rows of them, so it takes four tokens at
+  // least (1001 tokens of 16 groups of 80 in fp32: 8.7 us + 5 for the sums; no less in all
+  // with two)
   if (bwd && !a.shared && a.dweight && step > (rows + 3) / 4) step = (rows + 3) / 4;
   Walks w;
   w.step = (int)step;

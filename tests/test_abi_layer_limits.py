@@ -19,3 +19,10 @@ def test_chunk_bwd_refuses_more_than_a_launch_holds(L, kw):  # noqa: F811
 def test_chunk_bwd_refuses_rows_past_32_bit_offsets(L):  # noqa: F811
     assert _chunk_bwd(L, wsb=1 << 62, B=1, Hk=1, HV=1 << 16) == 2
     assert b"2^23" in L.gdn_last_error()
+
+
+@pytest.mark.parametrize("scale", [2.0 ** -15, -1e5, 1e30, float("inf"), float("nan")])
+def test_chunk_bwd_refuses_scales_that_fp16_cannot_hold(L, scale):  # noqa: F811
+    assert _chunk_bwd(L, scale=scale) == 2
+    assert b"scale" in L.gdn_last_error()
+    assert _chunk_bwd(L, scale=scale, dt=0, ws=None) == 4   # fp32 io goes on to the next check
