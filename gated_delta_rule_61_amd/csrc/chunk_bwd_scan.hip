@@ -21,8 +21,9 @@
 // to the next launch; eight ragged sequences of 16001 tokens in all, 32 heads: 370 - 410 us,
 // 1.44 GB.  With loads by the state waves themselves the first took 260 us, with stores in
 // rows of the arrays instead of the order in which waves hold them the second 405.
-// fp32: bound by the matrix units of the few CUs that a small problem fills (1000 tokens x 2,
-// 4 heads of 64: 65 us, 4 us a chunk, five products of 64^3 at 32 cycles an instruction).
+// fp32: the chunks' products one after the other on the few CUs that a small problem fills
+// (1000 tokens x 2, 4 heads of 64: 65 us, 4 us a chunk; the state gradients' five products
+// are 288 instructions of 32 cycles on each SIMD).
 //
 // h and dh' leave as [V][K], Vn and dR transposed ([V][64]): what a lane's
 // accumulators hold in order, a wave's stores 1 KiB in a row.

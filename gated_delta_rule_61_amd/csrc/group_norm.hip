@@ -12,11 +12,12 @@
 //   dw = sum over the tokens (and groups that share w) of da n,  db of da
 //
 // Memory-bound: three rows of C channels forward (x, z, y), five backward
-// (x, z, dy, dx, dz) against 10 and 25 operations a channel.  16384 tokens of 16 groups
-// of 128 in bf16: 33 us forward (201 MB at 6 TB/s, part of it from the last-level cache),
-// 69 us backward (337 MB at 4.9 TB/s) and 4 for the sums of the weights' gradients; a
-// large copy reaches 5.2 TB/s.  One token: 2.7 us, a launch.  A lane owns 8
-// consecutive channels (16 bytes of bf16); LPG lanes of a wave hold a group,
+// (x, z, dy, dx, dz) against 10 and 25 operations a channel.  16384 tokens of 16
+// groups of 128 in bf16: 38 us forward (201 MB at 5.3 TB/s), 68 us backward (337 MB at
+// 4.9 TB/s) and 5 for the sums of the weights' gradients; a large copy reaches 5.2
+// TB/s.  One token: 2.6 us, a launch.
+//
+// A lane owns 8 consecutive channels (16 bytes of bf16); LPG lanes of a wave hold a group,
 // so the sums are in-register: squares of x - mean, not differences of sums.
 // The gradient computes n again from x: nothing is kept from the forward pass.
 // Groups above 1024 channels take a whole work-group.  A thread keeps its
