@@ -716,8 +716,10 @@ def gdn_chunk_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: Optional
     (io dtype), and ``dht`` [N,HV,V,K] fp32, that of its final states (None:
     zeros); the other arguments as they were given there.  Returns (dq, dk, dv,
     dg, dbeta, dh0) in the io dtype, of the shapes of q, k, v, g, beta and h0;
-    dg is None without ``g``, dh0 without ``h0``.  A ``workspace`` (of
-    ``chunk_bwd_workspace_bytes``; else allocated) serves one call at a time."""
+    dg is None without ``g``, dh0 without ``h0``; rows behind the last boundary of
+    ``cu_seqlens`` are not written (they hold whatever the new memory held).  A
+    ``workspace`` (of ``chunk_bwd_workspace_bytes``; else allocated) serves one
+    call at a time."""
     if q.dim() != 4 or v.dim() != 4:
         raise ValueError("q, k must be [B, T, Hk, K] and v [B, T, HV, V]")
     dev = _cuda(q, "q")
@@ -749,8 +751,9 @@ def causal_conv_bwd(dout, x: torch.Tensor, weight: torch.Tensor, bias: Optional[
     zeros).  ``dout``: the gradient of its result, one tensor or with
     ``sections`` a tuple, packed; the other arguments as they were given there.
     Returns (dx [B,T,D], dweight [D,W], dbias [D] or None without a bias) in the
-    io dtype; dx's rows behind the last boundary of ``cu_seqlens`` are left as
-    they are.  A ``workspace`` (else allocated) serves one call at a time."""
+    io dtype; dx's rows behind the last boundary of ``cu_seqlens`` are not written
+    (they hold whatever the new memory held).  A ``workspace`` (else allocated)
+    serves one call at a time."""
     douts = (dout,) if isinstance(dout, torch.Tensor) else tuple(dout)
     head, (B, T, D, W, code), _, _, _, dev = _conv_args(x, weight, bias, activation, sections, None, douts, "dout")
     N, cu = _seqs(cu_seqlens, B, dev)

@@ -18,8 +18,8 @@
 // Bound by memory: 4 sequences of 4096 tokens, 16 heads of 128, bf16: 183 - 196 us, 911 MB
 // at 4.8 TB/s; eight ragged sequences of 16001 tokens in all, 16 x 32 heads: 330 - 350 us.
 // 128 registers, so that two work-groups share a CU and one's loads cover the other's
-// products; with a work-group a v-head the second size took 510 us.  Two chunks of two heads of 128: 24 us, the latency of eight
-// blocks, one after the other.
+// products; with a work-group a v-head the second size took 510 us.  Two chunks of two
+// heads of 128: 24 us, the latency of eight blocks, one after the other.
 
 #include "chunk_bwd.h"
 #include "chunk_common.h"
