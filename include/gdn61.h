@@ -210,10 +210,11 @@ int gdn_chunk_fwd_noalloc(const void* q, const void* k, const void* v,
  *
  * Every gradient is of the io dtype.  With bf16 io the operands of the products
  * (states, gradients of states and of the new values, scores) are fp16 with fp32
- * sums, which limits all of them alike (2^-14 .. 65504, fewer bits below); the gradients among them are kept times a
- * power of two, one for each (sequence, key head), that brings the largest |dout|
- * and |dht| of its v-heads to 2 .. 4, so gradients of any size keep their
- * precision, and one 2^-16 of that largest still has a bf16's.  A value past 65504
+ * sums, which limits all of them alike (2^-14 .. 65504, fewer bits below); the
+ * gradients among them are kept times a power of two, one for each (sequence, key
+ * head), that brings the largest |dout| and |dht| of its v-heads to 2 .. 4, so
+ * gradients of any size keep their precision, and one 2^-16 of that largest still
+ * has a bf16's.  A value past 65504
  * times that scale becomes an infinity; where dout or dht hold an infinity or NaN,
  * all gradients of that sequence and key head are NaN; one in v, a gate, beta or an
  * initial state can reach the other v-heads of its key head, in its sequence.
