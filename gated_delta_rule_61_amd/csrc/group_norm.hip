@@ -394,8 +394,8 @@ Walks walks_of(const GroupNormArgs& a, bool bwd) {
   if (step > rows) step = rows;
   // sums of weights per channel: a walk leaves two rows of them, so it takes four tokens at
   // least (1001 tokens of 16 groups of 80 in fp32: 8.7 us + 5 for the sums; no less in all
-  // with two)
-  if (bwd && !a.shared && a.dweight && step > (rows + 3) / 4) step = (rows + 3) / 4;
+  // with two), whichever of the sums is wanted: the size of the workspace tells nothing of that
+  if (bwd && !a.shared && (a.dweight || a.dbias) && step > (rows + 3) / 4) step = (rows + 3) / 4;
   Walks w;
   w.step = (int)step;
   w.blocks = (step * per + TPB - 1) / TPB;

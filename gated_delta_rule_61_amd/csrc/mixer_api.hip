@@ -240,7 +240,7 @@ size_t gdn_conv_bwd_workspace_bytes(int B, int T, int D, int W) {
   if (B < 0 || T < 0 || D <= 0 || D % 8 || W < 2 || W > 4) return 0;
   ConvBwdArgs a{};
   a.B = B; a.T = T; a.D = D; a.W = W;
-  a.dweight = &a;   // any: the size does not depend on which sums are wanted
+  a.dweight = &a;   // any: the size is the same for one of the sums and for both
   return conv_bwd_bytes(a);
 }
 
@@ -303,7 +303,7 @@ size_t gdn_group_norm_bwd_workspace_bytes(int B, int T, int G, int d, int weight
     return 0;
   GroupNormArgs a{};
   a.B = B; a.T = T; a.G = G; a.d = d; a.shared = weight_shared;
-  a.dweight = &a;   // any: the size does not depend on which sums are wanted
+  a.dweight = &a;   // any: the size is the same for one of the sums and for both
   return group_norm_bwd_bytes(a);
 }
 
