@@ -141,7 +141,7 @@ __global__ __launch_bounds__(64) void conv_bwd_kernel(ConvBwdArgs a, int run, in
           for (int e = 0; e < 8; ++e) {
             const float p = __builtin_amdgcn_rcpf(1.0f + __expf(-y[e]));
             y[e] *= p;
-            slope[e] = fmaf(-y[e], p, p + y[e]);   // p + silu (1 - p)
+            slope[e] = fmaf(y[e], 1.0f - p, p);   // y may be large: 1 - p is 0 there, p + y would round p away
           }
         } else {
 #pragma unroll
