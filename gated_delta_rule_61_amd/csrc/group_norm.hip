@@ -75,14 +75,25 @@ __device__ __forceinline__ void act_slope(float a, int kind, float& f, float& df
 template <int LPG, int NV>
 __device__ __forceinline__ float normalise(float (&x)[NV][8], const bool (&on)[NV], bool rms, float eps, float inv_d,
                                            float* sm) {
-  auto pass = [&](float add) -> float {   // centres x, returns the mean square + add
+  float k = 1.0f;
+  auto times = [&](float f) {
+    k *= f;
+#pragma unroll
+    for (int v = 0; v < NV; ++v)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x[v][e] *= f;
+  };
+  auto sum = [&]() -> float {
+    float s = 0.f;
+#pragma unroll
+    for (int v = 0; v < NV; ++v)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) s += x[v][e];
+    return group_sum<LPG>(s, sm);
+  };
+  auto pass = [&](float s) -> float {   // centres x with its sum s, returns the mean square + eps
     if (!rms) {
-      float s = 0.f;
-#pragma unroll
-      for (int v = 0; v < NV; ++v)
-#pragma unroll
-        for (int e = 0; e < 8; ++e) s += x[v][e];
-      const float mean = group_sum<LPG>(s, sm) * inv_d;
+      const float mean = s * inv_d;
 #pragma unroll
       for (int v = 0; v < NV; ++v)
 #pragma unroll
@@ -93,19 +104,25 @@ __device__ __forceinline__ float normalise(float (&x)[NV][8], const bool (&on)[N
     for (int v = 0; v < NV; ++v)
 #pragma unroll
       for (int e = 0; e < 8; ++e) q = fmaf(x[v][e], x[v][e], q);
-    return fmaf(group_sum<LPG>(q, sm), inv_d, add);
+    return fmaf(group_sum<LPG>(q, sm), inv_d, eps * k * k);   // k * k alone may pass fp32's largest number
   };
-  float q = pass(eps), k = 1.0f;
-  // Squares that leave fp32's range, or its normal numbers, where the reciprocal root
-  // takes 0 (the same in all threads of a group): once more from the group times a
-  // power of two, eps times its square.
+  // What leaves fp32's range, or its normal numbers, where the reciprocal root takes 0, is
+  // taken from the group times a power of two, eps times its square (the same in all
+  // threads of a group).  The sum, before anything is made from it: below 2^102 the mean is
+  // less than half a step of fp32's largest numbers, so x - mean is finite.  Then the
+  // squares: times 2^-80, 2^13 of any size have room.
+  float s = 0.f;
+  if (!rms) {
+    s = sum();
+    if (!(fabsf(s) <= 0x1p102f)) {
+      times(0x1p-80f);
+      s = sum();
+    }
+  }
+  float q = pass(s);
   if (!(q >= 0x1p-100f && q <= 0x1p100f)) {
-    k = q < 1.0f ? 0x1p100f : 0x1p-70f;
-#pragma unroll
-    for (int v = 0; v < NV; ++v)
-#pragma unroll
-      for (int e = 0; e < 8; ++e) x[v][e] *= k;
-    q = pass(eps * k * k);   // k * k alone may pass fp32's largest number
+    times(q < 1.0f ? 0x1p100f : 0x1p-80f);
+    q = pass(rms ? 0.f : sum());
   }
   const float r = __builtin_amdgcn_rsqf(q);
 #pragma unroll
