@@ -64,9 +64,12 @@ __device__ __forceinline__ float act_f(float a, int kind) {
   const float p = sigmoid_f(a);
   return kind == 0 ? a : kind == 1 ? a * p : p;
 }
+// 1 - p = e^-a p: the difference keeps nothing of it from a = 17 on.  (e^-a may be infinite,
+// where p is 0.)
 __device__ __forceinline__ void act_slope(float a, int kind, float& f, float& df) {
-  const float p = sigmoid_f(a);
-  const float q = p * (1.0f - p);
+  const float e = __expf(-a);
+  const float p = __builtin_amdgcn_rcpf(1.0f + e);
+  const float q = p * (fminf(e, 3.4028235e38f) * p);
   f = kind == 0 ? a : kind == 1 ? a * p : p;
   df = kind == 0 ? 1.0f : kind == 1 ? fmaf(a, q, p) : q;
 }

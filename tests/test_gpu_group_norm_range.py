@@ -1,5 +1,5 @@
 """GPU tests of the group norm and its gradients where fp32's range or precision
-ends: groups whose sums or squares leave it; and a bias without a
+ends: groups whose sums or squares leave it, saturated gates; and a bias without a
 weight.  Bounds: the running error analysis where values are ordinary ones, else as
 derived at each test."""
 
@@ -54,3 +54,64 @@ def test_small_variance_around_a_large_mean_without_eps():
     x = torch.stack([dev, 3 * dev, 2.0 ** -40 + dev.double().float()]).reshape(1, 3, 64)
     y = gdn.group_norm_fwd(d(x), 1, activation=None, rms=False, eps=0.0)
     close("y", f64(y)[0], np.sign(f64(dev))[None].repeat(3, 0), np.full((3, 64), 2.0 ** -19))
+
+
+SATURATED = [0.0, 3.0, 8.0, 11.0, 12.5, 15.0, 17.0, 20.0, 30.0, 60.0, 80.0, 200.0, 1e4, 1e30]
+
+
+def slope(a, act):
+    """act'(a) without cancellation; e^{-|a|} underflows to 0 in 64 bits where fp32's is 0 long before"""
+    e = np.exp(-np.abs(a))
+    q = e / (1 + e) ** 2
+    if act == "sigmoid":
+        return q
+    return np.where(a >= 0, 1.0, e) / (1 + e) + a * q
+
+
+def slope_bound(a, act):
+    """exp's argument is scaled by log2(e) first, one rounding of its size: (|a| 2^-23 + 2^-22) of e^{-a}, the
+    reciprocal 2^-22 of its own, twice, the product three roundings; taken twice: 2^-19 + |a| 2^-22 of a (1 - p) p.
+    Below 2^-125 nothing is asked for.  silu adds a times that, and p, which is as good."""
+    e = np.exp(-np.abs(a))
+    q = e / (1 + e) ** 2
+    rel = 2.0 ** -19 + np.minimum(np.abs(a), 200) * 2.0 ** -22
+    if act == "sigmoid":
+        return rel * q + 2.0 ** -125
+    return rel * (np.where(a >= 0, 1.0, e) / (1 + e) + np.abs(a) * q) + 2.0 ** -125
+
+
+@pytest.mark.parametrize("act", ["sigmoid", "silu"])
+@pytest.mark.parametrize("io", [BF, F32])
+def test_saturated_gates(act, io):
+    v = torch.tensor(SATURATED + [-s for s in SATURATED] + [0.0] * 4)
+    z = v.repeat(2).reshape(1, 1, 64).to(io)
+    x = torch.ones(1, 1, 64, dtype=io)
+    x[..., ::3] = -1
+    dy = (randn(1, 1, 1, 64).abs() + 0.5).to(io)
+    _, dz, _, _ = gdn.group_norm_bwd(d(dy), d(x), 1, z=d(z), activation=act, rms=True, eps=0.0)
+    zz, a = f64(z), f64(dy) * f64(x)     # n is x to 2^-21
+    ref = a * slope(zz, act)
+    bar = np.abs(a) * slope_bound(zz, act) + 2.0 ** -20 * np.abs(ref)
+    close("dz", f64(dz), ref, bar + (2.0 ** -8 if io == BF else 2.0 ** -24) * (np.abs(ref) + bar))
+
+
+@pytest.mark.parametrize("act", ["sigmoid", "silu"])
+def test_saturated_results(act):
+    # one token: dbias = dy act'(n w), with n = 1 to 2^-21, so the argument is good to 2^-21 of itself
+    w = torch.tensor([s for s in SATURATED if s < 100] + [-s for s in SATURATED if s < 100] + [1.0] * 2)
+    x = torch.ones(1, 1, w.numel())
+    dy = randn(2, 1, 1, w.numel()).abs() + 0.5
+    _, _, _, db = gdn.group_norm_bwd(d(dy), d(x), 1, d(w), d(torch.zeros_like(w)), activation=act, rms=True, eps=0.0)
+    a = f64(w)
+    ref = f64(dy)[0, 0] * slope(a, act)
+    shift = np.abs(a) * 2.0 ** -20          # of the argument; the slopes' logarithms change by at most that ..
+    size = f64(dy)[0, 0] * (slope_bound(a, act) + shift * slope_bound(a, act) / (2.0 ** -19 + np.abs(a) * 2.0 ** -22))
+    close("dbias", f64(db), ref, 2 * size)
+
+
+def test_forward_of_saturated_gates_is_unchanged_in_its_limits():
+    z = torch.tensor([[[200.0, -200.0, 1e30, -1e30, 30.0, -30.0, float("inf"), 0.0]]])
+    x = torch.ones(1, 1, 8)
+    y = gdn.group_norm_fwd(d(x), 1, z=d(z), activation="sigmoid", rms=True, eps=0.0)
+    ref = np.array([[[1, 0, 1, 0, 1 / (1 + np.exp(-30.0)), 1 / (1 + np.exp(30.0)), 1, 0.5]]])
+    close("y", f64(y), ref, 2.0 ** -18 * ref + 2.0 ** -125)
