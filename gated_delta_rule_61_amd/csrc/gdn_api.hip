@@ -692,7 +692,7 @@ int gdn_decode(const void* q, const void* k, const void* v, const void* a, const
   d.q = q; d.k = k; d.v = v; d.a = a; d.b = b; d.A_log = A_log; d.dt_bias = dt_bias;
   d.state = state; d.idx = state_indices; d.o = o;
   d.B = B; d.T = T; d.H = H; d.HV = HV; d.K = K; d.V = V; d.pool = pool;
-  d.scale = scale; d.sp_beta = softplus_beta; d.sp_thr = softplus_threshold; d.eps = eps;
+  d.scale = scale; d.sp_beta = softplus_beta; d.sp_thr = softplus_cut(softplus_threshold); d.eps = eps;
   d.use_norm = use_qk_l2norm != 0;
   prof_begin(GDN_STAGE_DECODE, (hipStream_t)stream);
   const hipError_t e = launch_decode(d, (hipStream_t)stream);

@@ -12,6 +12,10 @@ namespace gdn {
 void prof_begin(int stage, hipStream_t s);
 void prof_end(int stage, hipStream_t s);
 
+// Up to where the steps form softplus(x) as log(1 + e^x): the caller's threshold, but no
+// further than e^x is finite.  From x = 80 on it is x to the last bit.
+inline float softplus_cut(float threshold) { return threshold > 80.f ? 80.f : threshold; }
+
 struct DecodeArgs {
   const void *q, *k, *v, *a, *b;
   const float *A_log, *dt_bias;

@@ -365,7 +365,7 @@ int kda_decode(const void* q, const void* k, const void* v, const void* a, const
   s.q = q; s.k = k; s.v = v; s.a = a; s.b = b; s.A_log = A_log; s.dt_bias = dt_bias;
   s.state = state; s.state_bf16 = state_dtype == GDN_DTYPE_BF16; s.idx = state_indices; s.pool = pool; s.o = o;
   s.B = B; s.T = T; s.H = H; s.HV = HV; s.K = K; s.V = V;
-  s.scale = scale; s.sp_beta = softplus_beta; s.sp_thr = softplus_threshold; s.eps = eps;
+  s.scale = scale; s.sp_beta = softplus_beta; s.sp_thr = softplus_cut(softplus_threshold); s.eps = eps;
   s.use_norm = use_qk_l2norm != 0; s.bf16 = dtype == GDN_DTYPE_BF16;
   return timed(GDN_STAGE_DECODE, stream, [&](hipStream_t st) { return launch_kda_decode(s, st); });
 }
