@@ -28,6 +28,7 @@
 
 #include "gdn_device.h"
 #include "mixer_launch.h"
+#include "ssm_rate.h"
 #include "state_rows.h"
 
 namespace gdn {
@@ -61,6 +62,13 @@ __device__ __forceinline__ float row_sum_each(const float (&x)[8], int cl) {
   float r = choose(b0, q, p) + dpp_f<0xB1>(choose(b0, p, q));
   if constexpr (LPR == 16) r += dpp_f<0x128>(r);   // the lane 8 further on
   return r;
+}
+
+// exp(A_log) step for A_log > FAST_RATE: step is softplus(bu) / beta where `soft`, which
+// underflows where the product may not (there it is e^bu / beta).
+__device__ __forceinline__ double fast_rate(float A_log, float bu, bool soft, float step, float beta) {
+  if (soft && bu < -20.f) return (double)expf((float)((double)A_log + (double)bu)) / (double)beta;
+  return rate_of(A_log) * (double)step;
 }
 
 // T: io type, S: pool type.  A thread holds R = 8 consecutive state rows.
@@ -101,13 +109,17 @@ __global__ __launch_bounds__(V * K / 64) __attribute__((amdgpu_waves_per_eu(4)))
     const int t = i / (V / 4), r = i % (V / 4) * 4;
     load4(vp + (size_t)t * a.HV * V + r, &vs[t][r]);
   }
-  const float A = -expf(a.A_log[hv]);
+  const float A_log = a.A_log[hv];
+  const float A = -expf(A_log);
+  const bool fast = A_log > FAST_RATE;   // uniform
   for (int i = threadIdx.x; i < TT * K; i += TPB) {
     const int t = i / K, c = i % K;
     const float u = to_f(ap[(size_t)t * a.HV * K + c]) + a.dt_bias[(size_t)hv * K + c];
     const float bu = a.sp_beta * u;
     const float step = bu <= a.sp_thr ? log1pf(expf(bu)) / a.sp_beta : u;
-    gate[t][c] = step == 0.f ? 1.f : expf(A * step);   // A may be infinite
+    float Ad = A * step;
+    if (fast) Ad = -(float)fast_rate(A_log, bu, bu <= a.sp_thr, step, a.sp_beta);
+    gate[t][c] = expf(Ad);
   }
   // q, k and the scalars of a token: LPR lanes of the last wave each
   if (const int t = ((int)threadIdx.x - (TPB - 64)) / LPR; (int)threadIdx.x >= TPB - 64 && t < TT) {
