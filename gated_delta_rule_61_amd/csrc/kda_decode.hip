@@ -64,6 +64,27 @@ __device__ __forceinline__ float row_sum_each(const float (&x)[8], int cl) {
   return r;
 }
 
+// sqrt(sum of x^2 + eps) of a row of LPR lanes.  Squares that leave fp32's range or
+// its normal numbers: x becomes x times a power of two, and the result is of that.
+template <int LPR>
+__device__ __forceinline__ float row_norm(float (&x)[8], float eps) {
+  float s = 0.f;
+#pragma unroll
+  for (int c = 0; c < 8; ++c) s = fmaf(x[c], x[c], s);
+  s = row_sum<LPR>(s) + eps;
+  if (!(s >= 0x1p-100f && s <= 0x1p100f)) {
+    const float f = s < 1.f ? 0x1p100f : 0x1p-80f;
+    s = 0.f;
+#pragma unroll
+    for (int c = 0; c < 8; ++c) {
+      x[c] *= f;
+      s = fmaf(x[c], x[c], s);
+    }
+    s = row_sum<LPR>(s) + eps * f * f;
+  }
+  return sqrtf(s);
+}
+
 // exp(A_log) step for A_log > FAST_RATE: step is softplus(bu) / beta where `soft`, which
 // underflows where the product may not (there it is e^bu / beta).
 __device__ __forceinline__ double fast_rate(float A_log, float bu, bool soft, float step, float beta) {
@@ -132,19 +153,15 @@ __global__ __launch_bounds__(V * K / 64) __attribute__((amdgpu_waves_per_eu(4)))
     load4(kp, k);
     load4(kp + second, k + 4);
     const float bt = to_f(reinterpret_cast<const T*>(a.b)[(tok0 + t) * a.HV + hv]);
-    float sq = 0.f, sk = 0.f, kq = 0.f;
-#pragma unroll
-    for (int c = 0; c < 8; ++c) {
-      sq = fmaf(q[c], q[c], sq);
-      sk = fmaf(k[c], k[c], sk);
-      kq = fmaf(k[c], q[c], kq);
-    }
-    kq = row_sum<LPR>(kq);
     float qs = a.scale, ks = 1.f;
     if (a.use_norm) {
-      qs = a.scale / sqrtf(row_sum<LPR>(sq) + a.eps);
-      ks = 1.f / sqrtf(row_sum<LPR>(sk) + a.eps);
+      qs = a.scale / row_norm<LPR>(q, a.eps);
+      ks = 1.f / row_norm<LPR>(k, a.eps);
     }
+    float kq = 0.f;
+#pragma unroll
+    for (int c = 0; c < 8; ++c) kq = fmaf(k[c], q[c], kq);
+    kq = row_sum<LPR>(kq);
     float* const kw = &kn[t][c0];
     float* const qw = &qn[t][c0];
     *reinterpret_cast<f32x4*>(kw) = f32x4{k[0], k[1], k[2], k[3]} * ks;

@@ -1,5 +1,6 @@
-"""GPU tests of the steps where their gates leave fp32's range on the way: thresholds
-past exp's largest argument, rates exp(A_log) past fp32."""
+"""GPU tests of the steps where their gates or norms leave fp32's range on the way:
+thresholds past exp's largest argument, rates exp(A_log) past fp32, rows whose squares
+fp32 does not hold."""
 
 import numpy as np
 import pytest
@@ -60,3 +61,16 @@ def test_rates_past_fp32_times_small_steps(A, sb):
     rate = np.exp(A + bu) / sb * np.where(bu < -30, 1.0, np.log1p(np.exp(near)) / np.exp(near))
     ref = f64(i["state"]) * np.exp(-rate)
     close("state", f64(g["state"]), ref, np.abs(f64(i["state"])) * np.exp(-rate) * (rate * 2.0 ** -19 + 2.0 ** -20) + 2.0 ** -125)
+
+
+@pytest.mark.parametrize("io", [BF, F32])
+@pytest.mark.parametrize("K,V", [(64, 64), (128, 128)])
+def test_rows_whose_squares_leave_fp32(K, V, io):
+    i = make(4, 4, 2, 2, 2, K, V, io, F32)
+    size = torch.tensor([1e25, 1e-25, 3e37, 1.0])[:, None, None, None]
+    i["q"] = (i["q"].float() * size.flip(0)).to(io)
+    i["k"] = (i["k"].float() * size).to(io)
+    check(i, eps=0.0)
+    i["k"][1:2] = i["k"][3:4]                 # with eps, 1e-25 is as good as 0
+    i["q"][2:3] = i["q"][0:1]
+    check(i)
