@@ -711,15 +711,18 @@ def chunk_bwd_workspace_bytes(B: int, T: int, Hk: int, HV: int, K: int, V: int, 
 def gdn_chunk_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: Optional[torch.Tensor], beta: torch.Tensor,
                   dout: torch.Tensor, dht: Optional[torch.Tensor] = None, scale: Optional[float] = None,
                   h0: Optional[torch.Tensor] = None, cu_seqlens: Optional[torch.Tensor] = None, chunk_size: int = 64,
-                  g_gamma: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None):
+                  g_gamma: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                  output_dg: Optional[bool] = None):
     """Gradients of ``gdn_chunk_fwd`` from ``dout`` [B,T,HV,V], that of its output
     (io dtype), and ``dht`` [N,HV,V,K] fp32, that of its final states (None:
     zeros); the other arguments as they were given there.  Returns (dq, dk, dv,
-    dg, dbeta, dh0) in the io dtype, of the shapes of q, k, v, g, beta and h0;
-    dg is None without ``g``, dh0 without ``h0``; rows behind the last boundary of
-    ``cu_seqlens`` are not written (they hold whatever the new memory held).  A
-    ``workspace`` (of ``chunk_bwd_workspace_bytes``; else allocated) serves one
-    call at a time."""
+    dg, dbeta, dh0) in the io dtype, of the shapes of q, k, v, beta, beta and h0;
+    dh0 is None without ``h0``, and dg without ``g`` unless ``output_dg`` is True:
+    it is the gradient of every token's log-gate, so that of ``g_gamma`` is its sum
+    over the tokens (``dg.float().sum((0, 1))``); False leaves it out.  Rows behind
+    the last boundary of ``cu_seqlens`` are not written (they hold whatever the new
+    memory held).  A ``workspace`` (of ``chunk_bwd_workspace_bytes``; else
+    allocated) serves one call at a time."""
     if q.dim() != 4 or v.dim() != 4:
         raise ValueError("q, k must be [B, T, Hk, K] and v [B, T, HV, V]")
     dev = _cuda(q, "q")
@@ -731,7 +734,9 @@ def gdn_chunk_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: Optional
     _want(dout, "dout", io, v.shape, dev)
     _want(dht, "dht", torch.float32, (N, HV, V, K), dev)
     dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
-    dg = None if g is None else torch.empty((B, T, HV), dtype=io, device=dev)
+    if output_dg is None:
+        output_dg = g is not None
+    dg = torch.empty((B, T, HV), dtype=io, device=dev) if output_dg else None
     dbeta = torch.empty((B, T, HV), dtype=io, device=dev)
     dh0 = None if h0 is None else torch.empty((N, HV, V, K), dtype=io, device=dev)
     L, code = lib(), _io_code(io)
