@@ -21,6 +21,7 @@ LIB_PATH = os.path.join(_HERE, "libgdn61.so")
 
 GDN_DTYPE_F32 = 0
 GDN_DTYPE_BF16 = 1
+GDN_ROWS_ZERO = 0x100
 GDN_Q8_INT8 = 0
 GDN_Q8_E4M3 = 1
 
@@ -720,9 +721,8 @@ def gdn_chunk_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: Optional
     dh0 is None without ``h0``, and dg without ``g`` unless ``output_dg`` is True:
     it is the gradient of every token's log-gate, so that of ``g_gamma`` is its sum
     over the tokens (``dg.float().sum((0, 1))``); False leaves it out.  Rows behind
-    the last boundary of ``cu_seqlens`` are not written (they hold whatever the new
-    memory held).  A ``workspace`` (of ``chunk_bwd_workspace_bytes``; else
-    allocated) serves one call at a time."""
+    the last boundary of ``cu_seqlens`` are zeros.  A ``workspace`` (of
+    ``chunk_bwd_workspace_bytes``; else allocated) serves one call at a time."""
     if q.dim() != 4 or v.dim() != 4:
         raise ValueError("q, k must be [B, T, Hk, K] and v [B, T, HV, V]")
     dev = _cuda(q, "q")
@@ -744,7 +744,8 @@ def gdn_chunk_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: Optional
     workspace, wp = _scratch(workspace, nbytes, dev)
     _call(dev, L.gdn_chunk_bwd, _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(g_gamma), _ptr(beta),
           K ** -0.5 if scale is None else scale, _ptr(h0), _ptr(dout), _ptr(dht), _ptr(cu_seqlens), N, B, T, Hk, HV, K, V,
-          chunk_size, code, _ptr(dq), _ptr(dk), _ptr(dv), _ptr(dg), _ptr(dbeta), _ptr(dh0), wp, nbytes)
+          chunk_size, code if cu_seqlens is None else code | GDN_ROWS_ZERO, _ptr(dq), _ptr(dk), _ptr(dv), _ptr(dg),
+          _ptr(dbeta), _ptr(dh0), wp, nbytes)
     return dq, dk, dv, dg, dbeta, dh0
 
 
@@ -756,9 +757,8 @@ def causal_conv_bwd(dout, x: torch.Tensor, weight: torch.Tensor, bias: Optional[
     zeros).  ``dout``: the gradient of its result, one tensor or with
     ``sections`` a tuple, packed; the other arguments as they were given there.
     Returns (dx [B,T,D], dweight [D,W], dbias [D] or None without a bias) in the
-    io dtype; dx's rows behind the last boundary of ``cu_seqlens`` are not written
-    (they hold whatever the new memory held).  A ``workspace`` (else allocated)
-    serves one call at a time."""
+    io dtype; dx's rows behind the last boundary of ``cu_seqlens`` are zeros.  A
+    ``workspace`` (else allocated) serves one call at a time."""
     douts = (dout,) if isinstance(dout, torch.Tensor) else tuple(dout)
     head, (B, T, D, W, code), _, _, _, dev = _conv_args(x, weight, bias, activation, sections, None, douts, "dout")
     N, cu = _seqs(cu_seqlens, B, dev)
@@ -769,7 +769,7 @@ def causal_conv_bwd(dout, x: torch.Tensor, weight: torch.Tensor, bias: Optional[
     workspace, wp = _scratch(workspace, nbytes, dev)
     xp, xb, xt, wptr, bptr, silu = head[:6]
     _call(dev, L.gdn_conv_bwd, *head[6:], xp, xb, xt, wptr, bptr, silu, norm_dim, norm_sections, norm_eps, cu, N, B, T,
-          D, W, code, dx.data_ptr(), dw.data_ptr(), _ptr(db), wp, nbytes)
+          D, W, code if cu is None else code | GDN_ROWS_ZERO, dx.data_ptr(), dw.data_ptr(), _ptr(db), wp, nbytes)
     return dx, dw, db
 
 

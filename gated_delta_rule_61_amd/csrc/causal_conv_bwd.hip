@@ -216,6 +216,11 @@ __global__ __launch_bounds__(64) void conv_bwd_kernel(ConvBwdArgs a, int run, in
       }
     }
   }
+  if (a.zero_rows && a.cu && live) {   // the run's rows behind the last sequence
+    const long long last = bound(a.N);
+    const float none[8] = {};
+    for (long long t = last > t0 ? last : t0; t < t1; ++t) put8(dxb + t * a.D, none);
+  }
   if (live && (a.dweight || a.dbias)) {
     float* out = a.partial + (size_t)r * (W + 1) * a.D + c;
 #pragma unroll

@@ -131,6 +131,7 @@ struct ChunkBwdArgs {
   void *hs, *ds;         // [chunks, HV, V, K] states at the chunks' starts, gradients at their ends
   void *vn, *dr;         // [chunks, HV, V, 64] new values, their gradients, a column a row
   int nslots;            // chunks that these hold
+  int zero_rows;         // rows behind the last boundary become zeros
 };
 hipError_t launch_chunk_bwd_amax(const ChunkBwdArgs& a, hipStream_t s);
 hipError_t launch_chunk_bwd_scan(const ChunkBwdArgs& a, hipStream_t s);

@@ -249,6 +249,8 @@ int gdn_conv_bwd(const void* dout0, const void* dout1, const void* dout2, int wi
                  int norm_dim, int norm_sections, float norm_eps, const int64_t* cu_seqlens, int num_seqs, int B,
                  int T, int D, int W, int dtype, void* dx, void* dweight, void* dbias, void* workspace,
                  size_t workspace_bytes, void* stream) {
+  const int zero_rows = dtype & GDN_ROWS_ZERO;
+  dtype &= ~GDN_ROWS_ZERO;
   // the checks of the forward convolution, dout in the place of its outputs
   ConvArgs f{};
   f.x = {x, x_batch, x_token};
@@ -273,7 +275,7 @@ int gdn_conv_bwd(const void* dout0, const void* dout1, const void* dout2, int wi
   a.end[0] = f.end[0]; a.end[1] = f.end[1]; a.end[2] = f.end[2];
   a.norm_dim = norm_dim; a.norm_sections = norm_sections; a.eps = norm_eps; a.silu = silu;
   a.dx = dx; a.dweight = dweight; a.dbias = dbias;
-  a.cu = cu_seqlens; a.N = f.N; a.B = B; a.T = T; a.D = D; a.W = W; a.bf16 = f.bf16;
+  a.cu = cu_seqlens; a.zero_rows = zero_rows; a.N = f.N; a.B = B; a.T = T; a.D = D; a.W = W; a.bf16 = f.bf16;
   if (int st = check_workspace(workspace, workspace_bytes, conv_bwd_bytes(a))) return st;
   a.partial = (float*)workspace;
   return timed(GDN_STAGE_CONV_BWD, stream, [&](hipStream_t s) { return launch_conv_bwd(a, s); });

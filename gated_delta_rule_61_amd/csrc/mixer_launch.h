@@ -120,6 +120,7 @@ struct ConvBwdArgs {
   void *dweight, *dbias;        // [D, W], [D] (nullptr: not wanted)
   float* partial;               // workspace: sums of the runs
   const int64_t* cu;            // [N + 1] or nullptr (dense)
+  int zero_rows;                // rows behind the last boundary become zeros
   int N, B, T, D, W;
   int bf16;
 };

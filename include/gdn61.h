@@ -224,8 +224,11 @@ int gdn_chunk_fwd_noalloc(const void* q, const void* k, const void* v,
  * same bits in every run.  Supported sizes and errors as in
  * gdn_chunk_fwd; also GDN_ERR_UNSUPPORTED where HV * V reaches 2^23, or a launch
  * would hold 2^32 threads.  T = 0 (or all sequences empty) is valid: dh0 = dht (or
- * zeros) is written.  Rows behind the last boundary are left as they are.
+ * zeros) is written.  Rows behind the last boundary are left as they are, or with
+ * dtype | GDN_ROWS_ZERO become zeros, as what takes gradients of all rows needs
+ * (the products with them that make a projection's).
  */
+enum { GDN_ROWS_ZERO = 0x100 };
 size_t gdn_chunk_bwd_workspace_bytes(int B, int T, int Hk, int HV, int K, int V, int num_seqs, int varlen,
                                      int dtype);
 int gdn_chunk_bwd(const void* q, const void* k, const void* v, const float* g, const float* g_gamma,
@@ -537,7 +540,8 @@ int gdn_conv_step(const void* x, long long x_batch, long long x_token, const voi
  *   x, weight, bias, silu, norm_*, cu_seqlens, ...   as in gdn_conv_fwd; c is
  *                               computed again from them
  *   dx           [B, T, D]      io dtype out, packed; rows behind the last
- *                               boundary are left as they are
+ *                               boundary are left as they are, or with dtype |
+ *                               GDN_ROWS_ZERO become zeros
  *   dweight      [D, W]         io dtype out, or NULL
  *   dbias        [D]            io dtype out, or NULL (also without a bias)
  *   workspace    device buffer of gdn_conv_bwd_workspace_bytes() bytes, 256-byte
