@@ -22,6 +22,7 @@ LIB_PATH = os.path.join(_HERE, "libgdn61.so")
 GDN_DTYPE_F32 = 0
 GDN_DTYPE_BF16 = 1
 GDN_ROWS_ZERO = 0x100
+GDN_GRADS_F32 = 0x200
 GDN_Q8_INT8 = 0
 GDN_Q8_E4M3 = 1
 
@@ -713,11 +714,12 @@ def gdn_chunk_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: Optional
                   dout: torch.Tensor, dht: Optional[torch.Tensor] = None, scale: Optional[float] = None,
                   h0: Optional[torch.Tensor] = None, cu_seqlens: Optional[torch.Tensor] = None, chunk_size: int = 64,
                   g_gamma: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
-                  output_dg: Optional[bool] = None):
+                  output_dg: Optional[bool] = None, grads_in_fp32: bool = False):
     """Gradients of ``gdn_chunk_fwd`` from ``dout`` [B,T,HV,V], that of its output
     (io dtype), and ``dht`` [N,HV,V,K] fp32, that of its final states (None:
     zeros); the other arguments as they were given there.  Returns (dq, dk, dv,
-    dg, dbeta, dh0) in the io dtype, of the shapes of q, k, v, beta, beta and h0;
+    dg, dbeta, dh0) in the io dtype (the last three in fp32 with ``grads_in_fp32``,
+    as g, beta and h0 are), of the shapes of q, k, v, beta, beta and h0;
     dh0 is None without ``h0``, and dg without ``g`` unless ``output_dg`` is True:
     it is the gradient of every token's log-gate, so that of ``g_gamma`` is its sum
     over the tokens (``dg.float().sum((0, 1))``); False leaves it out.  Rows behind
@@ -736,16 +738,17 @@ def gdn_chunk_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: Optional
     dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
     if output_dg is None:
         output_dg = g is not None
-    dg = torch.empty((B, T, HV), dtype=io, device=dev) if output_dg else None
-    dbeta = torch.empty((B, T, HV), dtype=io, device=dev)
-    dh0 = None if h0 is None else torch.empty((N, HV, V, K), dtype=io, device=dev)
+    gdt = torch.float32 if grads_in_fp32 else io
+    dg = torch.empty((B, T, HV), dtype=gdt, device=dev) if output_dg else None
+    dbeta = torch.empty((B, T, HV), dtype=gdt, device=dev)
+    dh0 = None if h0 is None else torch.empty((N, HV, V, K), dtype=gdt, device=dev)
     L, code = lib(), _io_code(io)
     nbytes = int(L.gdn_chunk_bwd_workspace_bytes(B, T, Hk, HV, K, V, N, 0 if cu_seqlens is None else 1, code))
+    code |= (0 if cu_seqlens is None else GDN_ROWS_ZERO) | (GDN_GRADS_F32 if grads_in_fp32 else 0)
     workspace, wp = _scratch(workspace, nbytes, dev)
     _call(dev, L.gdn_chunk_bwd, _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(g_gamma), _ptr(beta),
           K ** -0.5 if scale is None else scale, _ptr(h0), _ptr(dout), _ptr(dht), _ptr(cu_seqlens), N, B, T, Hk, HV, K, V,
-          chunk_size, code if cu_seqlens is None else code | GDN_ROWS_ZERO, _ptr(dq), _ptr(dk), _ptr(dv), _ptr(dg),
-          _ptr(dbeta), _ptr(dh0), wp, nbytes)
+          chunk_size, code, _ptr(dq), _ptr(dk), _ptr(dv), _ptr(dg), _ptr(dbeta), _ptr(dh0), wp, nbytes)
     return dq, dk, dv, dg, dbeta, dh0
 
 

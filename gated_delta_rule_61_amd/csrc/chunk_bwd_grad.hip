@@ -448,8 +448,14 @@ __global__ __launch_bounds__(NTHREADS) __attribute__((amdgpu_waves_per_eu(sizeof
         }
         if (live) {
           const size_t at = (size_t)(c0 + lane) * HV + j;
-          if (a.dg) reinterpret_cast<T*>(a.dg)[at] = from_f<T>((dG + cross) * inv);
-          reinterpret_cast<T*>(a.dbeta)[at] = from_f<T>((sVdr[lane] + sVdr[BT + lane] + d[1]) * inv);
+          const float dg = (dG + cross) * inv, db = (sVdr[lane] + sVdr[BT + lane] + d[1]) * inv;
+          if (a.f32) {
+            if (a.dg) reinterpret_cast<float*>(a.dg)[at] = dg;
+            reinterpret_cast<float*>(a.dbeta)[at] = db;
+          } else {
+            if (a.dg) reinterpret_cast<T*>(a.dg)[at] = from_f<T>(dg);
+            reinterpret_cast<T*>(a.dbeta)[at] = from_f<T>(db);
+          }
         }
       }
     }

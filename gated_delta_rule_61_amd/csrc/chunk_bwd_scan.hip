@@ -414,9 +414,13 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
   if (back) walk(tiles::Stage1{});
   else walk(tiles::Stage0{});
   if (back && a.dh0) {
-    T* out = reinterpret_cast<T*>(a.dh0) + sbase;
 #pragma unroll
-    for (int s = 0; s < KS; ++s) store_io8(out + 32 * s + 8 * g, both(S[2 * s], S[2 * s + 1]) * inv);
+    for (int s = 0; s < KS; ++s) {
+      const f32x8 x = both(S[2 * s], S[2 * s + 1]) * inv;
+      const size_t at = sbase + 32 * s + 8 * g;
+      if (a.f32) store_io8(reinterpret_cast<float*>(a.dh0) + at, x);
+      else store_io8(reinterpret_cast<T*>(a.dh0) + at, x);
+    }
   }
 }
 

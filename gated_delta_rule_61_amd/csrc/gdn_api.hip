@@ -133,7 +133,7 @@ __global__ __launch_bounds__(1024) void bwd_tables_kernel(ChunkBwdArgs a) {
       const size_t at = (size_t)t * f.HV + j;
       for (void* p : {a.dg, a.dbeta}) {
         if (!p) continue;
-        if (eb == 2) reinterpret_cast<uint16_t*>(p)[at] = 0;
+        if (eb == 2 && !a.f32) reinterpret_cast<uint16_t*>(p)[at] = 0;
         else reinterpret_cast<uint32_t*>(p)[at] = 0;
       }
     }
@@ -453,7 +453,7 @@ int gdn_chunk_fwd(const void* q, const void* k, const void* v, const float* g,
 size_t gdn_chunk_bwd_workspace_bytes(int B, int T, int Hk, int HV, int K, int V, int num_seqs, int varlen,
                                      int dtype) {
   if (B < 0 || T < 0 || Hk <= 0 || HV <= 0 || K <= 0 || V <= 0 || num_seqs < 0) return 0;
-  dtype &= ~GDN_ROWS_ZERO;
+  dtype &= ~(GDN_ROWS_ZERO | GDN_GRADS_F32);
   if (dtype != GDN_DTYPE_F32 && dtype != GDN_DTYPE_BF16) return 0;
   if ((long long)B * T >= (1LL << 31) / 64) return 0;
   return bwd_workspace_layout(B, T, HV, K, V, varlen ? num_seqs : B, varlen != 0, dtype == GDN_DTYPE_BF16).total;
@@ -465,8 +465,8 @@ int gdn_chunk_bwd(const void* q, const void* k, const void* v, const float* g, c
                   int chunk_size, int dtype, void* dq, void* dk, void* dv, void* dg, void* dbeta, void* dh0,
                   void* workspace, size_t workspace_bytes, void* stream) {
   Problem P;
-  const int zero_rows = dtype & GDN_ROWS_ZERO;
-  dtype &= ~GDN_ROWS_ZERO;
+  const int zero_rows = dtype & GDN_ROWS_ZERO, grads_f32 = dtype & GDN_GRADS_F32;
+  dtype &= ~(GDN_ROWS_ZERO | GDN_GRADS_F32);
   int st = check_chunk(q, k, v, g, false, beta, h0, nullptr, nullptr, 64, 0, GDN_DTYPE_F32, cu_seqlens, num_seqs, B,
                        T, Hk, HV, K, V, chunk_size, dtype, dout, P);
   if (st != GDN_OK) return st;
@@ -511,6 +511,7 @@ int gdn_chunk_bwd(const void* q, const void* k, const void* v, const float* g, c
   a.hs = ws + L.hs; a.ds = ws + L.ds; a.vn = ws + L.vn; a.dr = ws + L.dr;
   a.nslots = L.nslots;
   a.zero_rows = zero_rows;
+  a.f32 = grads_f32;
   const hipError_t e = launch_chunk_bwd(a, (hipStream_t)stream);
   if (e != hipSuccess) return fail(GDN_ERR_LAUNCH, "HIP launch failed: %s", hipGetErrorString(e));
   return ok();

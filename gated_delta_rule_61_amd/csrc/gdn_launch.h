@@ -125,6 +125,7 @@ struct ChunkBwdArgs {
   void *dq, *dk, *dv;    // [B, T, Hk, K] x 2, [B, T, HV, V]
   void *dg, *dbeta;      // [B, T, HV]; dg may be nullptr
   void* dh0;             // [N, HV, V, K] or nullptr
+  int f32;               // dg, dbeta and dh0 in fp32 (else the io dtype)
   // workspace
   uint32_t *amax_dht, *part;   // bf16 io: bits of the largest |dht| [N, HV], |dout| [chunks, 4, HV]
   uint32_t* amax;        // [N, Hk] ... of both and of a key head's v-heads; nullptr with fp32 io

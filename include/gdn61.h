@@ -50,7 +50,8 @@
  *     chunk_h.py", chunk_fwd_h / chunk_bwd_dh: states in the input dtype
  *     unless states_in_fp32).  A bf16 state is the fp32 state rounded to
  *     nearest, ties to even.  Initial and final states (h0, ht, dht, dh0)
- *     are always fp32.  A stored-state buffer comes with its capacity in
+ *     are always fp32, but for the dh0 of gdn_chunk_bwd, which has a choice.
+ *     A stored-state buffer comes with its capacity in
  *     entries of [HV, V, K]: without cu_seqlens a buffer smaller than the
  *     call needs is rejected (GDN_ERR_INVALID_ARGUMENT); with cu_seqlens
  *     (whose values the host never reads) entries at or past the capacity
@@ -203,12 +204,15 @@ int gdn_chunk_fwd_noalloc(const void* q, const void* k, const void* v,
  *                               log-gate (with g_gamma too: its tokens' sum is that
  *                               of the head's fixed decay)
  *   dbeta        [B, T, HV]     io dtype out
- *   dh0          [N, HV, V, K]  io dtype out, or NULL (also without h0)
+ *   dh0          [N, HV, V, K]  io dtype out, or NULL (also without h0).  With
+ *                               dtype | GDN_GRADS_F32 dg, dbeta and dh0 are fp32,
+ *                               as g, beta and h0 are: dh0 can then be passed on
+ *                               as the dht of the segment before
  *   workspace    device buffer of gdn_chunk_bwd_workspace_bytes() bytes, 256-byte
  *                aligned (varlen: whether cu_seqlens is given).  Calls that share
  *                one (captured graphs too) must not run at the same time.
  *
- * Every gradient is of the io dtype.  With bf16 io the operands of the products
+ * Every gradient is of the io dtype but for that.  With bf16 io the operands of the products
  * (states, gradients of states and of the new values, scores) are fp16 with fp32
  * sums, which limits all of them alike (2^-14 .. 65504, fewer bits below); the
  * gradients among them are kept times a power of two, one for each (sequence, key
@@ -228,7 +232,7 @@ int gdn_chunk_fwd_noalloc(const void* q, const void* k, const void* v,
  * dtype | GDN_ROWS_ZERO become zeros, as what takes gradients of all rows needs
  * (the products with them that make a projection's).
  */
-enum { GDN_ROWS_ZERO = 0x100 };
+enum { GDN_ROWS_ZERO = 0x100, GDN_GRADS_F32 = 0x200 };
 size_t gdn_chunk_bwd_workspace_bytes(int B, int T, int Hk, int HV, int K, int V, int num_seqs, int varlen,
                                      int dtype);
 int gdn_chunk_bwd(const void* q, const void* k, const void* v, const float* g, const float* g_gamma,

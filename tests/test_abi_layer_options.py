@@ -31,3 +31,13 @@ def test_no_sequences(L):  # noqa: F811
     # without the option there is nothing to do; with it (and tokens) rows are written, so pointers count
     assert _chunk_bwd(L, cu=FAKE, n=0, B=1) == 0
     assert _chunk_bwd(L, cu=FAKE, n=0, B=1, dt=1 | ZERO, dq=None) == 1
+
+
+@pytest.mark.parametrize("io", [0, 1])
+def test_grads_f32(L, io):  # noqa: F811
+    F = binding.GDN_GRADS_F32
+    assert _chunk_bwd(L, dt=io | F, ws=None) == 4
+    assert _chunk_bwd(L, dt=io | F | ZERO, ws=None) == 4
+    assert _conv_bwd(L, dt=io | F, ws=None) == 1 and b"dtype" in L.gdn_last_error()
+    size = L.gdn_chunk_bwd_workspace_bytes
+    assert size(1, 300, 2, 4, 64, 64, 3, 1, io | F) == size(1, 300, 2, 4, 64, 64, 3, 1, io) > 0
