@@ -222,7 +222,7 @@ __global__ __launch_bounds__(NTHREADS) __attribute__((amdgpu_waves_per_eu(sizeof
       const int tl = lane < nrow ? lane : nrow - 1;
       const float graw = a.f.g ? a.f.g[(size_t)(c0 + tl) * HV + j] : (a.f.g_gamma ? a.f.g_gamma[j] : 0.f);
       const float b = a.f.beta[(size_t)(c0 + tl) * HV + j];
-      const float G = intra::wave_incl_scan(lane < nrow ? graw : 0.f, lane);
+      const float G = intra::wave_incl_scan(lane < nrow ? intra::log_gate(graw) : 0.f, lane);
       const float Gl = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, G), nrow - 1));
       sG[lane] = G;
       sG[BT + lane] = __expf(G);

@@ -21,6 +21,11 @@ __device__ __forceinline__ float wave_incl_scan(float x, int lane) {
   return x;
 }
 
+// A log-gate as it enters the sums.  Below -100 (-inf too) its exponential is 0 in fp32
+// whatever it is, but differences of sums that hold it lose what the gates behind it say:
+// 2^-24 of its size, all of it from 1e7 on.  A NaN stays one.
+__device__ __forceinline__ float log_gate(float g) { return g < -100.f ? -100.f : g; }
+
 // Work-group -> (chunk slot, v-head).  Work-group ids are dealt round-robin
 // to the 8 XCDs, each with its own L2.  The order below puts the HV heads of
 // a chunk slot on one XCD, next to each other in time, so that per-token

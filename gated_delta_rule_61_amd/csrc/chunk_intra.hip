@@ -80,7 +80,7 @@ __global__ __launch_bounds__(64) __attribute__((amdgpu_waves_per_eu(3))) void gd
   const float g_raw = g ? g[(size_t)(c0 + tl) * HV + j] : (gamma ? gamma[j] : 0.f);
   const float b_raw = beta[(size_t)(c0 + tl) * HV + j];
   if (DK / 32 > 1) load_slab(1, kf[1], qf[1]);
-  const float gl = lane < nrow ? g_raw : 0.f;
+  const float gl = lane < nrow ? log_gate(g_raw) : 0.f;
   const float G = wave_incl_scan(gl, lane);
   const float bl = lane < nrow ? b_raw : 0.f;
   // per-token gate factors for the scan: e^G, e^{G_last - G}, beta, e^{G_last}

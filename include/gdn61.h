@@ -108,7 +108,8 @@ size_t kda_chunk_fwd_workspace_bytes(int B, int T, int Hk, int HV, int K, int V,
  *   v           [B, T, HV, V]   io dtype
  *   g           [B, T, HV]      fp32 per-token natural-log gate (the chunk-
  *                               local cumulative sum is taken inside), or
- *                               NULL
+ *                               NULL; below -100 (-inf too) the state is
+ *                               wiped out (a decay that fp32 takes as 0)
  *   g_gamma     [HV]            fp32 fixed per-head natural-log decay applied
  *                               at every token, or NULL ("fla ops/common/
  *                               chunk_h.py", USE_G_GAMMA: the chunk-local
