@@ -20,7 +20,10 @@
 // Every array that holds a gradient is kept times a power of two, one for each
 // (sequence, key head), that brings the largest of its dO and dht to 2 .. 4: with
 // bf16 io the operands of the products are fp16 (2^-11 where bf16 has 2^-8), and
-// the gradients of a mean over many tokens lie far below fp16's normal numbers.
+// the gradients of a mean over many tokens lie far below fp16's normal numbers.  Rows
+// that enter a product times their tokens' gate factor are rounded three times: the row,
+// the factor, their product.  (The prefill carries its state's operands as pairs of fp16;
+// here they are single ones, and the state that is differentiated around is that.)
 #pragma once
 
 #include "gdn_device.h"

@@ -21,9 +21,11 @@
 // to the next launch; eight ragged sequences of 16001 tokens in all, 32 heads: 370 - 410 us,
 // 1.44 GB.  With loads by the state waves themselves the first took 260 us, with stores in
 // rows of the arrays instead of the order in which waves hold them the second 405.
-// fp32: the chunks' products one after the other on the few CUs that a small problem fills
-// (1000 tokens x 2, 4 heads of 64: 65 us, 4 us a chunk; the state gradients' five products
-// are 288 instructions of 32 cycles on each SIMD).
+// Where sequences x heads are few, the chunks one after the other on the few CUs that
+// these fill: one sequence of 16384 tokens, 16 heads of 128, bf16: 600 us, 2.3 a chunk,
+// on 64 of them.  fp32 likewise, at its products' rate: 2 x 1000 tokens, 4 heads of 64:
+// 65 us, 4 us a chunk (the state gradients' five products are 288 instructions of 32
+// cycles on each SIMD); the first size in fp32 917 us.
 //
 // h and dh' leave as [V][K], Vn and dR transposed ([V][64]): what a lane's
 // accumulators hold in order, a wave's stores 1 KiB in a row.
@@ -37,7 +39,7 @@ namespace {
 
 using namespace bwd;
 
-// chunk slot's offset of the sequence, its bounds; false when it has no chunks
+// the sequence's bounds, clamped to the tokens
 __device__ __forceinline__ void seq_bounds(const ChunkArgs& a, int ns, int& bos, int& eos) {
   if (a.cu_seqlens) {
     long long b0 = a.cu_seqlens[ns], b1 = a.cu_seqlens[ns + 1];
