@@ -23,7 +23,9 @@ __device__ __forceinline__ float wave_incl_scan(float x, int lane) {
 
 // A log-gate as it enters the sums.  Below -100 (-inf too) its exponential is 0 in fp32
 // whatever it is, but differences of sums that hold it lose what the gates behind it say:
-// 2^-24 of its size, all of it from 1e7 on.  A NaN stays one.
+// 2^-24 of its size, all of it from 1e7 on.  (Gates above 0 would have to grow a state by
+// e^80 within the chunk for the difference to show, which fp32 hardly holds.)  A NaN stays
+// one.
 __device__ __forceinline__ float log_gate(float g) { return g < -100.f ? -100.f : g; }
 
 // Work-group -> (chunk slot, v-head).  Work-group ids are dealt round-robin

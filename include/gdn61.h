@@ -213,25 +213,27 @@ int gdn_chunk_fwd_noalloc(const void* q, const void* k, const void* v,
  *                aligned (varlen: whether cu_seqlens is given).  Calls that share
  *                one (captured graphs too) must not run at the same time.
  *
- * Every gradient is of the io dtype but for that.  With bf16 io the operands of the products
- * (states, gradients of states and of the new values, scores) are fp16 with fp32
- * sums, which limits all of them alike (2^-14 .. 65504, fewer bits below); the
- * gradients among them are kept times a power of two, one for each (sequence, key
- * head), that brings the largest |dout| and |dht| of its v-heads to 2 .. 4, so
- * gradients of any size keep their precision, and one 2^-16 of that largest still
- * has a bf16's.  A value past 65504
- * times that scale becomes an infinity; where dout or dht hold an infinity or NaN,
- * all gradients of that sequence and key head are NaN; one in v, a gate, beta or an
- * initial state can reach the other v-heads of its key head, in its sequence.
- * |scale| is 0 or within fp16's normal numbers (2^-14 .. 65504).  fp32 io: fp32
- * throughout.  With either, a v-head's dg comes from sums that grow from one v-head
- * of its key head to the next, and is good to some fp32 steps of their largest.  The
- * same bits in every run.  Supported sizes and errors as in
- * gdn_chunk_fwd; also GDN_ERR_UNSUPPORTED where HV * V reaches 2^23, or a launch
- * would hold 2^32 threads.  T = 0 (or all sequences empty) is valid: dh0 = dht (or
- * zeros) is written.  Rows behind the last boundary are left as they are, or with
- * dtype | GDN_ROWS_ZERO become zeros, as what takes gradients of all rows needs
- * (the products with them that make a projection's).
+ * Every gradient is of the io dtype but for that.  With bf16 io the operands of
+ * the products (states, gradients of states and of the new values, scores) are
+ * fp16 with fp32 sums, which limits all of them alike (2^-14 .. 65504, fewer bits
+ * below); the gradients among them are kept times a power of two, one for each
+ * (sequence, key head), that brings the largest |dout| and |dht| of its v-heads to
+ * 2 .. 4, so gradients of any size keep their precision, and one 2^-16 of that
+ * largest still has a bf16's.  A value past 65504 times that scale becomes an
+ * infinity; where dout or dht hold an infinity or NaN, all gradients of that
+ * sequence and key head are NaN; one in v, a gate, beta or an initial state can
+ * reach the other v-heads of its key head, in its sequence (a gate of -inf is a
+ * number like others, see gdn_chunk_fwd).  |scale| is 0 or within fp16's normal
+ * numbers (2^-14 .. 65504).  fp32 io: fp32 throughout.  With either, a v-head's dg
+ * comes from sums that grow from one v-head of its key head to the next, and is
+ * good to some fp32 steps of their largest.  The same bits in every run.
+ *
+ * Supported sizes and errors as in gdn_chunk_fwd; also GDN_ERR_UNSUPPORTED where
+ * HV * V reaches 2^23, or a launch would hold 2^32 threads.  T = 0 (or all
+ * sequences empty) is valid: dh0 = dht (or zeros) is written.  Rows behind the
+ * last boundary are left as they are, or with dtype | GDN_ROWS_ZERO become zeros,
+ * as what takes gradients of all rows needs (the products with them that make a
+ * projection's).
  */
 enum { GDN_ROWS_ZERO = 0x100, GDN_GRADS_F32 = 0x200 };
 size_t gdn_chunk_bwd_workspace_bytes(int B, int T, int Hk, int HV, int K, int V, int num_seqs, int varlen,
