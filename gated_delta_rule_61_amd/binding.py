@@ -838,7 +838,8 @@ def group_norm_bwd(dout: torch.Tensor, x: torch.Tensor, num_groups: int, weight:
     given there.  Returns (dx [B,T,C], dz [B,T,C], dweight, dbias), the last
     three None where z, weight or bias is; those of weight and bias in their
     dtype, as sums over all tokens: rows of padding must hold finite values, and
-    zeros in ``dout``, to add nothing.  A ``workspace`` (else allocated) serves one call at a time."""
+    zeros in ``dout``, to add nothing.  A ``workspace`` (else allocated) serves one
+    call at a time."""
     xr, tail, dims, dev = _norm_args(x, num_groups, weight, bias, z, activation)
     B, T, G, d, _ = dims
     dx = x.new_empty(x.shape)
